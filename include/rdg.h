@@ -14,6 +14,14 @@
  *                    the down GEMM's per-row-tile completion signals;
  *                    rdg_combine_finish: the rest once the GEMM is done)
  *
+ * and the attention half of the same serving step, over a paged 8-bit cache:
+ *
+ *   rdg_kv_plan             block tables and slot maps from the requests' lengths
+ *                           (rdg_kv_trim: pages of finished or shortened requests back)
+ *   rdg_qk_norm_rope_store  norm of each query and key head, position rotation,
+ *                           keys and values into the cache
+ *   rdg_paged_attention     attention over the cache, prefill and decode
+ *
  * Page names used in the citations below:
  *   [LEP]  "Large-scale EP: DeepEP, EPLB and two-batch overlap" (SGLang handbook)
  *   [SBO]  "Single Batch Overlap (SBO): Overlaping of Down GEMM with Combine Send"
@@ -29,7 +37,7 @@
  *     the default stream) and returns without waiting.  Argument errors are
  *     returned synchronously (RDG_EINVAL / RDG_EUNSUPPORTED) and then nothing
  *     is enqueued.  A failed launch returns RDG_EHIP.
- *   - Errors found on the device (capacity overflow, signal timeout) are
+ *   - Errors found on the device (capacity overflow, signal timeout, data out of range) are
  *     written to the layout's status word [code, detail], first error wins;
  *     rdg_check_status is the one call that waits for the stream.
  *   - No C++ exception crosses this boundary.
@@ -52,7 +60,8 @@ enum {
     RDG_ECAPACITY = -2,    /* rows did not fit the preallocated layout (device status) */
     RDG_ETIMEOUT = -3,     /* a polled signal never reached its threshold (device status) */
     RDG_EHIP = -4,         /* the HIP runtime refused a launch or a query */
-    RDG_EUNSUPPORTED = -5  /* a valid but unimplemented combination of sizes / types */
+    RDG_EUNSUPPORTED = -5, /* a valid but unimplemented combination of sizes / types */
+    RDG_EDATA = -6         /* lengths, positions or page ids out of range in device data (device status) */
 };
 
 /* element types.  RDG_FP8_E4M3_UE8M0: e4m3 codes whose block scales are
@@ -401,6 +410,133 @@ int rdg_quantize_fp8(const void* src, int src_dtype, int rows, int cols, int blo
  * scaled matrix instructions take.) */
 int rdg_quantize_fp8_ue8m0(const void* src, int src_dtype, int rows, int cols, int block_rows, uint8_t* q,
                            float* scales, rdg_stream_t stream);
+
+/* ---------------------------------------------------------------- paged cache
+ * The attention half of a decoder layer's serving step (not on the pages; the
+ * MoE half above is what they describe).  A cache holds pages of page_rows
+ * tokens; a request's block table lists its pages in order.
+ *
+ * A cache in e4m3 codes, with one power-of-two scale (RDG_FP8_E4M3_UE8M0's) for
+ * each page and head: value = code * scale.
+ *   n_pages    pages; n_pages * page_rows < 2^31
+ *   page_rows  tokens per page: 16, 32, 64 or 128
+ *   n_kv       key/value heads
+ *   head_dim   64, 128 or 256 (others: RDG_EUNSUPPORTED)
+ *   k, v              [n_pages, n_kv, page_rows, head_dim] codes
+ *   k_scale, v_scale  [n_pages, n_kv] fp32 powers of two (only the exponent is used)
+ * Nothing needs clearing: rows that no call has stored are never read as values. */
+typedef struct rdg_kv_cache {
+    int32_t n_pages, page_rows, n_kv, head_dim;
+    uint8_t* k;
+    uint8_t* v;
+    float* k_scale;
+    float* v_scale;
+} rdg_kv_cache;
+
+/* One step's batch of requests, filled by the caller with sizes and buffers.
+ *   n_req       requests (0..4096 for rdg_kv_plan / rdg_kv_trim)
+ *   max_blocks  pages a request may hold; max_blocks * page_rows <= 2^30
+ *   t_cap       new tokens the buffers hold (at most 2^30)
+ *   seg_cap     at least rdg_kv_seg_cap(t_cap, n_req, page_rows)
+ *   block_table [n_req, max_blocks] in/out: page ids of each request, kept across steps
+ *   cu_q        [n_req+1] out: first new token of each request
+ *   kv_len      [n_req] out: cached tokens once the new ones are stored
+ *   slots       [t_cap] out: page * page_rows + row of each new token, or -1
+ *   positions   [t_cap] out: each new token's position in its request (0 past the last)
+ *   seg_tok     [seg_cap] out: the first new token in each page touched, then -1
+ *   status      [2] {code, detail}: set by rdg_kv_plan and rdg_kv_trim; the
+ *               other calls only add an error (first error wins)
+ *   work        rdg_kv_step_work_bytes() bytes, zeroed once by the caller
+ * A caller with a planner of its own fills these buffers itself (in seg_tok,
+ * each token whose slot does not follow its predecessor's inside one page). */
+typedef struct rdg_kv_step {
+    int32_t n_req, max_blocks, page_rows, n_pages, t_cap, seg_cap;
+    int32_t* block_table;
+    int32_t* cu_q;
+    int32_t* kv_len;
+    int32_t* slots;
+    int32_t* positions;
+    int32_t* seg_tok;
+    int32_t* status;
+    int32_t* work;
+} rdg_kv_step;
+
+size_t rdg_kv_step_work_bytes(void);
+int rdg_kv_seg_cap(int t_cap, int n_req, int page_rows);
+
+/* Plan a step: a page for every page_rows tokens that each request will hold,
+ * from a stack of free pages, and the place of every new token.
+ *   kv_len      [n_req] tokens already in the cache (may be S->kv_len)
+ *   q_len       [n_req] new tokens (0: an idle row)
+ *   free_list   ids of the free pages, the first *n_free of it; *n_free <= n_pages
+ *   n_free_out  [1] what is left (may be n_free)
+ * Requests are served in order: request r's i-th new page is
+ * free_list[*n_free - 1 - (new pages of the requests before it) - i].  One that does not
+ * fit -- too few free pages, more than max_blocks pages, tokens past t_cap --
+ * gets none, nor does a later one that needs a page: its tokens' slots are -1, its
+ * kv_len stays, and status is RDG_ECAPACITY with the first such request as detail.  Negative lengths and page ids
+ * outside the cache give RDG_EDATA, with the request.  Deterministic; nothing
+ * waits for the host, so a step can be captured with the kernels that read it. */
+int rdg_kv_plan(const rdg_kv_step* S, const int32_t* kv_len, const int32_t* q_len, const int32_t* free_list,
+                const int32_t* n_free, int32_t* n_free_out, rdg_stream_t stream);
+
+/* Shorten requests (0: a finished request; less: drafted tokens that were not
+ * accepted) and hand back the pages behind their new lengths.
+ *   kv_len    [n_req] cached tokens (may be S->kv_len)
+ *   new_len   [n_req] tokens to keep, at most kv_len; a request with a length out
+ *             of range is left as it is, with status RDG_EDATA
+ *   free_list [n_pages] the freed pages are added behind the first *n_free, in request
+ *             and block order; their table entries become -1
+ * S->kv_len becomes new_len.  More pages than the list can hold: no request is
+ * changed and status is RDG_ECAPACITY, with their number. */
+int rdg_kv_trim(const rdg_kv_step* S, const int32_t* kv_len, const int32_t* new_len, int32_t* free_list,
+                const int32_t* n_free, int32_t* n_free_out, rdg_stream_t stream);
+
+/* Norm of each query and key head, position rotation, and the store of keys
+ * and values, in one pass over the projections.
+ *   qkv       [T, qkv_stride]: each token's n_q query heads, n_kv key heads and n_kv
+ *             value heads of head_dim elements (RDG_F32 or RDG_BF16); T <= S->t_cap
+ *   q_weight, k_weight  [head_dim] fp32 gains of x / sqrt(mean(x^2) + eps), or NULL for
+ *             no norm
+ *   cos_sin   [n_pos, rot_dim] fp32: rot_dim/2 cosines, then as many sines, of each
+ *             position (S->positions); a position outside is cut to the table, with
+ *             status RDG_EDATA and the token
+ *   rot_dim   elements rotated at the front of each head: a multiple of 16, 0 for none
+ *   neighbours  0: element i turns with i + rot_dim/2; else 2i with 2i + 1
+ *   q_out     [T, q_stride] queries (n_q heads) in dtype
+ *   C         the cache (NULL with n_kv = 0: queries only)
+ * Strides are in elements, multiples of 16 bytes.  Everything is fp32 up to the
+ * one rounding of q and of the codes.  A page and head's scale is the smallest 2^k that
+ * holds the new rows' largest finite magnitude (2^k * 448 >= it, k in [-126, 127]; -126 for zeros);
+ * a page that already holds rows before the new ones keeps the larger of that
+ * and its own, and its older codes are rounded to a grown scale.  Infinities are stored as
+ * +-448 * scale, NaN as NaN (0x7f).  Tokens with slot -1 are not stored. */
+int rdg_qk_norm_rope_store(const void* qkv, int dtype, int64_t qkv_stride, int T, int n_q, int n_kv, int head_dim,
+                           const float* q_weight, const float* k_weight, float eps, const float* cos_sin, int n_pos,
+                           int rot_dim, int neighbours, const rdg_kv_step* S, const rdg_kv_cache* C, void* q_out,
+                           int64_t q_stride, rdg_stream_t stream);
+
+/* Attention over the cache.  For query i of the n new tokens of a request
+ * (tokens cu_q[r] .. cu_q[r+1]) whose cache holds kv tokens with them, at position
+ * kv - n + i:
+ *   out[i] = sum_j p_j v_j,  p = softmax_j(scale * q_i . k_j),  lse[i] = log sum_j exp(scale * q_i . k_j)
+ * over keys j <= position and, with a window, j > position - window; over all kv
+ * keys with causal = 0 (window then 0).  A query that sees no key gives 0 and -inf.
+ *   q, out   [T, q_stride] / [T, out_stride], n_q heads of head_dim (RDG_F32 or
+ *            RDG_BF16); query head h reads key head h / (n_q / n_kv)
+ *   max_q, max_kv  host bounds of the requests' new and cached tokens: grids
+ *            and workspace are sized by them.  A request past max_kv is cut to it (RDG_EDATA);
+ *            rows past max_q are not computed
+ *   lse      [T, n_q] fp32 or NULL
+ *   work     rdg_paged_attention_workspace_bytes(...) bytes (NULL when that is 0)
+ * Softmax, sums and products are fp32; with RDG_BF16 the probabilities are
+ * rounded to bf16 for the product with v.  Deterministic.  A NaN in a row
+ * that a query does not see does not reach it. */
+size_t rdg_paged_attention_workspace_bytes(const rdg_kv_cache* C, int T, int n_req, int n_q, int max_q, int max_kv,
+                                           int dtype);
+int rdg_paged_attention(const void* q, int dtype, int64_t q_stride, int T, int n_q, const rdg_kv_step* S,
+                        const rdg_kv_cache* C, int max_q, int max_kv, float scale, int causal, int window, void* out,
+                        int64_t out_stride, float* lse, void* work, size_t work_bytes, rdg_stream_t stream);
 
 /* Fill n int32 words with value (a kernel, so it is safe inside captured graphs). */
 int rdg_fill_i32(int32_t* p, int32_t value, int64_t n, rdg_stream_t stream);

@@ -11,7 +11,7 @@ import os
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "librdg.so")
 
-RDG_OK, RDG_EINVAL, RDG_ECAPACITY, RDG_ETIMEOUT, RDG_EHIP, RDG_EUNSUPPORTED = 0, -1, -2, -3, -4, -5
+RDG_OK, RDG_EINVAL, RDG_ECAPACITY, RDG_ETIMEOUT, RDG_EHIP, RDG_EUNSUPPORTED, RDG_EDATA = 0, -1, -2, -3, -4, -5, -6
 RDG_F32, RDG_BF16, RDG_FP8_E4M3, RDG_FP8_E4M3_UE8M0 = 0, 1, 2, 3
 RDG_CONTIGUOUS, RDG_MASKED = 0, 1
 
@@ -30,6 +30,20 @@ class rdg_layout(ctypes.Structure):
                 ("work", ctypes.c_void_p), ("expert_load", ctypes.c_void_p)]
 
 
+class rdg_kv_cache(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int32), ("page_rows", ctypes.c_int32), ("n_kv", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class rdg_kv_step(ctypes.Structure):
+    _fields_ = [("n_req", ctypes.c_int32), ("max_blocks", ctypes.c_int32), ("page_rows", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("t_cap", ctypes.c_int32), ("seg_cap", ctypes.c_int32),
+                ("block_table", ctypes.c_void_p), ("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("seg_tok", ctypes.c_void_p),
+                ("status", ctypes.c_void_p), ("work", ctypes.c_void_p)]
+
+
 if not os.path.exists(LIB_PATH):
     raise ImportError("librdg.so is not built (run routing_dispatch_grouped_amd/_build.py or "
                       "__graft_entry__.build()); there is no fallback implementation")
@@ -37,6 +51,7 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 _P, _I, _I64, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 _LP = ctypes.POINTER(rdg_layout)
+_CP, _SP = ctypes.POINTER(rdg_kv_cache), ctypes.POINTER(rdg_kv_step)
 
 _SIGS = {
     "rdg_route": ([_P, _I, _I, _I, _I, _I, _F, _P, _P, _P], _I),
@@ -63,6 +78,13 @@ _SIGS = {
     "rdg_fill_i32": ([_P, ctypes.c_int32, _I64, _P], _I),
     "rdg_packed_weight_bytes": ([_I, _I, _I, _I], _SZ),
     "rdg_pack_weights": ([_P, _I, _I, _I, _I, _P, _P], _I),
+    "rdg_kv_step_work_bytes": ([], _SZ),
+    "rdg_kv_seg_cap": ([_I, _I, _I], _I),
+    "rdg_kv_plan": ([_SP, _P, _P, _P, _P, _P, _P], _I),
+    "rdg_kv_trim": ([_SP, _P, _P, _P, _P, _P, _P], _I),
+    "rdg_qk_norm_rope_store": ([_P, _I, _I64, _I, _I, _I, _I, _P, _P, _F, _P, _I, _I, _I, _SP, _CP, _P, _I64, _P], _I),
+    "rdg_paged_attention_workspace_bytes": ([_CP, _I, _I, _I, _I, _I, _I], _SZ),
+    "rdg_paged_attention": ([_P, _I, _I64, _I, _I, _SP, _CP, _I, _I, _F, _I, _I, _P, _I64, _P, _P, _SZ, _P], _I),
     "rdg_check_status": ([_P, _P, _P], _I),
     "rdg_strerror": ([_I], ctypes.c_char_p),
     "rdg_version": ([], _I),
@@ -119,6 +141,74 @@ class Layout:
         self.m_cap = m_cap
         self.block_m = block_m
         self.m_max = m_max
+
+    @property
+    def ref(self):
+        return ctypes.byref(self.c)
+
+
+def _tensor(t, what, dtype, *shape):
+    """Refuse a tensor that the C call would read wrongly: another element type
+    or size than the call assumes, or not contiguous."""
+    if t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise RdgError(RDG_EINVAL, "%s: want a contiguous %s tensor of shape %s, got %s %s" %
+                       (what, dtype, list(shape), t.dtype, list(t.shape)))
+    return t
+
+
+class KvCache:
+    """A paged 8-bit key/value cache (rdg_kv_cache) over the caller's tensors:
+    k, v [n_pages, n_kv, page_rows, head_dim] uint8, k_scale, v_scale [n_pages, n_kv] float32."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        if k.dim() != 4:
+            raise RdgError(RDG_EINVAL, "KvCache: k has to be [n_pages, n_kv, page_rows, head_dim]")
+        n_pages, n_kv, page_rows, head_dim = k.shape
+        self.k = _tensor(k, "KvCache.k", torch.uint8, *k.shape)
+        self.v = _tensor(v, "KvCache.v", torch.uint8, *k.shape)
+        self.k_scale = _tensor(k_scale, "KvCache.k_scale", torch.float32, n_pages, n_kv)
+        self.v_scale = _tensor(v_scale, "KvCache.v_scale", torch.float32, n_pages, n_kv)
+        self.n_pages, self.n_kv, self.page_rows, self.head_dim = n_pages, n_kv, page_rows, head_dim
+        self.c = rdg_kv_cache(n_pages, page_rows, n_kv, head_dim, k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
+                              v_scale.data_ptr())
+
+    @classmethod
+    def empty(cls, n_pages, n_kv, page_rows, head_dim, device):
+        import torch
+        code = dict(dtype=torch.uint8, device=device)
+        scale = dict(dtype=torch.float32, device=device)
+        shape = (n_pages, n_kv, page_rows, head_dim)
+        return cls(torch.zeros(shape, **code), torch.zeros(shape, **code), torch.ones(shape[:2], **scale),
+                   torch.ones(shape[:2], **scale))
+
+    @property
+    def ref(self):
+        return ctypes.byref(self.c)
+
+
+class KvStep:
+    """Device buffers of an rdg_kv_step, allocated with torch on ``device``."""
+
+    def __init__(self, n_req, max_blocks, page_rows, n_pages, t_cap, device):
+        import torch
+        self.n_req, self.max_blocks, self.page_rows = n_req, max_blocks, page_rows
+        self.n_pages, self.t_cap = n_pages, t_cap
+        seg_cap = _lib.rdg_kv_seg_cap(t_cap, n_req, page_rows)
+        _check(min(seg_cap, 0), "KvStep")
+        i32 = dict(dtype=torch.int32, device=device)
+        self.block_table = torch.full((n_req, max_blocks), -1, **i32)
+        self.cu_q = torch.zeros(n_req + 1, **i32)
+        self.kv_len = torch.zeros(n_req, **i32)
+        self.slots = torch.full((t_cap,), -1, **i32)
+        self.positions = torch.zeros(t_cap, **i32)
+        self.seg_tok = torch.full((seg_cap,), -1, **i32)
+        self.status = torch.zeros(2, **i32)
+        self.work = torch.zeros(_lib.rdg_kv_step_work_bytes(), dtype=torch.uint8, device=device)
+        self.c = rdg_kv_step(n_req, max_blocks, page_rows, n_pages, t_cap, seg_cap, self.block_table.data_ptr(),
+                             self.cu_q.data_ptr(), self.kv_len.data_ptr(), self.slots.data_ptr(),
+                             self.positions.data_ptr(), self.seg_tok.data_ptr(), self.status.data_ptr(),
+                             self.work.data_ptr())
 
     @property
     def ref(self):
@@ -289,11 +379,97 @@ def rdg_fill_i32(p, value, stream=None):
     _check(_lib.rdg_fill_i32(_ptr(p), value, p.numel(), _stream(stream)), "rdg_fill_i32")
 
 
+def rdg_kv_plan(step, kv_len, q_len, free_list, n_free, n_free_out, stream=None):
+    """kv_len, q_len [n_req], free_list [>= n_free], n_free, n_free_out [1]: int32 device tensors."""
+    import torch
+    i32, R = torch.int32, step.n_req
+    _tensor(kv_len, "rdg_kv_plan: kv_len", i32, R)
+    _tensor(q_len, "rdg_kv_plan: q_len", i32, R)
+    _tensor(free_list, "rdg_kv_plan: free_list", i32, free_list.numel())
+    _tensor(n_free, "rdg_kv_plan: n_free", i32, 1)
+    _tensor(n_free_out, "rdg_kv_plan: n_free_out", i32, 1)
+    _check(_lib.rdg_kv_plan(step.ref, _ptr(kv_len), _ptr(q_len), _ptr(free_list), _ptr(n_free), _ptr(n_free_out),
+                            _stream(stream)), "rdg_kv_plan")
+
+
+def rdg_kv_trim(step, kv_len, new_len, free_list, n_free, n_free_out, stream=None):
+    """kv_len, new_len [n_req], free_list [n_pages], n_free, n_free_out [1]: int32 device tensors."""
+    import torch
+    i32, R = torch.int32, step.n_req
+    _tensor(kv_len, "rdg_kv_trim: kv_len", i32, R)
+    _tensor(new_len, "rdg_kv_trim: new_len", i32, R)
+    _tensor(free_list, "rdg_kv_trim: free_list", i32, step.n_pages)
+    _tensor(n_free, "rdg_kv_trim: n_free", i32, 1)
+    _tensor(n_free_out, "rdg_kv_trim: n_free_out", i32, 1)
+    _check(_lib.rdg_kv_trim(step.ref, _ptr(kv_len), _ptr(new_len), _ptr(free_list), _ptr(n_free), _ptr(n_free_out),
+                            _stream(stream)), "rdg_kv_trim")
+
+
+def _rows(t, what, heads, head_dim):
+    """dtype code and token stride of [T, heads * head_dim] or [T, heads, head_dim] rows; tokens may be apart."""
+    import torch
+    inner = (head_dim, 1) if t.dim() == 3 else (1,)
+    width = (heads, head_dim) if t.dim() == 3 else (heads * head_dim,)
+    code = {torch.bfloat16: RDG_BF16, torch.float32: RDG_F32}.get(t.dtype)
+    if code is None or tuple(t.shape[1:]) != width or tuple(t.stride()[1:]) != inner:
+        raise RdgError(RDG_EINVAL, "%s: want bfloat16 or float32 rows of %s, got %s %s with strides %s" %
+                       (what, list(width), t.dtype, list(t.shape), list(t.stride())))
+    return code, t.stride(0) if t.shape[0] > 1 else heads * head_dim
+
+
+def rdg_qk_norm_rope_store(qkv, n_q, n_kv, head_dim, q_weight, k_weight, eps, cos_sin, rot_dim, neighbours, step, cache,
+                           q_out, stream=None):
+    """qkv [T, (n_q + 2 n_kv) * head_dim] (token stride free), q_out [T, n_q, head_dim], weights [head_dim] float32
+    or None, cos_sin [n_pos, rot_dim] float32 or None; cache None with n_kv = 0."""
+    import torch
+    f32, T = torch.float32, qkv.shape[0]
+    dt, stride = _rows(qkv, "rdg_qk_norm_rope_store: qkv", n_q + 2 * n_kv, head_dim)
+    q_stride = 0
+    if n_q > 0:
+        q_dt, q_stride = _rows(q_out, "rdg_qk_norm_rope_store: q_out", n_q, head_dim)
+        if q_dt != dt or q_out.shape[0] != T:
+            raise RdgError(RDG_EINVAL, "rdg_qk_norm_rope_store: q_out differs from qkv in type or tokens")
+    if q_weight is not None:
+        _tensor(q_weight, "rdg_qk_norm_rope_store: q_weight", f32, head_dim)
+    if k_weight is not None:
+        _tensor(k_weight, "rdg_qk_norm_rope_store: k_weight", f32, head_dim)
+    n_pos = 0
+    if rot_dim:
+        n_pos = cos_sin.shape[0]
+        _tensor(cos_sin, "rdg_qk_norm_rope_store: cos_sin", f32, n_pos, rot_dim)
+    _check(_lib.rdg_qk_norm_rope_store(_ptr(qkv), dt, stride, T, n_q, n_kv, head_dim, _ptr(q_weight), _ptr(k_weight),
+                                       eps, _ptr(cos_sin), n_pos, rot_dim, int(bool(neighbours)), step.ref,
+                                       None if cache is None else cache.ref, _ptr(q_out), q_stride, _stream(stream)),
+           "rdg_qk_norm_rope_store")
+
+
+def rdg_paged_attention_workspace_bytes(cache, T, n_req, n_q, max_q, max_kv, dtype):
+    return int(_lib.rdg_paged_attention_workspace_bytes(cache.ref, T, n_req, n_q, max_q, max_kv, dtype))
+
+
+def rdg_paged_attention(q, step, cache, max_q, max_kv, scale, out, lse=None, work=None, causal=True, window=0,
+                        stream=None):
+    """q, out [T, n_q, head_dim] (token strides free), lse [T, n_q] float32 or None; work: a uint8 tensor of
+    rdg_paged_attention_workspace_bytes."""
+    import torch
+    T, n_q = q.shape[:2]
+    dt, q_stride = _rows(q, "rdg_paged_attention: q", n_q, cache.head_dim)
+    out_dt, out_stride = _rows(out, "rdg_paged_attention: out", n_q, cache.head_dim)
+    if out_dt != dt or out.shape[0] != T:
+        raise RdgError(RDG_EINVAL, "rdg_paged_attention: out differs from q in type or tokens")
+    if lse is not None:
+        _tensor(lse, "rdg_paged_attention: lse", torch.float32, T, n_q)
+    _check(_lib.rdg_paged_attention(_ptr(q), dt, q_stride, T, n_q, step.ref, cache.ref, max_q, max_kv, scale,
+                                    int(bool(causal)), window, _ptr(out), out_stride, _ptr(lse), _ptr(work),
+                                    0 if work is None else work.numel() * work.element_size(), _stream(stream)),
+           "rdg_paged_attention")
+
+
 def rdg_check_status(layout_or_status, stream=None):
     """Waits for the stream; returns (code, detail)."""
-    st = layout_or_status.status if isinstance(layout_or_status, Layout) else layout_or_status
+    st = layout_or_status.status if isinstance(layout_or_status, (Layout, KvStep)) else layout_or_status
     host = (ctypes.c_int32 * 2)()
     rc = _lib.rdg_check_status(_ptr(st), host, _stream(stream))
-    if rc in (RDG_EINVAL, RDG_EHIP):  # the query itself failed (device codes are -2 / -3)
+    if rc in (RDG_EINVAL, RDG_EHIP):  # the query itself failed (device codes are -2, -3 and -6)
         raise RdgError(rc, "rdg_check_status")
     return int(host[0]), int(host[1])

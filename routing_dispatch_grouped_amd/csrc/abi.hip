@@ -73,7 +73,7 @@ uint64_t wall_ticks_per_us() {
 
 extern "C" {
 
-int rdg_version(void) { return 100; }
+int rdg_version(void) { return 200; }
 
 const char* rdg_strerror(int code) {
     switch (code) {
@@ -83,6 +83,7 @@ const char* rdg_strerror(int code) {
         case RDG_ETIMEOUT: return "a completion signal did not reach its threshold in time";
         case RDG_EHIP: return "HIP runtime error";
         case RDG_EUNSUPPORTED: return "unsupported size or type combination";
+        case RDG_EDATA: return "lengths, positions or page ids out of range in device data";
         default: return "unknown status";
     }
 }

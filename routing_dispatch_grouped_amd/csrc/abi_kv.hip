@@ -1,0 +1,196 @@
+// C ABI of the paged key/value cache (include/rdg.h): argument checks, the
+// choice of kernels, then enqueue.
+#include <math.h>
+
+#include "rdg_internal.h"
+
+using namespace rdg;
+
+namespace {
+
+inline int hip_rc(hipError_t e) { return e == hipSuccess ? RDG_OK : RDG_EHIP; }
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool page_rows_ok(int p) { return p == 16 || p == 32 || p == 64 || p == 128; }
+
+int page_shift_of(int p) { return p == 16 ? 4 : p == 32 ? 5 : p == 64 ? 6 : 7; }
+
+// The fields of a step that every call reads.
+bool step_ok(const rdg_kv_step* S) {
+    if (S == nullptr) return false;
+    if (S->n_req < 0 || S->max_blocks < 1 || S->n_pages < 1 || S->t_cap < 0 || S->seg_cap < 0) return false;
+    if (!page_rows_ok(S->page_rows)) return false;
+    if ((int64_t)S->n_pages * S->page_rows >= (int64_t)1 << 31) return false;
+    if ((int64_t)S->max_blocks * S->page_rows > (int64_t)1 << 30 || S->t_cap > 1 << 30) return false;
+    return S->status != nullptr;
+}
+
+int cache_rc(const rdg_kv_cache* C) {
+    if (C == nullptr || C->n_pages < 1 || C->n_kv < 1 || !page_rows_ok(C->page_rows)) return RDG_EINVAL;
+    if ((int64_t)C->n_pages * C->page_rows >= (int64_t)1 << 31) return RDG_EINVAL;
+    if (C->head_dim != 64 && C->head_dim != 128 && C->head_dim != 256) return RDG_EUNSUPPORTED;
+    return RDG_OK;
+}
+
+int cache_buffers_rc(const rdg_kv_cache* C) {
+    if (!C->k || !C->v || !C->k_scale || !C->v_scale || !aligned16(C->k) || !aligned16(C->v)) return RDG_EINVAL;
+    return RDG_OK;
+}
+
+constexpr int kChunkMin = 256, kChunkMax = 4096;  // keys; a workgroup's lanes hold the pages of 4096
+constexpr int kUnits = 1024;                      // workgroups wanted: four per CU
+
+// How k_attn_rows splits its work.
+struct RowsPlan {
+    int nr, row_tiles, chunk, max_chunks;
+};
+
+RowsPlan plan_rows(int R, int n_kv, int group, int head_dim, bool bf16, int n_most, int span) {
+    RowsPlan p;
+    const int64_t rows = (int64_t)n_most * group;
+    p.nr = !bf16 || rows <= 16 ? 1 : rows <= 32 || head_dim == 256 ? 2 : 4;
+    p.row_tiles = (int)((rows + 16 * p.nr - 1) / (16 * p.nr));
+    const double units = (double)R * n_kv * p.row_tiles;
+    double want = ceil(span * units / kUnits / kChunkMin) * kChunkMin;
+    if (want < kChunkMin) want = kChunkMin;
+    p.chunk = want > kChunkMax ? kChunkMax : (int)want;
+    p.max_chunks = (int)(((int64_t)span + 63 + p.chunk - 1) / p.chunk);
+    if (p.max_chunks < 1) p.max_chunks = 1;
+    return p;
+}
+
+// Bytes of one part (fp32 row, maximum and sum) of every row.
+size_t part_bytes(int T, int n_q, int head_dim) { return sizeof(float) * (size_t)T * n_q * (head_dim + 2); }
+
+// The longest run of keys that one request's queries see together.
+int key_span(int max_q, int max_kv, int window) {
+    const int64_t w = window > 0 ? (int64_t)window + max_q : max_kv;
+    return w < max_kv ? (int)w : max_kv;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t rdg_kv_step_work_bytes(void) { return 16; }
+
+int rdg_kv_seg_cap(int t_cap, int n_req, int page_rows) {
+    if (t_cap < 0 || n_req < 0 || !page_rows_ok(page_rows)) return RDG_EINVAL;
+    const int64_t n = t_cap / page_rows + 2 * (int64_t)n_req;
+    return n < t_cap ? (int)n : t_cap;
+}
+
+int rdg_kv_plan(const rdg_kv_step* S, const int32_t* kv_len, const int32_t* q_len, const int32_t* free_list,
+                const int32_t* n_free, int32_t* n_free_out, rdg_stream_t stream) {
+    if (!step_ok(S) || !S->work || !n_free || !n_free_out || !S->cu_q) return RDG_EINVAL;
+    if (S->n_req > 0 && (!kv_len || !q_len || !free_list || !S->block_table || !S->kv_len)) return RDG_EINVAL;
+    if (S->t_cap > 0 && (!S->slots || !S->positions || !aligned16(S->slots) || !aligned16(S->positions)))
+        return RDG_EINVAL;
+    if (S->seg_cap < rdg_kv_seg_cap(S->t_cap, S->n_req, S->page_rows) || (S->seg_cap > 0 && !S->seg_tok))
+        return RDG_EINVAL;
+    if (S->n_req > kMaxRequests) return RDG_EUNSUPPORTED;
+    return hip_rc(launch_kv_plan(*S, kv_len, q_len, free_list, n_free, n_free_out, stream));
+}
+
+int rdg_kv_trim(const rdg_kv_step* S, const int32_t* kv_len, const int32_t* new_len, int32_t* free_list,
+                const int32_t* n_free, int32_t* n_free_out, rdg_stream_t stream) {
+    if (!step_ok(S) || !S->work || !n_free || !n_free_out) return RDG_EINVAL;
+    if (S->n_req > 0 && (!kv_len || !new_len || !free_list || !S->block_table || !S->kv_len)) return RDG_EINVAL;
+    if (S->n_req > kMaxRequests) return RDG_EUNSUPPORTED;
+    return hip_rc(launch_kv_trim(*S, new_len, kv_len, free_list, n_free, n_free_out, stream));
+}
+
+int rdg_qk_norm_rope_store(const void* qkv, int dtype, int64_t qkv_stride, int T, int n_q, int n_kv, int head_dim,
+                           const float* q_weight, const float* k_weight, float eps, const float* cos_sin, int n_pos,
+                           int rot_dim, int neighbours, const rdg_kv_step* S, const rdg_kv_cache* C, void* q_out,
+                           int64_t q_stride, rdg_stream_t stream) {
+    if (dtype != RDG_F32 && dtype != RDG_BF16) return RDG_EINVAL;
+    if (T < 0 || n_q < 0 || n_kv < 0 || n_q > 4096 || n_kv > 4096 || !(eps >= 0.0f) || !step_ok(S)) return RDG_EINVAL;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return RDG_EUNSUPPORTED;
+    if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 16 != 0) return RDG_EINVAL;
+    const int vec = dtype == RDG_BF16 ? 8 : 4;
+    if (T > 0) {
+        if (T > S->t_cap || !qkv || !aligned16(qkv) || qkv_stride < (int64_t)(n_q + 2 * n_kv) * head_dim ||
+            qkv_stride % vec != 0)
+            return RDG_EINVAL;
+        if (rot_dim > 0 && (!cos_sin || !aligned16(cos_sin) || n_pos < 1 || !S->positions)) return RDG_EINVAL;
+        if (n_q > 0 && (!q_out || !aligned16(q_out) || q_stride < (int64_t)n_q * head_dim || q_stride % vec != 0))
+            return RDG_EINVAL;
+        if ((q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight))) return RDG_EINVAL;
+    }
+    QkStoreCall a = {};
+    if (n_kv > 0) {
+        const int rc = cache_rc(C);
+        if (rc != RDG_OK) return rc;
+        if (C->n_kv != n_kv || C->head_dim != head_dim || C->page_rows != S->page_rows || C->n_pages != S->n_pages)
+            return RDG_EINVAL;
+        if (T > 0 && (cache_buffers_rc(C) != RDG_OK || !S->slots || !S->seg_tok)) return RDG_EINVAL;
+        a.k_codes = C->k, a.v_codes = C->v, a.k_scale = C->k_scale, a.v_scale = C->v_scale;
+    }
+    a.qkv = qkv, a.q_out = q_out, a.q_weight = q_weight, a.k_weight = k_weight, a.cos_sin = cos_sin;
+    a.positions = S->positions, a.slots = S->slots, a.seg_tok = S->seg_tok, a.status = S->status;
+    a.row_stride = qkv_stride, a.q_stride = q_stride, a.eps = eps;
+    a.T = T, a.n_q = n_q, a.n_kv = n_kv, a.rot_dim = rot_dim, a.n_pos = n_pos, a.n_pages = S->n_pages;
+    a.page_rows = S->page_rows, a.neighbours = neighbours != 0;
+    return hip_rc(launch_qk_store(a, head_dim, dtype == RDG_BF16, n_kv > 0 ? S->seg_cap : 0, stream));
+}
+
+size_t rdg_paged_attention_workspace_bytes(const rdg_kv_cache* C, int T, int n_req, int n_q, int max_q, int max_kv,
+                                           int dtype) {
+    if (cache_rc(C) != RDG_OK || T <= 0 || n_req <= 0 || n_q < C->n_kv || n_q % C->n_kv != 0 || max_q <= 0 ||
+        max_kv <= 0)
+        return 0;
+    if (max_q > T) max_q = T;
+    const RowsPlan p = plan_rows(n_req, C->n_kv, n_q / C->n_kv, C->head_dim, dtype == RDG_BF16, max_q, max_kv);
+    return p.max_chunks > 1 ? align256(part_bytes(T, n_q, C->head_dim) * p.max_chunks) : 0;
+}
+
+int rdg_paged_attention(const void* q, int dtype, int64_t q_stride, int T, int n_q, const rdg_kv_step* S,
+                        const rdg_kv_cache* C, int max_q, int max_kv, float scale, int causal, int window, void* out,
+                        int64_t out_stride, float* lse, void* work, size_t work_bytes, rdg_stream_t stream) {
+    if (dtype != RDG_F32 && dtype != RDG_BF16) return RDG_EINVAL;
+    if (!step_ok(S) || T < 0 || n_q < 1 || max_q < 0 || max_kv < 0 || window < 0) return RDG_EINVAL;
+    if (window > 0 && !causal) return RDG_EINVAL;
+    if (!(scale > 0.0f) || !(scale < INFINITY)) return RDG_EINVAL;
+    int rc = cache_rc(C);
+    if (rc != RDG_OK) return rc;
+    if (n_q % C->n_kv != 0 || n_q > 4096 || C->page_rows != S->page_rows || C->n_pages != S->n_pages) return RDG_EINVAL;
+    if (T == 0 || S->n_req == 0 || max_q == 0) return RDG_OK;
+    if (max_q > T) max_q = T;
+    const int D = C->head_dim, vec = dtype == RDG_BF16 ? 8 : 4;
+    if (!q || !out || !aligned16(q) || !aligned16(out) || cache_buffers_rc(C) != RDG_OK) return RDG_EINVAL;
+    if (q_stride < (int64_t)n_q * D || q_stride % vec != 0 || out_stride < (int64_t)n_q * D || out_stride % vec != 0)
+        return RDG_EINVAL;
+    if (!S->block_table || !S->cu_q || !S->kv_len) return RDG_EINVAL;
+    AttnCall a = {};
+    a.q = q, a.out = out, a.lse = lse, a.block_table = S->block_table, a.cu_q = S->cu_q, a.kv_len = S->kv_len;
+    a.k_codes = C->k, a.v_codes = C->v, a.k_scale = C->k_scale, a.v_scale = C->v_scale, a.status = S->status;
+    a.q_stride = q_stride, a.out_stride = out_stride, a.scale_log2 = scale * 1.4426950408889634f;
+    a.T = T, a.R = S->n_req, a.n_q = n_q, a.n_kv = C->n_kv, a.group = n_q / C->n_kv;
+    a.max_blocks = S->max_blocks, a.n_pages = C->n_pages, a.page_shift = page_shift_of(C->page_rows);
+    const int64_t table = (int64_t)S->max_blocks * C->page_rows;
+    a.kv_cap = table < max_kv ? (int)table : max_kv;
+    a.window = window, a.causal = causal != 0;
+    const bool bf16 = dtype == RDG_BF16;
+    // The workspace is sized for all max_kv keys.  A window leaves a shorter run,
+    // which may be cut finer than the workspace holds parts for: then coarser.
+    const int span = key_span(max_q, max_kv, window);
+    RowsPlan p = plan_rows(a.R, a.n_kv, a.group, D, bf16, max_q, span);
+    const size_t part = part_bytes(T, n_q, D);
+    const size_t need = rdg_paged_attention_workspace_bytes(C, T, a.R, n_q, max_q, max_kv, dtype);
+    if (need > 0 && (!work || !aligned16(work) || work_bytes < need)) return RDG_EINVAL;
+    const int64_t room = need > 0 ? (int64_t)(need / part) : 1;
+    if (p.max_chunks > room) {
+        p.chunk = (int)((((int64_t)span + 63 + room - 1) / room + kChunkMin - 1) / kChunkMin * kChunkMin);
+        p.max_chunks = (int)room;
+    }
+    a.n_most = max_q, a.row_tiles = p.row_tiles, a.chunk = p.chunk, a.max_chunks = p.max_chunks;
+    if (p.max_chunks > 1) {
+        a.part_o = static_cast<float*>(work);
+        a.part_ml = a.part_o + (size_t)T * n_q * D * p.max_chunks;
+    }
+    return hip_rc(launch_attn_rows(a, D, bf16, p.nr, stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,425 @@
+// Attention over the 8-bit paged cache, few query rows per request: decode,
+// drafted tokens, fp32 queries.
+//
+//   o_i = sum_j softmax_j(scale * q_i . k_j) v_j     lse_i = log sum_j exp(scale * q_i . k_j)
+//
+// over the keys that query i sees, in one pass with a running maximum and sum
+// (fp32, base-2 exponents).  Bound by HBM: every code is read once, 2 * head_dim
+// bytes per key and key head, and the G = n_q / n_kv query heads of a key head
+// share the read: the rows of a tile are (query token, head of the group).
+//
+// Nothing goes through LDS on the way in.  A wave computes
+//   S^T = K Q^T   16 keys x 16 rows per v_mfma_f32_16x16x32_bf16
+//   O^T = V^T P^T 16 columns x 16 rows, 32 keys per MFMA
+// and takes both operands from registers as the cache holds them: the order of
+// the reduction index is free, so a lane's 16 consecutive K codes serve two
+// MFMA steps, and the keys that S^T leaves in a lane (4 of each 16) are the
+// ones that its P^T operand holds, with V's 4-byte columns transposed by byte
+// permutes to match.  The codes become bf16 exactly, times their page's power
+// of two (v_cvt_scalef32_pk_bf16_fp8).  fp32 queries and probabilities go in as
+// three bf16 parts each, which carries 24 bits.
+//
+// A workgroup's four waves take 64-key blocks in turn from one chunk of one
+// request's keys and join in LDS; chunks of one row are joined by a second
+// launch, in chunk order, so results do not depend on scheduling.  A wave's
+// next K block is in flight while its softmax and V product run, and its next
+// V block during the K product: 16 KB a wave at head_dim 128.
+#include "attn.h"
+
+namespace rdg {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kBlock = 64;  // keys per wave and step
+
+template <int D>
+struct VWords {
+    static constexpr int n = D / 64;  // dwords of V per key and lane (D / 16 codes)
+};
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+    if constexpr (N == 1) {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (N == 2) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        w[0] = u.x, w[1] = u.y;
+    } else {
+        const uint4 u = *reinterpret_cast<const uint4*>(p);
+        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    }
+}
+
+// x as NS bf16 parts that sum to it (NS = 1: x rounded).
+template <int NS>
+__device__ __forceinline__ void split_bf16(float x, __bf16 (&part)[NS]) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        part[i] = (__bf16)x;
+        if (i + 1 < NS) x -= (float)part[i];
+    }
+}
+
+// NS = 1: bf16 queries and output; 3: fp32.  NR: 16-row tiles per wave.
+template <int D, int NS, int NR>
+__global__ __launch_bounds__(kWaves * kWave, 1) void k_attn_rows(AttnCall a) {
+    constexpr int KJ = D / 64, W = VWords<D>::n, U = D / 16;
+    __shared__ float lds_o[kWaves][16][D + 4];
+    __shared__ float lds_m[kWaves][16], lds_l[kWaves][16];
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+    const int col = lane & 15, g4 = lane >> 4;
+    int id = (int)blockIdx.x;
+    const int head = id % a.n_kv;
+    id /= a.n_kv;
+    const int tile = id % a.row_tiles;
+    id /= a.row_tiles;
+    const int r = id % a.R, chunk = id / a.R;
+    const ReqSpan s = req_span(a, r);
+    const int G = a.group, rows = s.n * G, row0 = tile * 16 * NR;
+    if (row0 >= rows || s.n > a.n_most) return;
+    const int begin = key_lo(a, s, 0) & ~(kBlock - 1), end = key_hi(a, s, s.n - 1);
+    const int chunks = end > begin ? (end - begin + a.chunk - 1) / a.chunk : 1;
+    if (chunk >= chunks) return;
+    const int k0 = begin + chunk * a.chunk;
+    const int last_row = row0 + 16 * NR < rows ? row0 + 16 * NR - 1 : rows - 1;
+    const int i_first = row0 / G, i_last = last_row / G;
+    // keys that every row of the tile sees, and that any does
+    const int all_lo = key_lo(a, s, i_last), all_hi = key_hi(a, s, i_first);
+    const int any_lo = key_lo(a, s, i_first), any_hi = key_hi(a, s, i_last);
+    const int k1 = any_hi < k0 + a.chunk ? any_hi : k0 + a.chunk;
+
+    // page and scales of each of this wave's 16-key groups, one per lane
+    const int my_key = k0 + ((lane >> 2) * kWaves + wave) * kBlock + (lane & 3) * 16;
+    int my_page = 0;
+    float my_ks = 1.0f, my_vs = 1.0f;
+    if (my_key < k1) {
+        my_page = page_of(a, r, my_key);
+        my_ks = pow2_scale(a.k_scale[(int64_t)my_page * a.n_kv + head]);
+        my_vs = pow2_scale(a.v_scale[(int64_t)my_page * a.n_kv + head]);
+    }
+
+    // queries: lane (row col, reduction group g4)
+    bf16x8_t q[NR][2 * KJ][NS];
+    int hi[NR], lo[NR];
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+        const int row = row0 + nr * 16 + col;
+        const bool live = row < rows;
+        const int i = live ? row / G : 0, h = head * G + (live ? row % G : 0);
+        hi[nr] = key_hi(a, s, live ? i : i_last);
+        lo[nr] = key_lo(a, s, live ? i : i_last);
+        const int64_t at = (int64_t)(s.t0 + i) * a.q_stride + (int64_t)h * D + 16 * g4;
+#pragma unroll
+        for (int j = 0; j < KJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if constexpr (NS == 1) {
+                    bf16x8_t v = *reinterpret_cast<const bf16x8_t*>(static_cast<const uint16_t*>(a.q) + at + 64 * j + 8 * e);
+                    q[nr][2 * j + e][0] = v;
+                } else {
+                    const float* f = static_cast<const float*>(a.q) + at + 64 * j + 8 * e;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        __bf16 part[NS];
+                        split_bf16<NS>(f[c], part);
+#pragma unroll
+                        for (int n = 0; n < NS; ++n) q[nr][2 * j + e][n][c] = part[n];
+                    }
+                }
+            }
+    }
+
+    f32x4_t o[NR][U];
+    float m[NR], l[NR];
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+        m[nr] = -__builtin_inff();
+        l[nr] = 0.0f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) o[nr][u] = f32x4_t{0, 0, 0, 0};
+    }
+
+    uint4 kreg[4][KJ];
+    uint32_t vreg[4][4][W];
+    const auto row_base = [&](int step, int t) -> int64_t {  // first code of a 16-key group's first row
+        const int page = __builtin_amdgcn_readlane(my_page, step * 4 + t);
+        const int key = k0 + (step * kWaves + wave) * kBlock + t * 16;
+        return ((((int64_t)page * a.n_kv + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1))) * D;
+    };
+    const auto load_k = [&](int step) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const uint8_t* p = a.k_codes + row_base(step, t) + col * D + 16 * g4;
+#pragma unroll
+            for (int j = 0; j < KJ; ++j) kreg[t][j] = *reinterpret_cast<const uint4*>(p + 64 * j);
+        }
+    };
+    const auto load_v = [&](int step) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const uint8_t* p = a.v_codes + row_base(step, t) + 4 * g4 * D + col * (D / 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) load_words<W>(p + i * D, vreg[t][i]);
+        }
+    };
+
+    const int steps = k1 > k0 + wave * kBlock ? (k1 - k0 - wave * kBlock + kWaves * kBlock - 1) / (kWaves * kBlock) : 0;
+    if (steps > 0) {
+        load_k(0);
+        load_v(0);
+    }
+    const float c = a.scale_log2;
+    for (int step = 0; step < steps; ++step) {
+        const int kb = k0 + (step * kWaves + wave) * kBlock;
+        f32x4_t sc[NR][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const float ks = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_ks), step * 4 + t));
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) sc[nr][t] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < KJ; ++j) {
+                const bf16x8_t k_lo = codes_to_bf16(kreg[t][j].x, kreg[t][j].y, ks, ks);
+                const bf16x8_t k_hi = codes_to_bf16(kreg[t][j].z, kreg[t][j].w, ks, ks);
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                    for (int n = NS - 1; n >= 0; --n) {  // small parts first
+                        sc[nr][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k_lo, q[nr][2 * j][n], sc[nr][t], 0, 0, 0);
+                        sc[nr][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k_hi, q[nr][2 * j + 1][n], sc[nr][t], 0, 0, 0);
+                    }
+            }
+        }
+        if (step + 1 < steps) load_k(step + 1);
+
+        const bool masked = kb < all_lo || kb + kBlock > all_hi;
+        bool nan = false;
+        if (masked) {
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = kb + 16 * t + 4 * g4 + i;
+                        if (key < lo[nr] || key >= hi[nr]) sc[nr][t][i] = -__builtin_inff();
+                    }
+            // keys that no row sees may hold anything; those that some rows do
+            // not see must not reach them through 0 * NaN
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int key = kb + 16 * t + 4 * g4 + i;
+                    const bool any = key >= any_lo && key < any_hi;
+#pragma unroll
+                    for (int w = 0; w < W; ++w) {
+                        vreg[t][i][w] = any ? vreg[t][i][w] : 0;
+                        nan |= has_nan(vreg[t][i][w]);
+                    }
+                }
+            nan = __any(nan);
+        }
+        bf16x8_t p[NR][2][NS];
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+            float top = -__builtin_inff();
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[nr][t][i]);
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float m_new = fmaxf(m[nr], top * c);
+            if (__any(m_new > m[nr])) {
+                const float shrink = __builtin_amdgcn_exp2f(m[nr] - (m_new == -__builtin_inff() ? 0.0f : m_new));
+                l[nr] *= shrink;
+#pragma unroll
+                for (int u = 0; u < U; ++u) o[nr][u] *= shrink;
+                m[nr] = m_new;
+            }
+            const float ref = m[nr] == -__builtin_inff() ? 0.0f : m[nr];
+            float sum = 0.0f;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float e = __builtin_amdgcn_exp2f(fmaf(sc[nr][t][i], c, -ref));
+                    sum += e;
+                    __bf16 part[NS];
+                    split_bf16<NS>(e, part);
+#pragma unroll
+                    for (int n = 0; n < NS; ++n) p[nr][t / 2][n][(t & 1) * 4 + i] = part[n];
+                }
+            l[nr] += sum;
+        }
+        // O^T += V^T P^T; column of output tile u in lane col: col * U + u
+#pragma unroll
+        for (int t2 = 0; t2 < 2; ++t2) {
+            const float va = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_vs), step * 4 + 2 * t2));
+            const float vb = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_vs), step * 4 + 2 * t2 + 1));
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                uint32_t in[4], x[4], y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) in[i] = vreg[2 * t2][i][w];
+                transpose4(in, x);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) in[i] = vreg[2 * t2 + 1][i][w];
+                transpose4(in, y);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    bf16x8_t v = codes_to_bf16(x[b], y[b], va, vb);
+                    const int u = 4 * w + b;
+                    if (nan) {
+                        const bf16x8_t where = take_nan(v);
+#pragma unroll
+                        for (int nr = 0; nr < NR; ++nr) {
+                            bf16x8_t seen;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int key = kb + 32 * t2 + 16 * (i / 4) + 4 * g4 + (i & 3);
+                                seen[i] = key >= lo[nr] && key < hi[nr] ? (__bf16)1.0f : (__bf16)0.0f;
+                            }
+                            const f32x4_t n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(where, seen, f32x4_t{0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (n[i] > 0.0f) o[nr][u][i] = __builtin_nanf("");
+                        }
+                    }
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                        for (int n = NS - 1; n >= 0; --n)
+                            o[nr][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[nr][t2][n], o[nr][u], 0, 0, 0);
+                }
+            }
+        }
+        if (step + 1 < steps) load_v(step + 1);
+    }
+
+    // the four waves' parts, joined in LDS
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+        float sum = l[nr] + __shfl_xor(l[nr], 16);
+        sum += __shfl_xor(sum, 32);
+        if (nr > 0) __syncthreads();
+        if (lane < 16) {
+            lds_m[wave][col] = m[nr];
+            lds_l[wave][col] = sum;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int u = 0; u < U; u += 4)
+                *reinterpret_cast<float4*>(&lds_o[wave][col][(4 * g4 + i) * U + u]) =
+                    make_float4(o[nr][u][i], o[nr][u + 1][i], o[nr][u + 2][i], o[nr][u + 3][i]);
+        __syncthreads();
+        constexpr int TPR = D / 4;  // threads per row
+        for (int x = threadIdx.x; x < 16 * TPR; x += kWaves * kWave) {
+            const int rr = x / TPR, d = (x % TPR) * 4, row = row0 + nr * 16 + rr;
+            if (row >= rows) continue;
+            float top = lds_m[0][rr];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) top = fmaxf(top, lds_m[w][rr]);
+            const float ref = top == -__builtin_inff() ? 0.0f : top;
+            float total = 0.0f;
+            float4 acc = make_float4(0, 0, 0, 0);
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                const float f = __builtin_amdgcn_exp2f(lds_m[w][rr] - ref);
+                total = fmaf(f, lds_l[w][rr], total);
+                const float4 v = *reinterpret_cast<const float4*>(&lds_o[w][rr][d]);
+                acc.x = fmaf(f, v.x, acc.x), acc.y = fmaf(f, v.y, acc.y);
+                acc.z = fmaf(f, v.z, acc.z), acc.w = fmaf(f, v.w, acc.w);
+            }
+            const int i = row / G, h = head * G + row % G;
+            if (chunks == 1) {
+                const bool none = key_hi(a, s, i) <= key_lo(a, s, i);
+                store_part<NS == 1>(a, s.t0 + i, h, d, D, acc, total, top, none);
+            } else {
+                const int64_t at = ((int64_t)(s.t0 + i) * a.n_q + h) * a.max_chunks + chunk;
+                *reinterpret_cast<float4*>(a.part_o + at * D + d) = acc;
+                if (d == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(top, total);
+            }
+        }
+    }
+}
+
+// The chunks of each row, joined in order: one wave per row.
+template <int D, bool BF16>
+__global__ __launch_bounds__(kWaves * kWave) void k_attn_join(AttnCall a) {
+    int64_t id = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave;
+    const int h = (int)(id % a.n_q);
+    id /= a.n_q;
+    const int i = (int)(id % a.n_most), r = (int)(id / a.n_most);
+    if (r >= a.R) return;
+    const ReqSpan s = req_span(a, r);
+    if (i >= s.n || s.n > a.n_most) return;
+    const int begin = key_lo(a, s, 0) & ~(kBlock - 1), end = key_hi(a, s, s.n - 1);
+    const int chunks = end > begin ? (end - begin + a.chunk - 1) / a.chunk : 1;
+    if (chunks == 1) return;
+    const int lane = lane_id();
+    const int64_t at = ((int64_t)(s.t0 + i) * a.n_q + h) * a.max_chunks;
+    float top = -__builtin_inff();
+    for (int c = lane; c < chunks; c += kWave) top = fmaxf(top, a.part_ml[2 * (at + c)]);
+    top = wave_max_f32(top);
+    const float ref = top == -__builtin_inff() ? 0.0f : top;
+    float total = 0.0f;
+    float acc[D / kWave];
+#pragma unroll
+    for (int e = 0; e < D / kWave; ++e) acc[e] = 0.0f;
+#pragma unroll 4
+    for (int c = 0; c < chunks; ++c) {
+        const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * (at + c));
+        const float f = __builtin_amdgcn_exp2f(ml.x - ref);
+        total = fmaf(f, ml.y, total);
+#pragma unroll
+        for (int e = 0; e < D / kWave; ++e) acc[e] = fmaf(f, a.part_o[(at + c) * D + e * kWave + lane], acc[e]);
+    }
+    const bool none = key_hi(a, s, i) <= key_lo(a, s, i);
+    const float inv = none ? 0.0f : 1.0f / total;
+    const int64_t out = (int64_t)(s.t0 + i) * a.out_stride + (int64_t)h * D;
+#pragma unroll
+    for (int e = 0; e < D / kWave; ++e) {
+        const float v = none ? 0.0f : acc[e] * inv;
+        if constexpr (BF16) static_cast<__bf16*>(a.out)[out + e * kWave + lane] = (__bf16)v;
+        else static_cast<float*>(a.out)[out + e * kWave + lane] = v;
+    }
+    if (a.lse && lane == 0)
+        a.lse[(int64_t)(s.t0 + i) * a.n_q + h] = none ? -__builtin_inff() : (top + __builtin_amdgcn_logf(total)) * kLn2;
+}
+
+template <int D, int NS, int NR>
+hipError_t launch_rows(const AttnCall& a, hipStream_t s) {
+    const int64_t grid = (int64_t)a.n_kv * a.row_tiles * a.R * a.max_chunks;
+    if (grid >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;
+    k_attn_rows<D, NS, NR><<<(unsigned)grid, kWaves * kWave, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.max_chunks == 1) return e;
+    const int64_t rows = (int64_t)a.R * a.n_most * a.n_q;
+    if (rows >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
+    k_attn_join<D, NS == 1><<<(unsigned)((rows + kWaves - 1) / kWaves), kWaves * kWave, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_d(const AttnCall& a, bool bf16, int nr, hipStream_t s) {
+    if (!bf16) return launch_rows<D, 3, 1>(a, s);
+    if constexpr (D < 256) {
+        if (nr == 4) return launch_rows<D, 1, 4>(a, s);
+    }
+    return nr >= 2 ? launch_rows<D, 1, 2>(a, s) : launch_rows<D, 1, 1>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_attn_rows(const AttnCall& a, int head_dim, bool bf16, int nr, hipStream_t s) {
+    switch (head_dim) {
+        case 64: return launch_d<64>(a, bf16, nr, s);
+        case 128: return launch_d<128>(a, bf16, nr, s);
+        default: return launch_d<256>(a, bf16, nr, s);
+    }
+}
+
+}  // namespace rdg

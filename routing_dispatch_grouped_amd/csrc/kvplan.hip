@@ -1,0 +1,311 @@
+// Step plan of the paged key/value cache: block tables and slot maps built on
+// the GPU from the requests' lengths, and the pages handed back.
+//
+// With P = page_rows, request r holds ceil(kv_r / P) pages and needs
+//   need_r = ceil((kv_r + q_r) / P) - ceil(kv_r / P)
+// more.  An exclusive scan of need over the requests gives each its place on
+// the stack of free pages, one of q gives cu_q, and one of the pages that the
+// new tokens touch gives each request's first segment.  Every new page starts
+// with exactly one new token (its position is a multiple of P), so the
+// per-token pass writes the block table too.
+//
+// Bound by latency: a step writes 8 bytes per token and reads 8 per request,
+// a few microseconds' worth of one launch.  Every workgroup therefore scans
+// all the requests by itself in LDS (12 bytes a request) instead of waiting
+// for another launch or workgroup, and then expands its own 1024 tokens.
+// The last workgroup to finish (a ticket in S.work) writes what a caller may
+// pass as input and output at once: kv_len, the free count, the status.
+#include "rdg_internal.h"
+
+namespace rdg {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTokPerThread = 4;
+constexpr uint32_t kSat = 1u << 30;
+
+// Saturating sum of values <= 2^30: associative, so lengths of any size scan
+// without wrapping.
+__device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) {
+    const uint32_t s = a + b;
+    return s < kSat ? s : kSat;
+}
+
+// Exclusive saturating scan of one value per thread over the workgroup; part
+// holds one word per wave.  The total is left in *total.
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* part, uint32_t* total) {
+    const int lane = lane_id(), wave = (int)threadIdx.x / kWave;
+    uint32_t inc = v;
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) {
+        const uint32_t o = __shfl_up(inc, off);
+        if (lane >= off) inc = sat_add(inc, o);
+    }
+    __syncthreads();  // part may still be read from the scan before
+    if (lane == kWave - 1) part[wave] = inc;
+    uint32_t exc = __shfl_up(inc, 1);
+    if (lane == 0) exc = 0;
+    __syncthreads();
+    uint32_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / kWave; ++w) {
+        if (w < wave) before = sat_add(before, part[w]);
+        all = sat_add(all, part[w]);
+    }
+    *total = all;
+    return sat_add(before, exc);
+}
+
+// Last i in [0, n) with begin[i] <= t (begin[0] = 0, ascending).
+__device__ __forceinline__ int find_row(const uint32_t* begin, int n, uint32_t t) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (begin[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// True in every thread of the last workgroup of the grid to get here; the
+// ticket is then 0 again for the next launch.
+__device__ __forceinline__ bool last_block(int32_t* ticket) {
+    __shared__ int last;
+    __syncthreads();  // every wave has used what it read
+    if (threadIdx.x == 0) {
+        last = 1;
+        if (gridDim.x > 1) {
+            last = __hip_atomic_fetch_add(ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
+            if (last) __hip_atomic_store(ticket, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+    }
+    __syncthreads();
+    return last != 0;
+}
+
+// work[1]: 1 + the first request found with a page id outside the cache.
+__device__ __forceinline__ void note_bad(int32_t* work, int r) {
+    int32_t none = 0;
+    __hip_atomic_compare_exchange_strong(work + 1, &none, r + 1, __ATOMIC_RELAXED, __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__device__ __forceinline__ void write_status(int32_t* status, int32_t* work, int code, int detail) {
+    const int bad = __hip_atomic_load(work + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (bad != 0) {
+        __hip_atomic_store(work + 1, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (code == RDG_OK) {
+            code = RDG_EDATA;
+            detail = bad - 1;
+        }
+    }
+    status[0] = code;
+    status[1] = detail;
+}
+
+struct Lens {
+    int kv, q;
+    bool bad;
+};
+
+// A request's lengths, made safe: negative ones count as 0 and are reported.
+__device__ __forceinline__ Lens lens_of(const int32_t* kv_len, const int32_t* q_len, int r) {
+    Lens l = {kv_len[r], q_len[r], false};
+    if (l.kv < 0 || l.q < 0 || l.kv > (int)kSat || l.q > (int)kSat) {
+        l.bad = true;
+        l.kv = 0;
+        l.q = 0;
+    }
+    return l;
+}
+
+__global__ __launch_bounds__(kThreads) void k_kv_plan(rdg_kv_step S, int shift, const int32_t* kv_len,
+                                                      const int32_t* q_len, const int32_t* __restrict__ free_list,
+                                                      const int32_t* n_free, int32_t* n_free_out) {
+    extern __shared__ uint32_t lds[];
+    __shared__ uint32_t part[kThreads / kWave];
+    __shared__ uint32_t used;        // pages taken
+    __shared__ uint32_t failed[2];   // first request that did not fit / had bad lengths
+    const int R = S.n_req, P1 = S.page_rows - 1, tid = (int)threadIdx.x;
+    uint32_t* cu = lds;              // [R + 1] first token
+    int32_t* page0 = (int32_t*)(lds + R + 1);  // [R] place on the free stack, -1: not admitted
+    uint32_t* seg0 = lds + 2 * R + 1;          // [R] first segment
+    if (tid == 0) {
+        used = 0;
+        failed[0] = failed[1] = 0xffffffffu;
+        cu[0] = 0;
+    }
+    int nf = n_free[0];
+    nf = nf < 0 ? 0 : nf > S.n_pages ? S.n_pages : nf;
+    const int per = (R + kThreads - 1) / kThreads;
+    const int r0 = tid * per < R ? tid * per : R, r1 = r0 + per < R ? r0 + per : R;
+
+    uint32_t q_sum = 0, need_sum = 0;
+    for (int r = r0; r < r1; ++r) {
+        const Lens l = lens_of(kv_len, q_len, r);
+        const int old_b = (l.kv + P1) >> shift, new_b = (int)(((uint32_t)l.kv + l.q + P1) >> shift);
+        q_sum = sat_add(q_sum, l.q);
+        need_sum = sat_add(need_sum, new_b > S.max_blocks ? 0 : new_b - old_b);
+    }
+    uint32_t n_tok, n_seg, all;
+    uint32_t tok = block_scan(q_sum, part, &n_tok), pg = block_scan(need_sum, part, &all);
+    uint32_t seg_sum = 0;
+    for (int r = r0; r < r1; ++r) {
+        const Lens l = lens_of(kv_len, q_len, r);
+        const int old_b = (l.kv + P1) >> shift, new_b = (int)(((uint32_t)l.kv + l.q + P1) >> shift);
+        const bool fits = new_b <= S.max_blocks;
+        const uint32_t need = fits ? new_b - old_b : 0;
+        const uint32_t begin = pg;
+        tok = sat_add(tok, l.q);
+        pg = sat_add(pg, need);
+        const bool ok = !l.bad && fits && tok <= (uint32_t)S.t_cap && (need == 0 || pg <= (uint32_t)nf);
+        cu[r + 1] = tok;
+        page0[r] = ok ? (need ? (int)begin : 0) : -1;
+        uint32_t segs = 0;
+        if (ok && l.q > 0) segs = ((l.kv + l.q - 1) >> shift) - (l.kv >> shift) + 1;
+        seg0[r] = seg_sum;
+        seg_sum += segs;
+        if (ok && need) atomicMax(&used, pg);
+        if (!ok) atomicMin(&failed[l.bad ? 1 : 0], (uint32_t)r);
+    }
+    const uint32_t seg_before = block_scan(seg_sum, part, &n_seg);
+    for (int r = r0; r < r1; ++r) seg0[r] += seg_before;
+    __syncthreads();
+
+    // tokens: kTokPerThread consecutive ones per thread
+    const uint32_t total = n_tok < (uint32_t)S.t_cap ? n_tok : (uint32_t)S.t_cap;
+    const int t0 = ((int)blockIdx.x * kThreads + tid) * kTokPerThread;
+    if (t0 < S.t_cap) {
+        int32_t slot[kTokPerThread], pos[kTokPerThread];
+        int r = (uint32_t)t0 < total ? find_row(cu, R, t0) : 0;
+#pragma unroll
+        for (int i = 0; i < kTokPerThread; ++i) {
+            const uint32_t t = t0 + i;
+            slot[i] = -1;
+            pos[i] = 0;
+            if (t >= total) continue;
+            while (cu[r + 1] <= t) ++r;
+            const int kv = lens_of(kv_len, q_len, r).kv, base = page0[r];
+            const int p = kv + (int)(t - cu[r]), blk = p >> shift;
+            pos[i] = p;
+            if (base < 0) continue;
+            const int old_b = (kv + P1) >> shift;
+            int32_t* entry = S.block_table + (int64_t)r * S.max_blocks + blk;
+            int page;
+            if (blk < old_b) {
+                page = *entry;
+            } else {
+                page = free_list[nf - 1 - base - (blk - old_b)];
+                if ((p & P1) == 0) *entry = page;
+            }
+            if ((unsigned)page < (unsigned)S.n_pages) slot[i] = (page << shift) + (p & P1);
+            else note_bad(S.work, r);
+            if (p == kv || (p & P1) == 0) {
+                const uint32_t s = seg0[r] + (blk - (kv >> shift));
+                if (s < (uint32_t)S.seg_cap) S.seg_tok[s] = (int)t;
+            }
+        }
+        if (t0 + kTokPerThread <= S.t_cap) {
+            *reinterpret_cast<int4*>(S.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+            *reinterpret_cast<int4*>(S.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        } else {
+            for (int i = 0; t0 + i < S.t_cap; ++i) {
+                S.slots[t0 + i] = slot[i];
+                S.positions[t0 + i] = pos[i];
+            }
+        }
+    }
+    for (int s = (int)n_seg + (int)blockIdx.x * kThreads + tid; s < S.seg_cap; s += (int)gridDim.x * kThreads)
+        S.seg_tok[s] = -1;
+
+    if (!last_block(S.work)) return;
+    for (int r = tid; r < R; r += kThreads) {
+        const Lens l = lens_of(kv_len, q_len, r);
+        S.cu_q[r + 1] = (int)(cu[r + 1] < (uint32_t)S.t_cap ? cu[r + 1] : (uint32_t)S.t_cap);
+        S.kv_len[r] = page0[r] >= 0 ? l.kv + l.q : l.kv;
+    }
+    if (tid == 0) {
+        S.cu_q[0] = 0;
+        n_free_out[0] = nf - (int)used;
+        const bool bad = failed[1] != 0xffffffffu, full = failed[0] != 0xffffffffu;
+        write_status(S.status, S.work, bad ? RDG_EDATA : full ? RDG_ECAPACITY : RDG_OK,
+                     bad ? (int)failed[1] : full ? (int)failed[0] : 0);
+    }
+}
+
+// Pages behind the new lengths, in request and block order, onto the stack.
+__global__ __launch_bounds__(kThreads) void k_kv_trim(rdg_kv_step S, int shift, const int32_t* new_len,
+                                                      const int32_t* kv_len, int32_t* __restrict__ free_list,
+                                                      const int32_t* n_free, int32_t* n_free_out) {
+    extern __shared__ uint32_t lds[];
+    __shared__ uint32_t part[kThreads / kWave];
+    __shared__ uint32_t failed;
+    const int R = S.n_req, P1 = S.page_rows - 1, tid = (int)threadIdx.x;
+    uint32_t* begin = lds;  // [R] first freed page of each request
+    if (tid == 0) failed = 0xffffffffu;
+    int nf = n_free[0];
+    nf = nf < 0 ? 0 : nf > S.n_pages ? S.n_pages : nf;
+    const int limit = S.max_blocks << shift;
+    const int per = (R + kThreads - 1) / kThreads;
+    const int r0 = tid * per < R ? tid * per : R, r1 = r0 + per < R ? r0 + per : R;
+    __syncthreads();
+    uint32_t sum = 0;
+    for (int r = r0; r < r1; ++r) {
+        const int kv = kv_len[r], to = new_len[r];
+        uint32_t n = 0;
+        if (kv < 0 || kv > limit || to < 0 || to > kv) atomicMin(&failed, (uint32_t)r);
+        else n = ((kv + P1) >> shift) - ((to + P1) >> shift);
+        begin[r] = sum;
+        sum = sat_add(sum, n);
+    }
+    uint32_t total;
+    const uint32_t before = block_scan(sum, part, &total);
+    for (int r = r0; r < r1; ++r) begin[r] = sat_add(begin[r], before);
+    __syncthreads();
+    const bool fits = total <= (uint32_t)(S.n_pages - nf);
+    if (fits) {
+        for (uint32_t e = blockIdx.x * kThreads + tid; e < total; e += gridDim.x * kThreads) {
+            const int r = find_row(begin, R, e);
+            int32_t* entry = S.block_table + (int64_t)r * S.max_blocks + ((new_len[r] + P1) >> shift) + (e - begin[r]);
+            const int page = *entry;
+            if ((unsigned)page >= (unsigned)S.n_pages) note_bad(S.work, r);
+            free_list[nf + e] = page;
+            *entry = -1;
+        }
+    }
+    if (!last_block(S.work)) return;
+    for (int r = tid; r < R; r += kThreads) {
+        const int kv = kv_len[r], to = new_len[r];
+        S.kv_len[r] = (!fits || kv < 0 || kv > limit || to < 0 || to > kv) ? kv : to;
+    }
+    if (tid == 0) {
+        n_free_out[0] = nf + (fits ? (int)total : 0);
+        const bool bad = failed != 0xffffffffu;
+        write_status(S.status, S.work, bad ? RDG_EDATA : fits ? RDG_OK : RDG_ECAPACITY,
+                     bad ? (int)failed : fits ? 0 : (int)total);
+    }
+}
+
+inline int log2_of(int p) { return p == 16 ? 4 : p == 32 ? 5 : p == 64 ? 6 : 7; }
+
+}  // namespace
+
+hipError_t launch_kv_plan(const rdg_kv_step& S, const int32_t* kv_len, const int32_t* q_len, const int32_t* free_list,
+                          const int32_t* n_free, int32_t* n_free_out, hipStream_t s) {
+    const int per_block = kThreads * kTokPerThread;
+    const int blocks = S.t_cap > 0 ? (S.t_cap + per_block - 1) / per_block : 1;
+    const size_t bytes = sizeof(uint32_t) * (3 * (size_t)S.n_req + 1);
+    k_kv_plan<<<blocks, kThreads, bytes, s>>>(S, log2_of(S.page_rows), kv_len, q_len, free_list, n_free, n_free_out);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_trim(const rdg_kv_step& S, const int32_t* new_len, const int32_t* kv_len, int32_t* free_list,
+                          const int32_t* n_free, int32_t* n_free_out, hipStream_t s) {
+    const int64_t most = (int64_t)S.n_req * S.max_blocks;
+    const int blocks = (int)(most >= 64 * 2048 ? 64 : (most + 2047) / 2048);
+    k_kv_trim<<<blocks < 1 ? 1 : blocks, kThreads, sizeof(uint32_t) * (size_t)S.n_req, s>>>(
+        S, log2_of(S.page_rows), new_len, kv_len, free_list, n_free, n_free_out);
+    return hipGetLastError();
+}
+
+}  // namespace rdg

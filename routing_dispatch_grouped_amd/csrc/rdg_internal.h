@@ -225,4 +225,45 @@ hipError_t launch_combine_finish(const void* y, int y_dt, const int32_t* pos, in
                                  int H, const void* shared_out, void* out, int out_dt, int32_t* signals,
                                  int rows_per_sig, hipStream_t s);
 
+// Paged key/value cache: step plan, query/key norm and store, attention.
+constexpr int kMaxRequests = 4096;  // per step: the plan scans them in LDS, 12 bytes each
+hipError_t launch_kv_plan(const rdg_kv_step& S, const int32_t* kv_len, const int32_t* q_len, const int32_t* free_list,
+                          const int32_t* n_free, int32_t* n_free_out, hipStream_t s);
+hipError_t launch_kv_trim(const rdg_kv_step& S, const int32_t* new_len, const int32_t* kv_len, int32_t* free_list,
+                          const int32_t* n_free, int32_t* n_free_out, hipStream_t s);
+
+struct QkStoreCall {
+    const void* qkv;
+    void* q_out;
+    const float *q_weight, *k_weight, *cos_sin;
+    const int32_t *positions, *slots, *seg_tok;
+    uint8_t *k_codes, *v_codes;
+    float *k_scale, *v_scale;
+    int32_t* status;
+    int64_t row_stride, q_stride;  // elements
+    float eps;
+    int T, n_q, n_kv, rot_dim, n_pos, n_pages, page_rows;
+    bool neighbours;
+    // set by the launcher: page workgroups, and the split of the query heads over waves
+    int page_items, q_passes, q_chunks;
+    int64_t q_items;
+};
+hipError_t launch_qk_store(QkStoreCall a, int head_dim, bool bf16, int seg_cap, hipStream_t s);
+
+struct AttnCall {
+    const void* q;
+    void* out;
+    float *lse, *part_o, *part_ml;  // parts of rows whose keys are split: [T, n_q, max_chunks] x (D, 2)
+    const int32_t *block_table, *cu_q, *kv_len;
+    const uint8_t *k_codes, *v_codes;
+    const float *k_scale, *v_scale;
+    int32_t* status;
+    int64_t q_stride, out_stride;  // elements
+    float scale_log2;              // softmax scale times log2(e)
+    int T, R, n_q, n_kv, group, max_blocks, n_pages, page_shift, kv_cap, window;
+    bool causal;
+    int n_most, row_tiles, chunk, max_chunks;  // split of k_attn_rows
+};
+hipError_t launch_attn_rows(const AttnCall& a, int head_dim, bool bf16, int nr, hipStream_t s);
+
 }  // namespace rdg
