@@ -12,7 +12,8 @@ OUT = os.path.join(PKG, "librdg.so")
 BUILD = os.path.join(PKG, "_build")
 
 SOURCES = ["abi.hip", "route.hip", "dispatch.hip", "quant.hip", "pack.hip", "ffn.hip", "ffn_tiled.hip", "combine.hip",
-           "kvplan.hip", "qkstore.hip", "attn.hip", "abi_kv.hip", "eplb.cpp", "tbo.cpp"]
+           "kvplan.hip", "qkstore.hip", "attn.hip", "attn_tiles.hip",
+           "abi_kv.hip", "eplb.cpp", "tbo.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -38,32 +38,62 @@ int cache_buffers_rc(const rdg_kv_cache* C) {
     return RDG_OK;
 }
 
-constexpr int kChunkMin = 256, kChunkMax = 4096;  // keys; a workgroup's lanes hold the pages of 4096
-constexpr int kUnits = 1024;                      // workgroups wanted: four per CU
+constexpr int kChunkMin = 256, kChunkMax = 4096;  // keys; a k_attn_rows workgroup's lanes hold the pages of 4096
+constexpr int kRowUnits = 1024;                   // k_attn_rows workgroups wanted: four per CU
+constexpr int kTileUnits = 512;                   // k_attn_tiles workgroups wanted: two per CU
+constexpr int kTileChunkMin = 512;
 
-// How k_attn_rows splits its work.
-struct RowsPlan {
-    int nr, row_tiles, chunk, max_chunks;
+// How a call's work is split.  span: the longest run of keys that one request's
+// queries see together.
+struct AttnPlan {
+    int nr;  // 16-row tiles per wave of k_attn_rows
+    int n_most, row_tiles, chunk, row_chunks;
+    int tile_slots, tile_chunk, tile_chunks;  // tile_slots 0: no k_attn_tiles
+    int max_chunks;
 };
 
-RowsPlan plan_rows(int R, int n_kv, int group, int head_dim, bool bf16, int n_most, int span) {
-    RowsPlan p;
-    const int64_t rows = (int64_t)n_most * group;
-    p.nr = !bf16 || rows <= 16 ? 1 : rows <= 32 || head_dim == 256 ? 2 : 4;
-    p.row_tiles = (int)((rows + 16 * p.nr - 1) / (16 * p.nr));
-    const double units = (double)R * n_kv * p.row_tiles;
-    double want = ceil(span * units / kUnits / kChunkMin) * kChunkMin;
-    if (want < kChunkMin) want = kChunkMin;
-    p.chunk = want > kChunkMax ? kChunkMax : (int)want;
-    p.max_chunks = (int)(((int64_t)span + 63 + p.chunk - 1) / p.chunk);
-    if (p.max_chunks < 1) p.max_chunks = 1;
+int chunks_of(int64_t span, int chunk) {
+    const int64_t n = (span + 63 + chunk - 1) / chunk;
+    return n < 1 ? 1 : (int)n;
+}
+
+AttnPlan plan_attn(int T, int R, int n_kv, int group, int head_dim, bool bf16, int max_q, int span) {
+    AttnPlan p = {};
+    // Requests of more than 64 rows (query x head of the group) go to
+    // k_attn_tiles, whose workgroups share the conversion of the codes.
+    const bool tiles = bf16 && (int64_t)max_q * group > 64;
+    p.n_most = max_q;
+    if (tiles) {
+        p.n_most = 64 / group;
+        // no request is that short if even max_q for all the others leaves more
+        if ((int64_t)T - (int64_t)(R - 1) * max_q > p.n_most) p.n_most = 0;
+        const int bm = attn_tile_rows(head_dim);
+        p.tile_slots = (int)((int64_t)T * group / bm + R);
+        const double units = (double)n_kv * ceil((double)T * group / bm);
+        double want = ceil(span * units / kTileUnits / 64) * 64;
+        if (want < kTileChunkMin) want = kTileChunkMin;
+        if (want > span + 63.0) want = (span + 63) / 64 * 64 + 64;
+        p.tile_chunk = (int)want;
+        p.tile_chunks = chunks_of(span, p.tile_chunk);
+        p.max_chunks = p.tile_chunks;
+    }
+    if (p.n_most > 0) {
+        const int64_t rows = (int64_t)p.n_most * group;
+        p.nr = !bf16 || rows <= 16 ? 1 : rows <= 32 || head_dim == 256 ? 2 : 4;
+        p.row_tiles = (int)((rows + 16 * p.nr - 1) / (16 * p.nr));
+        const double units = (double)R * n_kv * p.row_tiles;
+        double want = ceil(span * units / kRowUnits / kChunkMin) * kChunkMin;
+        if (want < kChunkMin) want = kChunkMin;
+        p.chunk = want > kChunkMax ? kChunkMax : (int)want;
+        p.row_chunks = chunks_of(span, p.chunk);
+        if (p.row_chunks > p.max_chunks) p.max_chunks = p.row_chunks;
+    }
     return p;
 }
 
 // Bytes of one part (fp32 row, maximum and sum) of every row.
 size_t part_bytes(int T, int n_q, int head_dim) { return sizeof(float) * (size_t)T * n_q * (head_dim + 2); }
 
-// The longest run of keys that one request's queries see together.
 int key_span(int max_q, int max_kv, int window) {
     const int64_t w = window > 0 ? (int64_t)window + max_q : max_kv;
     return w < max_kv ? (int)w : max_kv;
@@ -142,7 +172,7 @@ size_t rdg_paged_attention_workspace_bytes(const rdg_kv_cache* C, int T, int n_r
         max_kv <= 0)
         return 0;
     if (max_q > T) max_q = T;
-    const RowsPlan p = plan_rows(n_req, C->n_kv, n_q / C->n_kv, C->head_dim, dtype == RDG_BF16, max_q, max_kv);
+    const AttnPlan p = plan_attn(T, n_req, C->n_kv, n_q / C->n_kv, C->head_dim, dtype == RDG_BF16, max_q, max_kv);
     return p.max_chunks > 1 ? align256(part_bytes(T, n_q, C->head_dim) * p.max_chunks) : 0;
 }
 
@@ -176,21 +206,32 @@ int rdg_paged_attention(const void* q, int dtype, int64_t q_stride, int T, int n
     // The workspace is sized for all max_kv keys.  A window leaves a shorter run,
     // which may be cut finer than the workspace holds parts for: then coarser.
     const int span = key_span(max_q, max_kv, window);
-    RowsPlan p = plan_rows(a.R, a.n_kv, a.group, D, bf16, max_q, span);
+    AttnPlan p = plan_attn(T, a.R, a.n_kv, a.group, D, bf16, max_q, span);
     const size_t part = part_bytes(T, n_q, D);
     const size_t need = rdg_paged_attention_workspace_bytes(C, T, a.R, n_q, max_q, max_kv, dtype);
     if (need > 0 && (!work || !aligned16(work) || work_bytes < need)) return RDG_EINVAL;
     const int64_t room = need > 0 ? (int64_t)(need / part) : 1;
-    if (p.max_chunks > room) {
-        p.chunk = (int)((((int64_t)span + 63 + room - 1) / room + kChunkMin - 1) / kChunkMin * kChunkMin);
-        p.max_chunks = (int)room;
-    }
-    a.n_most = max_q, a.row_tiles = p.row_tiles, a.chunk = p.chunk, a.max_chunks = p.max_chunks;
-    if (p.max_chunks > 1) {
+    const auto fit = [&](int* chunk, int* chunks) {
+        if (*chunks <= room) return;
+        *chunk = (int)((((int64_t)span + 63 + room - 1) / room + kChunkMin - 1) / kChunkMin * kChunkMin);
+        *chunks = chunks_of(span, *chunk);
+    };
+    if (p.tile_slots > 0) fit(&p.tile_chunk, &p.tile_chunks);
+    if (p.n_most > 0) fit(&p.chunk, &p.row_chunks);
+    a.max_chunks = p.tile_chunks > p.row_chunks ? p.tile_chunks : p.row_chunks;
+    a.n_most = p.n_most, a.rows_per_tile = 16 * p.nr, a.row_tiles = p.row_tiles, a.chunk = p.chunk;
+    a.row_chunks = p.row_chunks, a.tile_rows = attn_tile_rows(D), a.tile_slots = p.tile_slots;
+    a.tile_chunk = p.tile_chunk, a.tile_chunks = p.tile_chunks;
+    a.join_q = p.tile_chunks > 1 ? max_q : p.n_most;
+    if (a.max_chunks > 1) {
         a.part_o = static_cast<float*>(work);
-        a.part_ml = a.part_o + (size_t)T * n_q * D * p.max_chunks;
+        a.part_ml = a.part_o + (size_t)T * n_q * D * a.max_chunks;
     }
-    return hip_rc(launch_attn_rows(a, D, bf16, p.nr, stream));
+    hipError_t e = hipSuccess;
+    if (p.tile_slots > 0) e = launch_attn_tiles(a, D, stream);
+    if (e == hipSuccess && p.n_most > 0) e = launch_attn_rows(a, D, bf16, p.nr, stream);
+    if (e == hipSuccess && a.max_chunks > 1) e = launch_attn_join(a, D, bf16, stream);
+    return hip_rc(e);
 }
 
 }  // extern "C"

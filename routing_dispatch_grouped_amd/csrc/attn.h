@@ -44,6 +44,20 @@ __device__ __forceinline__ int key_lo(const AttnCall& a, const ReqSpan& s, int i
     return lo < 0 ? 0 : lo;
 }
 
+// The keys of a tile of rows [row0, row1) of one request and key head (row =
+// query * group + head of the group): [begin, end) holds every key that any of them
+// sees, begin a multiple of the 64-key blocks; it is cut into chunks of `chunk` keys.
+struct TileKeys {
+    int begin, end, chunks;
+};
+__device__ __forceinline__ TileKeys tile_keys(const AttnCall& a, const ReqSpan& s, int row0, int row1, int chunk) {
+    TileKeys k;
+    k.begin = key_lo(a, s, row0 / a.group) & ~63;
+    k.end = key_hi(a, s, (row1 - 1) / a.group);
+    k.chunks = k.end > k.begin ? (k.end - k.begin + chunk - 1) / chunk : 1;
+    return k;
+}
+
 // Page of a key, made safe: ids outside the cache are reported and read page 0.
 __device__ __forceinline__ int page_of(const AttnCall& a, int r, int key) {
     int page = a.block_table[(int64_t)r * a.max_blocks + (key >> a.page_shift)];

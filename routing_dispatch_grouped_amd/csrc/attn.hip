@@ -77,15 +77,15 @@ __global__ __launch_bounds__(kWaves * kWave, 1) void k_attn_rows(AttnCall a) {
     const ReqSpan s = req_span(a, r);
     const int G = a.group, rows = s.n * G, row0 = tile * 16 * NR;
     if (row0 >= rows || s.n > a.n_most) return;
-    const int begin = key_lo(a, s, 0) & ~(kBlock - 1), end = key_hi(a, s, s.n - 1);
-    const int chunks = end > begin ? (end - begin + a.chunk - 1) / a.chunk : 1;
-    if (chunk >= chunks) return;
-    const int k0 = begin + chunk * a.chunk;
     const int last_row = row0 + 16 * NR < rows ? row0 + 16 * NR - 1 : rows - 1;
+    const TileKeys keys = tile_keys(a, s, row0, last_row + 1, a.chunk);
+    const int chunks = keys.chunks;
+    if (chunk >= chunks) return;
     const int i_first = row0 / G, i_last = last_row / G;
     // keys that every row of the tile sees, and that any does
     const int all_lo = key_lo(a, s, i_last), all_hi = key_hi(a, s, i_first);
-    const int any_lo = key_lo(a, s, i_first), any_hi = key_hi(a, s, i_last);
+    const int any_lo = key_lo(a, s, i_first), any_hi = keys.end;
+    const int k0 = keys.begin + chunk * a.chunk;
     const int k1 = any_hi < k0 + a.chunk ? any_hi : k0 + a.chunk;
 
     // page and scales of each of this wave's 16-key groups, one per lane
@@ -346,18 +346,20 @@ __global__ __launch_bounds__(kWaves * kWave, 1) void k_attn_rows(AttnCall a) {
     }
 }
 
-// The chunks of each row, joined in order: one wave per row.
+// The chunks of each row, joined in order: one wave per row.  Rows of requests
+// with up to n_most queries were split by k_attn_rows, the others by k_attn_tiles.
 template <int D, bool BF16>
 __global__ __launch_bounds__(kWaves * kWave) void k_attn_join(AttnCall a) {
     int64_t id = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave;
     const int h = (int)(id % a.n_q);
     id /= a.n_q;
-    const int i = (int)(id % a.n_most), r = (int)(id / a.n_most);
+    const int i = (int)(id % a.join_q), r = (int)(id / a.join_q);
     if (r >= a.R) return;
     const ReqSpan s = req_span(a, r);
-    if (i >= s.n || s.n > a.n_most) return;
-    const int begin = key_lo(a, s, 0) & ~(kBlock - 1), end = key_hi(a, s, s.n - 1);
-    const int chunks = end > begin ? (end - begin + a.chunk - 1) / a.chunk : 1;
+    if (i >= s.n || s.n > a.join_q) return;
+    const int per = s.n <= a.n_most ? a.rows_per_tile : a.tile_rows, row = i * a.group + h % a.group;
+    const int row0 = row / per * per, row1 = row0 + per < s.n * a.group ? row0 + per : s.n * a.group;
+    const int chunks = tile_keys(a, s, row0, row1, s.n <= a.n_most ? a.chunk : a.tile_chunk).chunks;
     if (chunks == 1) return;
     const int lane = lane_id();
     const int64_t at = ((int64_t)(s.t0 + i) * a.n_q + h) * a.max_chunks;
@@ -392,14 +394,18 @@ __global__ __launch_bounds__(kWaves * kWave) void k_attn_join(AttnCall a) {
 
 template <int D, int NS, int NR>
 hipError_t launch_rows(const AttnCall& a, hipStream_t s) {
-    const int64_t grid = (int64_t)a.n_kv * a.row_tiles * a.R * a.max_chunks;
+    const int64_t grid = (int64_t)a.n_kv * a.row_tiles * a.R * a.row_chunks;
     if (grid >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;
     k_attn_rows<D, NS, NR><<<(unsigned)grid, kWaves * kWave, 0, s>>>(a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.max_chunks == 1) return e;
-    const int64_t rows = (int64_t)a.R * a.n_most * a.n_q;
-    if (rows >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
-    k_attn_join<D, NS == 1><<<(unsigned)((rows + kWaves - 1) / kWaves), kWaves * kWave, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <int D>
+hipError_t join_d(const AttnCall& a, bool bf16, hipStream_t s) {
+    const int64_t rows = (int64_t)a.R * a.join_q * a.n_q, grid = (rows + kWaves - 1) / kWaves;
+    if (grid >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;
+    if (bf16) k_attn_join<D, true><<<(unsigned)grid, kWaves * kWave, 0, s>>>(a);
+    else k_attn_join<D, false><<<(unsigned)grid, kWaves * kWave, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -419,6 +425,14 @@ hipError_t launch_attn_rows(const AttnCall& a, int head_dim, bool bf16, int nr, 
         case 64: return launch_d<64>(a, bf16, nr, s);
         case 128: return launch_d<128>(a, bf16, nr, s);
         default: return launch_d<256>(a, bf16, nr, s);
+    }
+}
+
+hipError_t launch_attn_join(const AttnCall& a, int head_dim, bool bf16, hipStream_t s) {
+    switch (head_dim) {
+        case 64: return join_d<64>(a, bf16, s);
+        case 128: return join_d<128>(a, bf16, s);
+        default: return join_d<256>(a, bf16, s);
     }
 }
 

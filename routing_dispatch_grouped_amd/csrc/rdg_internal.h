@@ -262,8 +262,16 @@ struct AttnCall {
     float scale_log2;              // softmax scale times log2(e)
     int T, R, n_q, n_kv, group, max_blocks, n_pages, page_shift, kv_cap, window;
     bool causal;
-    int n_most, row_tiles, chunk, max_chunks;  // split of k_attn_rows
+    int max_chunks;  // parts that the workspace has for each row
+    // requests of up to n_most queries: tiles of rows_per_tile rows, chunk keys a workgroup
+    int n_most, rows_per_tile, row_tiles, chunk, row_chunks;
+    // longer ones: tile_slots places for tiles of tile_rows rows, tile_chunk keys a workgroup
+    int tile_rows, tile_slots, tile_chunk, tile_chunks;
+    int join_q;  // queries of the longest request whose parts are joined
 };
 hipError_t launch_attn_rows(const AttnCall& a, int head_dim, bool bf16, int nr, hipStream_t s);
+hipError_t launch_attn_tiles(const AttnCall& a, int head_dim, hipStream_t s);
+hipError_t launch_attn_join(const AttnCall& a, int head_dim, bool bf16, hipStream_t s);
+inline int attn_tile_rows(int head_dim) { return head_dim == 256 ? 128 : 256; }
 
 }  // namespace rdg
