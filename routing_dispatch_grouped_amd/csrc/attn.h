@@ -90,20 +90,12 @@ __device__ __forceinline__ void transpose4(const uint32_t (&r)[4], uint32_t (&ou
     out[3] = __builtin_amdgcn_perm(d, c, 0x07060302u);
 }
 
-// Whether a dword of e4m3 codes holds a NaN (0x7f or 0xff).
-__device__ __forceinline__ bool has_nan(uint32_t w) { return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0; }
-
-// NaN elements of a bf16 operand out of it: returns 1 where they were, else 0.
-__device__ __forceinline__ bf16x8_t take_nan(bf16x8_t& v) {
-    bf16x8_t where;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const bool nan = v[i] != v[i];
-        where[i] = nan ? (__bf16)1.0f : (__bf16)0.0f;
-        v[i] = nan ? (__bf16)0.0f : v[i];
-    }
-    return where;
-}
+// NaN in V.  0 * NaN would carry a key's NaN into rows that do not see it, so in
+// tiles that some row does not see whole, NaN codes go into the product as zeros;
+// where there were any, the rows that do see them get their NaN at the end.
+// 0x80 in each byte of w that is a NaN code (0x7f or 0xff):
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ uint32_t without_nan(uint32_t w, uint32_t nan) { return w & ~((nan >> 7) * 0xffu); }
 
 // Elements d..d+3 of a finished row: acc / total, 0 and -inf where it sees no key.
 template <bool BF16>

@@ -169,6 +169,7 @@ __global__ __launch_bounds__(kWaves * kWave, 1) void k_attn_rows(AttnCall a) {
         load_v(0);
     }
     const float c = a.scale_log2;
+    uint32_t saw_nan = 0;
     for (int step = 0; step < steps; ++step) {
         const int kb = k0 + (step * kWaves + wave) * kBlock;
         f32x4_t sc[NR][4];
@@ -193,7 +194,6 @@ __global__ __launch_bounds__(kWaves * kWave, 1) void k_attn_rows(AttnCall a) {
         if (step + 1 < steps) load_k(step + 1);
 
         const bool masked = kb < all_lo || kb + kBlock > all_hi;
-        bool nan = false;
         if (masked) {
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr)
@@ -204,8 +204,7 @@ __global__ __launch_bounds__(kWaves * kWave, 1) void k_attn_rows(AttnCall a) {
                         const int key = kb + 16 * t + 4 * g4 + i;
                         if (key < lo[nr] || key >= hi[nr]) sc[nr][t][i] = -__builtin_inff();
                     }
-            // keys that no row sees may hold anything; those that some rows do
-            // not see must not reach them through 0 * NaN
+            // keys that no row sees may hold anything
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -215,10 +214,11 @@ __global__ __launch_bounds__(kWaves * kWave, 1) void k_attn_rows(AttnCall a) {
 #pragma unroll
                     for (int w = 0; w < W; ++w) {
                         vreg[t][i][w] = any ? vreg[t][i][w] : 0;
-                        nan |= has_nan(vreg[t][i][w]);
+                        const uint32_t nan = nan_bytes(vreg[t][i][w]);
+                        vreg[t][i][w] = without_nan(vreg[t][i][w], nan);
+                        saw_nan |= nan;
                     }
                 }
-            nan = __any(nan);
         }
         bf16x8_t p[NR][2][NS];
 #pragma unroll
@@ -269,24 +269,8 @@ __global__ __launch_bounds__(kWaves * kWave, 1) void k_attn_rows(AttnCall a) {
                 transpose4(in, y);
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                    bf16x8_t v = codes_to_bf16(x[b], y[b], va, vb);
+                    const bf16x8_t v = codes_to_bf16(x[b], y[b], va, vb);
                     const int u = 4 * w + b;
-                    if (nan) {
-                        const bf16x8_t where = take_nan(v);
-#pragma unroll
-                        for (int nr = 0; nr < NR; ++nr) {
-                            bf16x8_t seen;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const int key = kb + 32 * t2 + 16 * (i / 4) + 4 * g4 + (i & 3);
-                                seen[i] = key >= lo[nr] && key < hi[nr] ? (__bf16)1.0f : (__bf16)0.0f;
-                            }
-                            const f32x4_t n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(where, seen, f32x4_t{0, 0, 0, 0}, 0, 0, 0);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (n[i] > 0.0f) o[nr][u][i] = __builtin_nanf("");
-                        }
-                    }
 #pragma unroll
                     for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
@@ -296,6 +280,30 @@ __global__ __launch_bounds__(kWaves * kWave, 1) void k_attn_rows(AttnCall a) {
             }
         }
         if (step + 1 < steps) load_v(step + 1);
+    }
+
+    if (__any(saw_nan != 0)) {
+        for (int step = 0; step < steps; ++step) {
+            const int kb = k0 + (step * kWaves + wave) * kBlock;
+            if (kb >= all_lo && kb + kBlock <= all_hi) continue;
+            for (int j = kb; j < kb + kBlock && j < any_hi; ++j) {
+                const int page = page_of(a, r, j);
+                const uint8_t* p = a.v_codes +
+                    ((((int64_t)page * a.n_kv + head) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * D;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int w = 0; w < W; ++w) {
+                        const uint32_t nan = nan_bytes(*reinterpret_cast<const uint32_t*>(p + (4 * g4 + i) * U + 4 * w));
+#pragma unroll
+                        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                            for (int b = 0; b < 4; ++b)
+                                if (j >= lo[nr] && j < hi[nr] && (nan >> (8 * b + 7) & 1))
+                                    o[nr][4 * w + b][i] = __builtin_nanf("");
+                    }
+            }
+        }
     }
 
     // the four waves' parts, joined in LDS
