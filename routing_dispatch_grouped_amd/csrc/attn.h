@@ -9,6 +9,10 @@ typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 constexpr float kLn2 = 0.6931471805599453f;
+// The running maximum is raised only when a row outgrows it by more than this
+// (base-2 exponent): probabilities then reach 2^8 instead of 1, at the same
+// relative precision, and the output is rescaled a few times instead of at most tiles.
+constexpr float kSlack = 8.0f;
 
 // A request's queries and keys.  Query i has position kv - n + i.
 struct ReqSpan {

@@ -231,7 +231,7 @@ __global__ __launch_bounds__(kWaves * kWave, 1) void k_attn_rows(AttnCall a) {
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
             const float m_new = fmaxf(m[nr], top * c);
-            if (__any(m_new > m[nr])) {
+            if (__any(m_new > m[nr] + kSlack)) {
                 const float shrink = __builtin_amdgcn_exp2f(m[nr] - (m_new == -__builtin_inff() ? 0.0f : m_new));
                 l[nr] *= shrink;
 #pragma unroll

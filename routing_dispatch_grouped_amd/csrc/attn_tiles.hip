@@ -35,20 +35,29 @@ struct TileLds {
     int nan;  // whether a masked tile's V held NaN
 };
 
-// Swizzles: the 16-byte piece that holds piece c of a K row / of a V^T row.
-__device__ __forceinline__ int k_piece(int key, int c) { return c ^ (key & 7); }
-__device__ __forceinline__ int v_piece(int d, int c) { return c ^ ((d & 7) ^ ((d >> 3) & 3)); }
+// Barrier for LDS alone: loads from memory stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    __builtin_amdgcn_sched_barrier(0);
+}
 
-template <int D, int NW>
+// Swizzles: the 16-byte piece that holds piece c of a K row / of a V^T row.
+template <int D>
+__device__ __forceinline__ int k_piece(int key, int c) {
+    return c ^ (D == 64 ? (key >> 1) & 7 : key & 15);
+}
+__device__ __forceinline__ int v_piece(int d, int c) { return c ^ (((d >> 1) & 7) ^ ((d >> 4) & 1)); }
+
+template <int D, int NW, int RB>
 __global__ __launch_bounds__(NW * kWave, 1) void k_attn_tiles(AttnCall a) {
-    constexpr int BM = 32 * NW;
+    constexpr int NT = NW * kWave, BM = 32 * RB * NW;
     constexpr int KS = D / 16, DB = D / 32;  // reduction steps of S^T, 32-row blocks of O^T
-    // Staging: the first half of the waves loads V, the second K.
-    constexpr int HT = NW / 2 * kWave;
-    constexpr int KU = kTile * D / 16 / HT;  // 16-code K units per thread
-    constexpr int VU = 8 * D / 4 / HT > 0 ? 8 * D / 4 / HT : 1;  // (8 keys x 4 columns) V units per thread
-    constexpr bool kAllV = 8 * D / 4 >= HT;
-    constexpr int RAW = 4 * KU > 8 * VU ? 4 * KU : 8 * VU;
+    // Staging, per thread: KU pieces of 16 K codes, VU of 8 keys x 4 columns of V.
+    constexpr int KP = kTile * D / 16, VP = 8 * D / 4;
+    constexpr int KU = (KP + NT - 1) / NT, VU = (VP + NT - 1) / NT;
     extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
     auto& lds = *reinterpret_cast<TileLds<D>*>(lds_raw);
 
@@ -85,261 +94,322 @@ __global__ __launch_bounds__(NW * kWave, 1) void k_attn_tiles(AttnCall a) {
     const int k1 = any_hi < k0 + a.tile_chunk ? any_hi : k0 + a.tile_chunk;
     const int tiles = k1 > k0 ? (k1 - k0 + kTile - 1) / kTile : 0;
 
-    // this wave's rows: one per lane of either half
-    const int first = row0 + wave * 32, row = first + col;
-    const int row_c = row < rows ? row : rows - 1;
-    const int lo = key_lo(a, s, row_c / G), hi = key_hi(a, s, row_c / G);
-    const int i0 = (first < rows ? first : rows - 1) / G, i1 = (first + 31 < rows ? first + 31 : rows - 1) / G;
-    const int all_lo = key_lo(a, s, i1), all_hi = key_hi(a, s, i0);
-    bf16x8_t q[KS];
-    {
-        const uint16_t* p = static_cast<const uint16_t*>(a.q) + (int64_t)(s.t0 + row_c / G) * a.q_stride +
-                            (int64_t)(head * G + row_c % G) * D + 8 * half;
+    // this wave's rows: RB blocks of 32, one row per lane of either half
+    int lo[RB], hi[RB], all_lo[RB], all_hi[RB];
+    bf16x8_t q[RB][KS];
 #pragma unroll
-        for (int x = 0; x < KS; ++x) q[x] = *reinterpret_cast<const bf16x8_t*>(p + 16 * x);
+    for (int rb = 0; rb < RB; ++rb) {
+        const int first = row0 + (wave * RB + rb) * 32, row = first + col;
+        const int i = (row < rows ? row : rows - 1) / G, h = head * G + (row < rows ? row : rows - 1) % G;
+        lo[rb] = key_lo(a, s, i);
+        hi[rb] = key_hi(a, s, i);
+        all_lo[rb] = key_lo(a, s, (first + 31 < rows ? first + 31 : rows - 1) / G);
+        all_hi[rb] = key_hi(a, s, (first < rows ? first : rows - 1) / G);
+        const uint16_t* p = static_cast<const uint16_t*>(a.q) + (int64_t)(s.t0 + i) * a.q_stride + (int64_t)h * D + 8 * half;
+#pragma unroll
+        for (int x = 0; x < KS; ++x) q[rb][x] = *reinterpret_cast<const bf16x8_t*>(p + 16 * x);
     }
 
     // pages and scales of 16-key groups: lane l holds group 64 b + l of this chunk
-    const bool stage_v = wave < NW / 2;
-    const int st = tid - (stage_v ? 0 : HT);  // place among the threads that stage this operand
-    const uint8_t* codes = stage_v ? a.v_codes : a.k_codes;
-    const float* scales = stage_v ? a.v_scale : a.k_scale;
     int page = 0;
-    float page_scale = 1.0f;
+    float ks = 1.0f, vs = 1.0f;
     const auto load_pages = [&](int b) {
         const int key = k0 + (b * kWave + lane) * 16;
-        page = 0;
-        page_scale = 1.0f;
+        page = 0;  // past the last key: page 0, whose codes are not used
+        ks = vs = 1.0f;
         if (key < k1) {
             page = page_of(a, r, key);
-            page_scale = pow2_scale(scales[(int64_t)page * a.n_kv + head]);
+            ks = pow2_scale(a.k_scale[(int64_t)page * a.n_kv + head]);
+            vs = pow2_scale(a.v_scale[(int64_t)page * a.n_kv + head]);
         }
     };
     const int in_page = (1 << a.page_shift) - 1;
-    // first code of key `key` of this chunk's 16-key group g, and its scale
-    const auto group_row = [&](int g, int key) -> const uint8_t* {
+    const auto row_at = [&](const uint8_t* codes, int g, int key) -> const uint8_t* {
         const int pg = __shfl(page, g & (kWave - 1));
         return codes + ((((int64_t)pg * a.n_kv + head) << a.page_shift) + (key & in_page)) * D;
     };
-    uint32_t raw[RAW];
-    float raw_scale[KU > VU ? KU : VU];
-    const auto load_tile = [&](int t) {  // V waves: tile t; K waves: tile t
-        const int t0 = k0 + t * kTile;
-        if (stage_v) {
-#pragma unroll
-            for (int u = 0; u < VU; ++u) {
-                const int x = st + u * HT, c = (x / (D / 4)) & 7, dq = x % (D / 4);
-                raw_scale[u] = __shfl(page_scale, (t * 4 + c / 2) & (kWave - 1));
-                const uint8_t* p = group_row(t * 4 + c / 2, t0 + 16 * (c / 2) + 4 * (c & 1)) + 4 * dq;
-                if (kAllV || x < 8 * D / 4) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        raw[8 * u + i] = *reinterpret_cast<const uint32_t*>(p + (8 * (i / 4) + (i & 3)) * D);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int u = 0; u < KU; ++u) {
-                const int x = st + u * HT, key = x / (D / 16), c = x % (D / 16);
-                raw_scale[u] = __shfl(page_scale, (t * 4 + key / 16) & (kWave - 1));
-                const uint4 w = *reinterpret_cast<const uint4*>(group_row(t * 4 + key / 16, t0 + key) + 16 * c);
-                raw[4 * u] = w.x, raw[4 * u + 1] = w.y, raw[4 * u + 2] = w.z, raw[4 * u + 3] = w.w;
-            }
-        }
-    };
-    const auto store_tile = [&](int t, uint16_t* to_k, uint16_t* to_v) {
-        if (stage_v) {
-            const int t0 = k0 + t * kTile;
-            const bool masked = t0 < wg_all_lo || t0 + kTile > wg_all_hi;
-            uint32_t saw = 0;
-#pragma unroll
-            for (int u = 0; u < VU; ++u) {
-                const int x = st + u * HT, c = (x / (D / 4)) & 7, dq = x % (D / 4);
-                if (kAllV || x < 8 * D / 4) {
-                    if (masked) {
-                        // keys that no row sees may hold anything
-                        const int key = t0 + 16 * (c / 2) + 4 * (c & 1);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int j = key + 8 * (i / 4) + (i & 3);
-                            if (j < any_lo || j >= any_hi) raw[8 * u + i] = 0;
-                            const uint32_t nan = nan_bytes(raw[8 * u + i]);
-                            raw[8 * u + i] = without_nan(raw[8 * u + i], nan);
-                            saw |= nan;
-                        }
-                    }
-                    const uint32_t in0[4] = {raw[8 * u], raw[8 * u + 1], raw[8 * u + 2], raw[8 * u + 3]};
-                    const uint32_t in1[4] = {raw[8 * u + 4], raw[8 * u + 5], raw[8 * u + 6], raw[8 * u + 7]};
-                    uint32_t x0[4], x1[4];
-                    transpose4(in0, x0);
-                    transpose4(in1, x1);
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const int d = 4 * dq + b;
-                        *reinterpret_cast<bf16x8_t*>(to_v + d * kTile + 8 * v_piece(d, c)) =
-                            codes_to_bf16(x0[b], x1[b], raw_scale[u], raw_scale[u]);
-                    }
-                }
-            }
-            if (saw) lds.nan = 1;
-        } else {
-#pragma unroll
-            for (int u = 0; u < KU; ++u) {
-                const int x = st + u * HT, key = x / (D / 16), c = x % (D / 16);
-                uint16_t* to = to_k + key * D;
-                *reinterpret_cast<bf16x8_t*>(to + 8 * k_piece(key, 2 * c)) =
-                    codes_to_bf16(raw[4 * u], raw[4 * u + 1], raw_scale[u], raw_scale[u]);
-                *reinterpret_cast<bf16x8_t*>(to + 8 * k_piece(key, 2 * c + 1)) =
-                    codes_to_bf16(raw[4 * u + 2], raw[4 * u + 3], raw_scale[u], raw_scale[u]);
-            }
-        }
-    };
-    // What a wave has staged: K waves run one tile ahead of V waves.
-    const int ahead = stage_v ? 0 : 1;
+    uint4 kraw[KU];
+    uint32_t vraw[VU][8];
+    float kscale[KU], vscale[VU];
+    // Loads of one step: V of tile t - 1, then K of tile t, whose pages may be the next set.
     const auto fetch = [&](int t) {
-        if (t < tiles) {
-            if ((t & 15) == 0) load_pages(t / 16);
-            load_tile(t);
+#pragma unroll
+        for (int u = 0; u < VU; ++u) {
+            const int x = tid + u * NT, c = (x / (D / 4)) & 7, dq = x % (D / 4), g = (t - 1) * 4 + c / 2;
+            vscale[u] = __shfl(vs, g & (kWave - 1));
+            const uint8_t* p = row_at(a.v_codes, g, k0 + (t - 1) * kTile + 16 * (c / 2) + 4 * (c & 1)) + 4 * dq;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) vraw[u][i] = *reinterpret_cast<const uint32_t*>(p + (8 * (i / 4) + (i & 3)) * D);
+        }
+        if ((t & 15) == 0) load_pages(t / 16);
+#pragma unroll
+        for (int u = 0; u < KU; ++u) {
+            const int x = tid + u * NT, key = (x / (D / 16)) & (kTile - 1), c = x % (D / 16), g = t * 4 + key / 16;
+            kscale[u] = __shfl(ks, g & (kWave - 1));
+            kraw[u] = *reinterpret_cast<const uint4*>(row_at(a.k_codes, g, k0 + t * kTile + key) + 16 * c);
+        }
+    };
+    // V codes of tile t before their conversion: keys that no row sees may hold
+    // anything, and a NaN that only some see is kept out of the product.
+    const auto clean = [&](int t) {
+        const int t0 = k0 + t * kTile;
+        if (t0 >= wg_all_lo && t0 + kTile <= wg_all_hi) return;
+        uint32_t saw = 0;
+#pragma unroll
+        for (int u = 0; u < VU; ++u) {
+            const int x = tid + u * NT, c = (x / (D / 4)) & 7, key = t0 + 16 * (c / 2) + 4 * (c & 1);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int j = key + 8 * (i / 4) + (i & 3);
+                if (j < any_lo || j >= any_hi) vraw[u][i] = 0;
+                const uint32_t nan = nan_bytes(vraw[u][i]);
+                vraw[u][i] = without_nan(vraw[u][i], nan);
+                saw |= nan;
+            }
+        }
+        if (saw) lds.nan = 1;
+    };
+    const auto stage_k = [&](uint16_t* to_k, int u, int part) {  // half of K unit u
+        const int x = tid + u * NT, key = (x / (D / 16)) & (kTile - 1), c = x % (D / 16);
+        if (KP % NT == 0 || x < KP)
+            *reinterpret_cast<bf16x8_t*>(to_k + key * D + 8 * k_piece<D>(key, 2 * c + part)) =
+                part == 0 ? codes_to_bf16(kraw[u].x, kraw[u].y, kscale[u], kscale[u])
+                          : codes_to_bf16(kraw[u].z, kraw[u].w, kscale[u], kscale[u]);
+    };
+    const auto stage_v = [&](uint16_t* to_v, int u) {
+        const int x = tid + u * NT, c = (x / (D / 4)) & 7, dq = x % (D / 4);
+        const uint32_t in0[4] = {vraw[u][0], vraw[u][1], vraw[u][2], vraw[u][3]};
+        const uint32_t in1[4] = {vraw[u][4], vraw[u][5], vraw[u][6], vraw[u][7]};
+        uint32_t x0[4], x1[4];
+        transpose4(in0, x0);
+        transpose4(in1, x1);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int d = 4 * dq + b;
+            if (VP % NT == 0 || x < VP)
+                *reinterpret_cast<bf16x8_t*>(to_v + d * kTile + 8 * v_piece(d, c)) =
+                    codes_to_bf16(x0[b], x1[b], vscale[u], vscale[u]);
         }
     };
 
-    f32x16_t o[DB];
-    float m = -__builtin_inff(), l = 0.0f;
+    f32x16_t o[RB][DB];
+    float m[RB], l[RB];
 #pragma unroll
-    for (int db = 0; db < DB; ++db)
+    for (int rb = 0; rb < RB; ++rb) {
+        m[rb] = -__builtin_inff();
+        l[rb] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[db][i] = 0.0f;
+        for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[rb][db][i] = 0.0f;
+    }
     const float scale = a.scale_log2;
 
     // LDS places of this lane's operand pieces: the swizzle touches only the low
-    // three bits of a piece's number, so four of each, the rest are offsets.
-    int k_at[4], v_at[4];
+    // bits of a piece's number, so a few places and offsets give them all.
+    constexpr int KA = D == 64 ? 4 : 8;
+    int k_at[KA], v_at[4];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-        k_at[x] = col * D + 8 * k_piece(col, 2 * x + half);
-        v_at[x] = col * kTile + 8 * v_piece(col, 2 * x + half);
-    }
-    // operand y of the logits of keys 32 kb ..
+    for (int x = 0; x < KA; ++x) k_at[x] = col * D + 8 * k_piece<D>(col, 2 * x + half);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) v_at[x] = col * kTile + 8 * v_piece(col, 2 * x + half);
+    // operand y of the logits of keys 32 kb .., operand x of output block db
     const auto k_frag = [&](const uint16_t* k, int kb, int y) {
-        return *reinterpret_cast<const bf16x8_t*>(k + k_at[y & 3] + kb * 32 * D + (y / 4) * 64);
+        return *reinterpret_cast<const bf16x8_t*>(k + k_at[y % KA] + kb * 32 * D + (y / KA) * KA * 16);
     };
     const auto v_frag = [&](const uint16_t* v, int db, int x) {
         return *reinterpret_cast<const bf16x8_t*>(v + v_at[x] + db * 32 * kTile);
     };
-    const auto logits = [&](f32x16_t (&sc)[2], const uint16_t* k) {
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) sc[kb][i] = 0.0f;
-#pragma unroll
-            for (int y = 0; y < KS; ++y)
-                sc[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k_frag(k, kb, y), q[y], sc[kb], 0, 0, 0);
-        }
-    };
-    // One tile: its softmax beside the next tile's logits, then its V product.
-    const auto tile = [&](f32x16_t (&sc)[2], f32x16_t (&next)[2], int t, auto parity) {
-        constexpr int B = decltype(parity)::value;
-        const uint16_t *k_next = lds.k[1 - B], *v_now = lds.v[B];
+    // A tile's logits: what the mask hides, then the largest of each row.
+    const auto mask = [&](f32x16_t (&sc)[RB][2], int t) {
         const int t0 = k0 + t * kTile;
-        fetch(t + 1 + ahead);
-        if (t0 < all_lo || t0 + kTile > all_hi) {
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+            if (t0 >= all_lo[rb] && t0 + kTile <= all_hi[rb]) continue;
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int key = t0 + kb * 32 + 8 * (i / 4) + 4 * half + (i & 3);
-                    if (key < lo || key >= hi) sc[kb][i] = -__builtin_inff();
+                    if (key < lo[rb] || key >= hi[rb]) sc[rb][kb][i] = -__builtin_inff();
                 }
         }
-        // eight groups of KG products and four exponentials, operands one group ahead
-        constexpr int KG = KS / 4;
-        bf16x8_t kf[KG];
-#pragma unroll
-        for (int x = 0; x < KG; ++x) kf[x] = k_frag(k_next, 0, x);
+    };
+    const auto row_top = [&](f32x16_t (&sc)[RB][2], int rb) {
         float top = -__builtin_inff();
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[kb][i]);
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float m_new = fmaxf(m, top * scale);
-        if (__any(m_new > m)) {
-            const float shrink = __builtin_amdgcn_exp2f(m - (m_new == -__builtin_inff() ? 0.0f : m_new));
-            l *= shrink;
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[rb][kb][i]);
+        return fmaxf(top, __shfl_xor(top, 32)) * scale;
+    };
+    const auto raise = [&](const float (&top)[RB]) {
+        bool grows = false;
 #pragma unroll
-            for (int db = 0; db < DB; ++db) o[db] *= shrink;
-            m = m_new;
-        }
-        const float ref = m == -__builtin_inff() ? 0.0f : m;
-        float sum = 0.0f;
-        bf16x8_t p[4], vf[2];
+        for (int rb = 0; rb < RB; ++rb) grows |= top[rb] > m[rb] + kSlack;
+        if (__any(grows)) {
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-            __builtin_amdgcn_sched_barrier(0);
-            const int kb = g / 4, y0 = (g & 3) * KG;
-            if ((g & 3) == 0)
+            for (int rb = 0; rb < RB; ++rb) {
+                const float m_new = fmaxf(m[rb], top[rb]);
+                const float shrink = __builtin_amdgcn_exp2f(m[rb] - (m_new == -__builtin_inff() ? 0.0f : m_new));
+                l[rb] *= shrink;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) next[kb][i] = 0.0f;
-            bf16x8_t ahead_f[KG];
-            if (g < 7) {
-#pragma unroll
-                for (int x = 0; x < KG; ++x) ahead_f[x] = k_frag(k_next, (g + 1) / 4, ((g + 1) & 3) * KG + x);
-            } else {
-                vf[0] = v_frag(v_now, 0, 0);
-                vf[1] = v_frag(v_now, 0, 1);
-            }
-            // past the last tile: of an old buffer, not used
-#pragma unroll
-            for (int x = 0; x < KG; ++x)
-                next[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[x], q[y0 + x], next[kb], 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float e = __builtin_amdgcn_exp2f(fmaf(sc[kb][4 * (g & 3) + i], scale, -ref));
-                sum += e;
-                p[g / 2][4 * (g & 1) + i] = (__bf16)e;
-            }
-            // summed here and not behind the loop, where 32 exponentials would have to be kept
-            asm volatile("" : "+v"(sum));
-            if (g < 7) {
-#pragma unroll
-                for (int x = 0; x < KG; ++x) kf[x] = ahead_f[x];
+                for (int db = 0; db < DB; ++db) o[rb][db] *= shrink;
+                m[rb] = m_new;
             }
         }
-        l += sum;
+    };
+    // One tile: its probabilities beside the next tile's logits; then its V product
+    // beside the next maximum and the staging of K(t + 2) and V(t + 1).
+    const auto tile = [&](f32x16_t (&sc)[RB][2], f32x16_t (&next)[RB][2], int t, auto parity) {
+        constexpr int B = decltype(parity)::value;
+        constexpr int KG = KS / 4;
+        const uint16_t *k_next = lds.k[1 - B], *v_now = lds.v[B];
+        bf16x8_t p[RB][4];
+        float sum[RB], ref[RB];
 #pragma unroll
-        for (int g = 0; g < 2 * DB; ++g) {
+        for (int rb = 0; rb < RB; ++rb) {
+            sum[rb] = 0.0f;
+            ref[rb] = m[rb] == -__builtin_inff() ? 0.0f : m[rb];
+        }
+        __builtin_amdgcn_s_setprio(1);
+        // Nine steps: the products of group g - 1, with their operands read two
+        // steps before, beside the exponentials of group g.
+        bf16x8_t kf[3][KG], vf[4][2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int x = 0; x < KG; ++x) kf[g][x] = k_frag(k_next, 0, g * KG + x);
+#pragma unroll
+        for (int g = 0; g < 9; ++g) {
             __builtin_amdgcn_sched_barrier(0);
-            bf16x8_t f0, f1;
-            if (g + 1 < 2 * DB) {
-                f0 = v_frag(v_now, (g + 1) / 2, 2 * ((g + 1) & 1));
-                f1 = v_frag(v_now, (g + 1) / 2, 2 * ((g + 1) & 1) + 1);
+            if (g > 0) {
+                const int w = g - 1, kb = w / 4;
+                if (g + 1 < 8) {
+#pragma unroll
+                    for (int x = 0; x < KG; ++x) kf[(g + 1) % 3][x] = k_frag(k_next, (g + 1) / 4, ((g + 1) & 3) * KG + x);
+                } else {
+                    vf[g - 7][0] = v_frag(v_now, 0, 2 * (g - 7));
+                    vf[g - 7][1] = v_frag(v_now, 0, 2 * (g - 7) + 1);
+                }
+                // past the last tile: of an old buffer, not used
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb) {
+                    if ((w & 3) == 0)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) next[rb][kb][i] = 0.0f;
+                }
+#pragma unroll
+                for (int x = 0; x < KG; ++x)
+#pragma unroll
+                    for (int rb = 0; rb < RB; ++rb)
+                        next[rb][kb] =
+                            __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[w % 3][x], q[rb][(w & 3) * KG + x], next[rb][kb], 0, 0, 0);
             }
-            o[g / 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[0], p[2 * (g & 1)], o[g / 2], 0, 0, 0);
-            o[g / 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[1], p[2 * (g & 1) + 1], o[g / 2], 0, 0, 0);
-            if (g + 1 < 2 * DB) vf[0] = f0, vf[1] = f1;
+            if (g < 8) {
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float e = __builtin_amdgcn_exp2f(fmaf(sc[rb][g / 4][4 * (g & 3) + i], scale, -ref[rb]));
+                        sum[rb] += e;
+                        p[rb][g / 2][4 * (g & 1) + i] = (__bf16)e;
+                    }
+                    // summed here and not behind the loop, where all the exponentials would have to be kept
+                    asm volatile("" : "+v"(sum[rb]));
+                }
+            }
         }
         __builtin_amdgcn_sched_barrier(0);
-        // K waves: into the buffer that this tile's logits came from
-        if (t + 1 + ahead < tiles) store_tile(t + 1 + ahead, lds.k[B], lds.v[1 - B]);
-        __syncthreads();
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) l[rb] += sum[rb];
+        if (t + 1 < tiles) {
+            mask(next, t + 1);
+            clean(t + 1);
+        }
+        __builtin_amdgcn_s_setprio(0);
+        float top[RB];
+        constexpr int G2 = 2 * DB;
+#pragma unroll
+        for (int g = 0; g < G2; ++g) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (g + 2 < G2) {
+                vf[(g + 2) & 3][0] = v_frag(v_now, (g + 2) / 2, 2 * (g & 1));
+                vf[(g + 2) & 3][1] = v_frag(v_now, (g + 2) / 2, 2 * (g & 1) + 1);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb)
+                    o[rb][g / 2] =
+                        __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[g & 3][x], p[rb][2 * (g & 1) + x], o[rb][g / 2], 0, 0, 0);
+            // staged past the last tile: never read
+#pragma unroll
+            for (int u = 0; u < VU; ++u)
+                if (g == u % G2) stage_v(lds.v[1 - B], u);
+#pragma unroll
+            for (int u = 0; u < KU; ++u)
+                if (g == (1 + u) % G2) {
+                    stage_k(lds.k[B], u, 0);
+                    stage_k(lds.k[B], u, 1);
+                }
+            if (g == G2 - 1)
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb) top[rb] = row_top(next, rb);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (t + 1 < tiles) raise(top);
+        fetch(t + 3);
+        lds_barrier();
     };
 
     if (tid == 0) lds.nan = 0;
     __syncthreads();
-    fetch(0);
-    if (tiles > 0) store_tile(0, lds.k[0], lds.v[0]);
-    if (!stage_v) {
-        fetch(1);
-        if (tiles > 1) store_tile(1, lds.k[1], lds.v[1]);
-    }
-    __syncthreads();
     if (tiles > 0) {
-        f32x16_t s0[2], s1[2];
-        logits(s0, lds.k[0]);
-        __syncthreads();  // the first tile's buffer takes the third tile
-        for (int t = 0; t < tiles; t += 2) {
+        f32x16_t s0[RB][2], s1[RB][2];
+        float top[RB];
+        load_pages(0);
+        const auto fill = [&](int t, uint16_t* to_k, uint16_t* to_v) {
+            if (to_v) clean(t - 1);
+#pragma unroll
+            for (int u = 0; u < VU; ++u)
+                if (to_v) stage_v(to_v, u);
+#pragma unroll
+            for (int u = 0; u < KU; ++u) {
+                stage_k(to_k, u, 0);
+                stage_k(to_k, u, 1);
+            }
+        };
+        fetch(0);
+        fill(0, lds.k[0], nullptr);
+        fetch(1);
+        fill(1, lds.k[1], lds.v[0]);
+        fetch(2);
+        lds_barrier();
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s0[rb][kb][i] = 0.0f;
+#pragma unroll
+            for (int y = 0; y < KS; ++y) {
+                const bf16x8_t f = k_frag(lds.k[0], kb, y);
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb)
+                    s0[rb][kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[rb][y], s0[rb][kb], 0, 0, 0);
+            }
+        }
+        mask(s0, 0);
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) top[rb] = row_top(s0, rb);
+        raise(top);
+        lds_barrier();  // the first tile's K buffer takes the third tile
+        for (int t = 0;;) {
             tile(s0, s1, t, std::integral_constant<int, 0>{});
-            if (t + 1 < tiles) tile(s1, s0, t + 1, std::integral_constant<int, 1>{});
+            if (++t >= tiles) break;
+            tile(s1, s0, t, std::integral_constant<int, 1>{});
+            if (++t >= tiles) break;
         }
     }
 
@@ -350,45 +420,54 @@ __global__ __launch_bounds__(NW * kWave, 1) void k_attn_tiles(AttnCall a) {
             for (int j = t0; j < t0 + kTile && j < any_hi; ++j) {
                 const int pg = page_of(a, r, j);
                 const uint8_t* p = a.v_codes + ((((int64_t)pg * a.n_kv + head) << a.page_shift) + (j & in_page)) * D;
-                if (j < lo || j >= hi) continue;
 #pragma unroll
-                for (int db = 0; db < DB; ++db)
+                for (int rb = 0; rb < RB; ++rb) {
+                    if (j < lo[rb] || j >= hi[rb]) continue;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if ((p[db * 32 + 8 * (i / 4) + 4 * half + (i & 3)] & 0x7f) == 0x7f) o[db][i] = __builtin_nanf("");
+                    for (int db = 0; db < DB; ++db)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if ((p[db * 32 + 8 * (i / 4) + 4 * half + (i & 3)] & 0x7f) == 0x7f)
+                                o[rb][db][i] = __builtin_nanf("");
+                }
             }
         }
     }
 
-    const float total = l + __shfl_xor(l, 32);
-    if (row >= rows) return;
-    const int i = row / G, h = head * G + row % G;
-    const bool none = hi <= lo;
-    const int64_t at = ((int64_t)(s.t0 + i) * a.n_q + h) * a.max_chunks + chunk;
-    if (keys.chunks > 1 && half == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(m, total);
 #pragma unroll
-    for (int db = 0; db < DB; ++db)
+    for (int rb = 0; rb < RB; ++rb) {
+        const int row = row0 + (wave * RB + rb) * 32 + col;
+        const float total = l[rb] + __shfl_xor(l[rb], 32);
+        if (row >= rows) continue;
+        const int i = row / G, h = head * G + row % G;
+        const bool none = hi[rb] <= lo[rb];
+        const int64_t at = ((int64_t)(s.t0 + i) * a.n_q + h) * a.max_chunks + chunk;
+        if (keys.chunks > 1 && half == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(m[rb], total);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int d = db * 32 + 8 * j + 4 * half;
-            const float4 v = make_float4(o[db][4 * j], o[db][4 * j + 1], o[db][4 * j + 2], o[db][4 * j + 3]);
-            if (keys.chunks == 1) store_part<true>(a, s.t0 + i, h, d, D, v, total, m, none);
-            else *reinterpret_cast<float4*>(a.part_o + at * D + d) = v;
-        }
+        for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int d = db * 32 + 8 * j + 4 * half;
+                const float4 v =
+                    make_float4(o[rb][db][4 * j], o[rb][db][4 * j + 1], o[rb][db][4 * j + 2], o[rb][db][4 * j + 3]);
+                if (keys.chunks == 1) store_part<true>(a, s.t0 + i, h, d, D, v, total, m[rb], none);
+                else *reinterpret_cast<float4*>(a.part_o + at * D + d) = v;
+            }
+    }
 }
 
-template <int D, int NW>
+template <int D, int NW, int RB>
 hipError_t launch(const AttnCall& a, hipStream_t s) {
     constexpr size_t bytes = sizeof(TileLds<D>);
     static_assert(bytes <= 160 * 1024, "LDS");
     const int64_t grid = (int64_t)a.n_kv * a.tile_slots * a.tile_chunks;
     if (grid >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;
     if (bytes > 64 * 1024) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attn_tiles<D, NW>),
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attn_tiles<D, NW, RB>),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
         if (e != hipSuccess) return e;
     }
-    k_attn_tiles<D, NW><<<(unsigned)grid, NW * kWave, bytes, s>>>(a);
+    k_attn_tiles<D, NW, RB><<<(unsigned)grid, NW * kWave, bytes, s>>>(a);
     return hipGetLastError();
 }
 
@@ -397,9 +476,9 @@ hipError_t launch(const AttnCall& a, hipStream_t s) {
 // a.tile_rows = attn_tile_rows(head_dim)
 hipError_t launch_attn_tiles(const AttnCall& a, int head_dim, hipStream_t s) {
     switch (head_dim) {
-        case 64: return launch<64, 8>(a, s);
-        case 128: return launch<128, 8>(a, s);
-        default: return launch<256, 4>(a, s);
+        case 64: return launch<64, 8, 1>(a, s);
+        case 128: return launch<128, 8, 1>(a, s);
+        default: return launch<256, 4, 1>(a, s);
     }
 }
 
