@@ -114,6 +114,26 @@ def _check(rc, what):
         raise RdgError(rc, what)
 
 
+_torch = None
+
+
+def _torch_module():
+    """torch, imported once: the small calls of a decode step are timed by their host side."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _raw_stream(stream):
+    """The HIP stream as an integer (None: torch's current one)."""
+    if stream is not None:
+        return stream.cuda_stream
+    c = _torch_module()._C
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+
+
 # ------------------------------------------------------------------ layout
 class Layout:
     """Device buffers of an rdg_layout, allocated with torch on ``device``."""
@@ -147,13 +167,13 @@ class Layout:
         return ctypes.byref(self.c)
 
 
-def _tensor(t, what, dtype, *shape):
-    """Refuse a tensor that the C call would read wrongly: another element type
-    or size than the call assumes, or not contiguous."""
-    if t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != shape:
+def _tensor(t, what, dtype, shape):
+    """The address of a tensor that the C call reads as it is: refuses another
+    element type or size than the call assumes, and one that is not contiguous."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise RdgError(RDG_EINVAL, "%s: want a contiguous %s tensor of shape %s, got %s %s" %
                        (what, dtype, list(shape), t.dtype, list(t.shape)))
-    return t
+    return t.data_ptr()
 
 
 class KvCache:
@@ -165,13 +185,13 @@ class KvCache:
         if k.dim() != 4:
             raise RdgError(RDG_EINVAL, "KvCache: k has to be [n_pages, n_kv, page_rows, head_dim]")
         n_pages, n_kv, page_rows, head_dim = k.shape
-        self.k = _tensor(k, "KvCache.k", torch.uint8, *k.shape)
-        self.v = _tensor(v, "KvCache.v", torch.uint8, *k.shape)
-        self.k_scale = _tensor(k_scale, "KvCache.k_scale", torch.float32, n_pages, n_kv)
-        self.v_scale = _tensor(v_scale, "KvCache.v_scale", torch.float32, n_pages, n_kv)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_pages, self.n_kv, self.page_rows, self.head_dim = n_pages, n_kv, page_rows, head_dim
-        self.c = rdg_kv_cache(n_pages, page_rows, n_kv, head_dim, k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
-                              v_scale.data_ptr())
+        self.c = rdg_kv_cache(n_pages, page_rows, n_kv, head_dim, _tensor(k, "KvCache.k", torch.uint8, k.shape),
+                              _tensor(v, "KvCache.v", torch.uint8, k.shape),
+                              _tensor(k_scale, "KvCache.k_scale", torch.float32, (n_pages, n_kv)),
+                              _tensor(v_scale, "KvCache.v_scale", torch.float32, (n_pages, n_kv)))
+        self.ref = ctypes.byref(self.c)
 
     @classmethod
     def empty(cls, n_pages, n_kv, page_rows, head_dim, device):
@@ -181,10 +201,6 @@ class KvCache:
         shape = (n_pages, n_kv, page_rows, head_dim)
         return cls(torch.zeros(shape, **code), torch.zeros(shape, **code), torch.ones(shape[:2], **scale),
                    torch.ones(shape[:2], **scale))
-
-    @property
-    def ref(self):
-        return ctypes.byref(self.c)
 
 
 class KvStep:
@@ -209,10 +225,7 @@ class KvStep:
                              self.cu_q.data_ptr(), self.kv_len.data_ptr(), self.slots.data_ptr(),
                              self.positions.data_ptr(), self.seg_tok.data_ptr(), self.status.data_ptr(),
                              self.work.data_ptr())
-
-    @property
-    def ref(self):
-        return ctypes.byref(self.c)
+        self.ref = ctypes.byref(self.c)
 
 
 # ------------------------------------------------------------------ entry points
@@ -381,66 +394,61 @@ def rdg_fill_i32(p, value, stream=None):
 
 def rdg_kv_plan(step, kv_len, q_len, free_list, n_free, n_free_out, stream=None):
     """kv_len, q_len [n_req], free_list [>= n_free], n_free, n_free_out [1]: int32 device tensors."""
-    import torch
-    i32, R = torch.int32, step.n_req
-    _tensor(kv_len, "rdg_kv_plan: kv_len", i32, R)
-    _tensor(q_len, "rdg_kv_plan: q_len", i32, R)
-    _tensor(free_list, "rdg_kv_plan: free_list", i32, free_list.numel())
-    _tensor(n_free, "rdg_kv_plan: n_free", i32, 1)
-    _tensor(n_free_out, "rdg_kv_plan: n_free_out", i32, 1)
-    _check(_lib.rdg_kv_plan(step.ref, _ptr(kv_len), _ptr(q_len), _ptr(free_list), _ptr(n_free), _ptr(n_free_out),
-                            _stream(stream)), "rdg_kv_plan")
+    i32, R = _torch_module().int32, (step.n_req,)
+    _check(_lib.rdg_kv_plan(step.ref, _tensor(kv_len, "rdg_kv_plan: kv_len", i32, R),
+                            _tensor(q_len, "rdg_kv_plan: q_len", i32, R),
+                            _tensor(free_list, "rdg_kv_plan: free_list", i32, (free_list.numel(),)),
+                            _tensor(n_free, "rdg_kv_plan: n_free", i32, (1,)),
+                            _tensor(n_free_out, "rdg_kv_plan: n_free_out", i32, (1,)), _raw_stream(stream)),
+           "rdg_kv_plan")
 
 
 def rdg_kv_trim(step, kv_len, new_len, free_list, n_free, n_free_out, stream=None):
     """kv_len, new_len [n_req], free_list [n_pages], n_free, n_free_out [1]: int32 device tensors."""
-    import torch
-    i32, R = torch.int32, step.n_req
-    _tensor(kv_len, "rdg_kv_trim: kv_len", i32, R)
-    _tensor(new_len, "rdg_kv_trim: new_len", i32, R)
-    _tensor(free_list, "rdg_kv_trim: free_list", i32, step.n_pages)
-    _tensor(n_free, "rdg_kv_trim: n_free", i32, 1)
-    _tensor(n_free_out, "rdg_kv_trim: n_free_out", i32, 1)
-    _check(_lib.rdg_kv_trim(step.ref, _ptr(kv_len), _ptr(new_len), _ptr(free_list), _ptr(n_free), _ptr(n_free_out),
-                            _stream(stream)), "rdg_kv_trim")
+    i32, R = _torch_module().int32, (step.n_req,)
+    _check(_lib.rdg_kv_trim(step.ref, _tensor(kv_len, "rdg_kv_trim: kv_len", i32, R),
+                            _tensor(new_len, "rdg_kv_trim: new_len", i32, R),
+                            _tensor(free_list, "rdg_kv_trim: free_list", i32, (step.n_pages,)),
+                            _tensor(n_free, "rdg_kv_trim: n_free", i32, (1,)),
+                            _tensor(n_free_out, "rdg_kv_trim: n_free_out", i32, (1,)), _raw_stream(stream)),
+           "rdg_kv_trim")
 
 
 def _rows(t, what, heads, head_dim):
     """dtype code and token stride of [T, heads * head_dim] or [T, heads, head_dim] rows; tokens may be apart."""
-    import torch
-    inner = (head_dim, 1) if t.dim() == 3 else (1,)
-    width = (heads, head_dim) if t.dim() == 3 else (heads * head_dim,)
-    code = {torch.bfloat16: RDG_BF16, torch.float32: RDG_F32}.get(t.dtype)
-    if code is None or tuple(t.shape[1:]) != width or tuple(t.stride()[1:]) != inner:
-        raise RdgError(RDG_EINVAL, "%s: want bfloat16 or float32 rows of %s, got %s %s with strides %s" %
-                       (what, list(width), t.dtype, list(t.shape), list(t.stride())))
-    return code, t.stride(0) if t.shape[0] > 1 else heads * head_dim
+    torch = _torch_module()
+    code = RDG_BF16 if t.dtype is torch.bfloat16 else RDG_F32 if t.dtype is torch.float32 else None
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        fits = shape[1] == heads and shape[2] == head_dim and stride[2] == 1 and (stride[1] == head_dim or heads == 1)
+    else:
+        fits = len(shape) == 2 and shape[1] == heads * head_dim and stride[1] == 1
+    if code is None or not fits:
+        raise RdgError(RDG_EINVAL, "%s: want bfloat16 or float32 rows of %d heads of %d, got %s %s with strides %s" %
+                       (what, heads, head_dim, t.dtype, list(shape), list(stride)))
+    return code, stride[0] if shape[0] > 1 else heads * head_dim
 
 
 def rdg_qk_norm_rope_store(qkv, n_q, n_kv, head_dim, q_weight, k_weight, eps, cos_sin, rot_dim, neighbours, step, cache,
                            q_out, stream=None):
     """qkv [T, (n_q + 2 n_kv) * head_dim] (token stride free), q_out [T, n_q, head_dim], weights [head_dim] float32
     or None, cos_sin [n_pos, rot_dim] float32 or None; cache None with n_kv = 0."""
-    import torch
-    f32, T = torch.float32, qkv.shape[0]
+    f32, T = _torch_module().float32, qkv.shape[0]
     dt, stride = _rows(qkv, "rdg_qk_norm_rope_store: qkv", n_q + 2 * n_kv, head_dim)
-    q_stride = 0
+    q_stride, q_ptr, n_pos, cs_ptr = 0, None, 0, None
     if n_q > 0:
         q_dt, q_stride = _rows(q_out, "rdg_qk_norm_rope_store: q_out", n_q, head_dim)
         if q_dt != dt or q_out.shape[0] != T:
             raise RdgError(RDG_EINVAL, "rdg_qk_norm_rope_store: q_out differs from qkv in type or tokens")
-    if q_weight is not None:
-        _tensor(q_weight, "rdg_qk_norm_rope_store: q_weight", f32, head_dim)
-    if k_weight is not None:
-        _tensor(k_weight, "rdg_qk_norm_rope_store: k_weight", f32, head_dim)
-    n_pos = 0
+        q_ptr = q_out.data_ptr()
+    wq = None if q_weight is None else _tensor(q_weight, "rdg_qk_norm_rope_store: q_weight", f32, (head_dim,))
+    wk = None if k_weight is None else _tensor(k_weight, "rdg_qk_norm_rope_store: k_weight", f32, (head_dim,))
     if rot_dim:
         n_pos = cos_sin.shape[0]
-        _tensor(cos_sin, "rdg_qk_norm_rope_store: cos_sin", f32, n_pos, rot_dim)
-    _check(_lib.rdg_qk_norm_rope_store(_ptr(qkv), dt, stride, T, n_q, n_kv, head_dim, _ptr(q_weight), _ptr(k_weight),
-                                       eps, _ptr(cos_sin), n_pos, rot_dim, int(bool(neighbours)), step.ref,
-                                       None if cache is None else cache.ref, _ptr(q_out), q_stride, _stream(stream)),
-           "rdg_qk_norm_rope_store")
+        cs_ptr = _tensor(cos_sin, "rdg_qk_norm_rope_store: cos_sin", f32, (n_pos, rot_dim))
+    _check(_lib.rdg_qk_norm_rope_store(qkv.data_ptr(), dt, stride, T, n_q, n_kv, head_dim, wq, wk, eps, cs_ptr, n_pos,
+                                       rot_dim, 1 if neighbours else 0, step.ref, None if cache is None else cache.ref,
+                                       q_ptr, q_stride, _raw_stream(stream)), "rdg_qk_norm_rope_store")
 
 
 def rdg_paged_attention_workspace_bytes(cache, T, n_req, n_q, max_q, max_kv, dtype):
@@ -451,18 +459,16 @@ def rdg_paged_attention(q, step, cache, max_q, max_kv, scale, out, lse=None, wor
                         stream=None):
     """q, out [T, n_q, head_dim] (token strides free), lse [T, n_q] float32 or None; work: a uint8 tensor of
     rdg_paged_attention_workspace_bytes."""
-    import torch
-    T, n_q = q.shape[:2]
+    T, n_q = q.shape[0], q.shape[1]
     dt, q_stride = _rows(q, "rdg_paged_attention: q", n_q, cache.head_dim)
     out_dt, out_stride = _rows(out, "rdg_paged_attention: out", n_q, cache.head_dim)
     if out_dt != dt or out.shape[0] != T:
         raise RdgError(RDG_EINVAL, "rdg_paged_attention: out differs from q in type or tokens")
-    if lse is not None:
-        _tensor(lse, "rdg_paged_attention: lse", torch.float32, T, n_q)
-    _check(_lib.rdg_paged_attention(_ptr(q), dt, q_stride, T, n_q, step.ref, cache.ref, max_q, max_kv, scale,
-                                    int(bool(causal)), window, _ptr(out), out_stride, _ptr(lse), _ptr(work),
-                                    0 if work is None else work.numel() * work.element_size(), _stream(stream)),
-           "rdg_paged_attention")
+    lse_ptr = None if lse is None else _tensor(lse, "rdg_paged_attention: lse", _torch_module().float32, (T, n_q))
+    work_ptr, work_bytes = (None, 0) if work is None else (work.data_ptr(), work.nbytes)
+    _check(_lib.rdg_paged_attention(q.data_ptr(), dt, q_stride, T, n_q, step.ref, cache.ref, max_q, max_kv, scale,
+                                    1 if causal else 0, window, out.data_ptr(), out_stride, lse_ptr, work_ptr, work_bytes,
+                                    _raw_stream(stream)), "rdg_paged_attention")
 
 
 def rdg_check_status(layout_or_status, stream=None):

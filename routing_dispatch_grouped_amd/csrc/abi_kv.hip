@@ -38,7 +38,8 @@ int cache_buffers_rc(const rdg_kv_cache* C) {
     return RDG_OK;
 }
 
-constexpr int kChunkMin = 256, kChunkMax = 4096;  // keys; a k_attn_rows workgroup's lanes hold the pages of 4096
+constexpr int kChunkMin = 256;                    // keys: one 64-key step of each of four waves
+constexpr int kWaveKeys = 1024;                   // keys whose pages the lanes of a k_attn_rows wave hold
 constexpr int kRowUnits = 1024;                   // k_attn_rows workgroups wanted: four per CU
 constexpr int kTileUnits = 512;                   // k_attn_tiles workgroups wanted: two per CU
 constexpr int kTileChunkMin = 512;
@@ -46,7 +47,7 @@ constexpr int kTileChunkMin = 512;
 // How a call's work is split.  span: the longest run of keys that one request's
 // queries see together.
 struct AttnPlan {
-    int nr;  // 16-row tiles per wave of k_attn_rows
+    int rt;  // 16-row tiles per workgroup of k_attn_rows
     int n_most, row_tiles, chunk, row_chunks;
     int tile_slots, tile_chunk, tile_chunks;  // tile_slots 0: no k_attn_tiles
     int max_chunks;
@@ -79,12 +80,13 @@ AttnPlan plan_attn(int T, int R, int n_kv, int group, int head_dim, bool bf16, i
     }
     if (p.n_most > 0) {
         const int64_t rows = (int64_t)p.n_most * group;
-        p.nr = !bf16 || rows <= 16 ? 1 : rows <= 32 || head_dim == 256 ? 2 : 4;
-        p.row_tiles = (int)((rows + 16 * p.nr - 1) / (16 * p.nr));
+        p.rt = rows <= 64 ? (int)((rows + 15) / 16) : 4;
+        p.row_tiles = (int)((rows + 16 * p.rt - 1) / (16 * p.rt));
+        const int most = kWaveKeys * (p.rt == 1 ? 4 : p.rt == 2 ? 2 : 1);
         const double units = (double)R * n_kv * p.row_tiles;
         double want = ceil(span * units / kRowUnits / kChunkMin) * kChunkMin;
         if (want < kChunkMin) want = kChunkMin;
-        p.chunk = want > kChunkMax ? kChunkMax : (int)want;
+        p.chunk = want > most ? most : (int)want;
         p.row_chunks = chunks_of(span, p.chunk);
         if (p.row_chunks > p.max_chunks) p.max_chunks = p.row_chunks;
     }
@@ -219,17 +221,16 @@ int rdg_paged_attention(const void* q, int dtype, int64_t q_stride, int T, int n
     if (p.tile_slots > 0) fit(&p.tile_chunk, &p.tile_chunks);
     if (p.n_most > 0) fit(&p.chunk, &p.row_chunks);
     a.max_chunks = p.tile_chunks > p.row_chunks ? p.tile_chunks : p.row_chunks;
-    a.n_most = p.n_most, a.rows_per_tile = 16 * p.nr, a.row_tiles = p.row_tiles, a.chunk = p.chunk;
+    a.n_most = p.n_most, a.rows_per_tile = 16 * p.rt, a.row_tiles = p.row_tiles, a.chunk = p.chunk;
     a.row_chunks = p.row_chunks, a.tile_rows = attn_tile_rows(D), a.tile_slots = p.tile_slots;
     a.tile_chunk = p.tile_chunk, a.tile_chunks = p.tile_chunks;
-    a.join_q = p.tile_chunks > 1 ? max_q : p.n_most;
     if (a.max_chunks > 1) {
         a.part_o = static_cast<float*>(work);
         a.part_ml = a.part_o + (size_t)T * n_q * D * a.max_chunks;
     }
     hipError_t e = hipSuccess;
     if (p.tile_slots > 0) e = launch_attn_tiles(a, D, stream);
-    if (e == hipSuccess && p.n_most > 0) e = launch_attn_rows(a, D, bf16, p.nr, stream);
+    if (e == hipSuccess && p.n_most > 0) e = launch_attn_rows(a, D, bf16, stream);
     if (e == hipSuccess && a.max_chunks > 1) e = launch_attn_join(a, D, bf16, stream);
     return hip_rc(e);
 }

@@ -19,17 +19,19 @@
 // of two (v_cvt_scalef32_pk_bf16_fp8).  fp32 queries and probabilities go in as
 // three bf16 parts each, which carries 24 bits.
 //
-// A workgroup's four waves take 64-key blocks in turn from one chunk of one
-// request's keys and join in LDS; chunks of one row are joined by a second
-// launch, in chunk order, so results do not depend on scheduling.  A wave's
-// next K block is in flight while its softmax and V product run, and its next
-// V block during the K product: 16 KB a wave at head_dim 128.
+// A workgroup's waves are RT row tiles x KG key groups (4 x 1, 3 x 1, 2 x 2 or 1 x
+// 4): the key groups take the 64-key blocks of one chunk of one request's keys in
+// turn and join in LDS; the row tiles read the same blocks, which the first brings
+// into the caches (tiles held in one wave's registers instead ran 64 rows at half the speed).
+// Chunks of one row are joined by a second launch, in chunk order, so results
+// do not depend on scheduling.  A wave's next K block is in flight while its
+// softmax and V product run, and its next V block during the K product: 16 KB
+// a wave at head_dim 128.
 #include "attn.h"
 
 namespace rdg {
 namespace {
 
-constexpr int kWaves = 4;
 constexpr int kBlock = 64;  // keys per wave and step
 
 template <int D>
@@ -60,13 +62,15 @@ __device__ __forceinline__ void split_bf16(float x, __bf16 (&part)[NS]) {
     }
 }
 
-// NS = 1: bf16 queries and output; 3: fp32.  NR: 16-row tiles per wave.
-template <int D, int NS, int NR>
-__global__ __launch_bounds__(kWaves * kWave, 1) void k_attn_rows(AttnCall a) {
+// NS = 1: bf16 queries and output; 3: fp32.  RT: 16-row tiles per workgroup.
+template <int D, int NS, int RT>
+__global__ __launch_bounds__((RT == 3 ? 3 : 4) * kWave, 1) void k_attn_rows(AttnCall a) {
     constexpr int KJ = D / 64, W = VWords<D>::n, U = D / 16;
-    __shared__ float lds_o[kWaves][16][D + 4];
-    __shared__ float lds_m[kWaves][16], lds_l[kWaves][16];
-    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+    constexpr int KG = RT == 1 ? 4 : RT == 2 ? 2 : 1;
+    __shared__ float lds_o[RT][KG][16][D + 4];
+    __shared__ float lds_m[RT][KG][16], lds_l[RT][KG][16];
+    const int lane = lane_id(), w_id = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+    const int rt = w_id / KG, wave = w_id % KG;  // row tile, key group
     const int col = lane & 15, g4 = lane >> 4;
     int id = (int)blockIdx.x;
     const int head = id % a.n_kv;
@@ -75,21 +79,23 @@ __global__ __launch_bounds__(kWaves * kWave, 1) void k_attn_rows(AttnCall a) {
     id /= a.row_tiles;
     const int r = id % a.R, chunk = id / a.R;
     const ReqSpan s = req_span(a, r);
-    const int G = a.group, rows = s.n * G, row0 = tile * 16 * NR;
-    if (row0 >= rows || s.n > a.n_most) return;
-    const int last_row = row0 + 16 * NR < rows ? row0 + 16 * NR - 1 : rows - 1;
-    const TileKeys keys = tile_keys(a, s, row0, last_row + 1, a.chunk);
+    const int G = a.group, rows = s.n * G, first = tile * 16 * RT;
+    if (first >= rows || s.n > a.n_most) return;
+    const int last = first + 16 * RT < rows ? first + 16 * RT - 1 : rows - 1;
+    const TileKeys keys = tile_keys(a, s, first, last + 1, a.chunk);
     const int chunks = keys.chunks;
     if (chunk >= chunks) return;
-    const int i_first = row0 / G, i_last = last_row / G;
-    // keys that every row of the tile sees, and that any does
-    const int all_lo = key_lo(a, s, i_last), all_hi = key_hi(a, s, i_first);
-    const int any_lo = key_lo(a, s, i_first), any_hi = keys.end;
     const int k0 = keys.begin + chunk * a.chunk;
+    // this wave's rows (none: those of the last row, not stored), keys that every one
+    // of them sees, and that any does
+    const int row0 = first + rt * 16;
+    const int i_first = (row0 < rows ? row0 : rows - 1) / G, i_last = (row0 + 15 < rows ? row0 + 15 : rows - 1) / G;
+    const int all_lo = key_lo(a, s, i_last), all_hi = key_hi(a, s, i_first);
+    const int any_lo = key_lo(a, s, i_first), any_hi = key_hi(a, s, i_last);
     const int k1 = any_hi < k0 + a.chunk ? any_hi : k0 + a.chunk;
 
     // page and scales of each of this wave's 16-key groups, one per lane
-    const int my_key = k0 + ((lane >> 2) * kWaves + wave) * kBlock + (lane & 3) * 16;
+    const int my_key = k0 + ((lane >> 2) * KG + wave) * kBlock + (lane & 3) * 16;
     int my_page = 0;
     float my_ks = 1.0f, my_vs = 1.0f;
     if (my_key < k1) {
@@ -99,15 +105,14 @@ __global__ __launch_bounds__(kWaves * kWave, 1) void k_attn_rows(AttnCall a) {
     }
 
     // queries: lane (row col, reduction group g4)
-    bf16x8_t q[NR][2 * KJ][NS];
-    int hi[NR], lo[NR];
-#pragma unroll
-    for (int nr = 0; nr < NR; ++nr) {
-        const int row = row0 + nr * 16 + col;
+    bf16x8_t q[2 * KJ][NS];
+    int hi, lo;
+    {
+        const int row = row0 + col;
         const bool live = row < rows;
         const int i = live ? row / G : 0, h = head * G + (live ? row % G : 0);
-        hi[nr] = key_hi(a, s, live ? i : i_last);
-        lo[nr] = key_lo(a, s, live ? i : i_last);
+        hi = key_hi(a, s, live ? i : i_last);
+        lo = key_lo(a, s, live ? i : i_last);
         const int64_t at = (int64_t)(s.t0 + i) * a.q_stride + (int64_t)h * D + 16 * g4;
 #pragma unroll
         for (int j = 0; j < KJ; ++j)
@@ -115,7 +120,7 @@ __global__ __launch_bounds__(kWaves * kWave, 1) void k_attn_rows(AttnCall a) {
             for (int e = 0; e < 2; ++e) {
                 if constexpr (NS == 1) {
                     bf16x8_t v = *reinterpret_cast<const bf16x8_t*>(static_cast<const uint16_t*>(a.q) + at + 64 * j + 8 * e);
-                    q[nr][2 * j + e][0] = v;
+                    q[2 * j + e][0] = v;
                 } else {
                     const float* f = static_cast<const float*>(a.q) + at + 64 * j + 8 * e;
 #pragma unroll
@@ -123,27 +128,22 @@ __global__ __launch_bounds__(kWaves * kWave, 1) void k_attn_rows(AttnCall a) {
                         __bf16 part[NS];
                         split_bf16<NS>(f[c], part);
 #pragma unroll
-                        for (int n = 0; n < NS; ++n) q[nr][2 * j + e][n][c] = part[n];
+                        for (int n = 0; n < NS; ++n) q[2 * j + e][n][c] = part[n];
                     }
                 }
             }
     }
 
-    f32x4_t o[NR][U];
-    float m[NR], l[NR];
+    f32x4_t o[U];
+    float m = -__builtin_inff(), l = 0.0f;
 #pragma unroll
-    for (int nr = 0; nr < NR; ++nr) {
-        m[nr] = -__builtin_inff();
-        l[nr] = 0.0f;
-#pragma unroll
-        for (int u = 0; u < U; ++u) o[nr][u] = f32x4_t{0, 0, 0, 0};
-    }
+    for (int u = 0; u < U; ++u) o[u] = f32x4_t{0, 0, 0, 0};
 
     uint4 kreg[4][KJ];
     uint32_t vreg[4][4][W];
     const auto row_base = [&](int step, int t) -> int64_t {  // first code of a 16-key group's first row
         const int page = __builtin_amdgcn_readlane(my_page, step * 4 + t);
-        const int key = k0 + (step * kWaves + wave) * kBlock + t * 16;
+        const int key = k0 + (step * KG + wave) * kBlock + t * 16;
         return ((((int64_t)page * a.n_kv + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1))) * D;
     };
     const auto load_k = [&](int step) {
@@ -163,7 +163,7 @@ __global__ __launch_bounds__(kWaves * kWave, 1) void k_attn_rows(AttnCall a) {
         }
     };
 
-    const int steps = k1 > k0 + wave * kBlock ? (k1 - k0 - wave * kBlock + kWaves * kBlock - 1) / (kWaves * kBlock) : 0;
+    const int steps = k1 > k0 + wave * kBlock ? (k1 - k0 - wave * kBlock + KG * kBlock - 1) / (KG * kBlock) : 0;
     if (steps > 0) {
         load_k(0);
         load_v(0);
@@ -171,23 +171,20 @@ __global__ __launch_bounds__(kWaves * kWave, 1) void k_attn_rows(AttnCall a) {
     const float c = a.scale_log2;
     uint32_t saw_nan = 0;
     for (int step = 0; step < steps; ++step) {
-        const int kb = k0 + (step * kWaves + wave) * kBlock;
-        f32x4_t sc[NR][4];
+        const int kb = k0 + (step * KG + wave) * kBlock;
+        f32x4_t sc[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const float ks = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_ks), step * 4 + t));
-#pragma unroll
-            for (int nr = 0; nr < NR; ++nr) sc[nr][t] = f32x4_t{0, 0, 0, 0};
+            sc[t] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
             for (int j = 0; j < KJ; ++j) {
                 const bf16x8_t k_lo = codes_to_bf16(kreg[t][j].x, kreg[t][j].y, ks, ks);
                 const bf16x8_t k_hi = codes_to_bf16(kreg[t][j].z, kreg[t][j].w, ks, ks);
 #pragma unroll
-                for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
                     for (int n = NS - 1; n >= 0; --n) {  // small parts first
-                        sc[nr][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k_lo, q[nr][2 * j][n], sc[nr][t], 0, 0, 0);
-                        sc[nr][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k_hi, q[nr][2 * j + 1][n], sc[nr][t], 0, 0, 0);
+                        sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k_lo, q[2 * j][n], sc[t], 0, 0, 0);
+                        sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k_hi, q[2 * j + 1][n], sc[t], 0, 0, 0);
                     }
             }
         }
@@ -196,13 +193,11 @@ __global__ __launch_bounds__(kWaves * kWave, 1) void k_attn_rows(AttnCall a) {
         const bool masked = kb < all_lo || kb + kBlock > all_hi;
         if (masked) {
 #pragma unroll
-            for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int key = kb + 16 * t + 4 * g4 + i;
-                        if (key < lo[nr] || key >= hi[nr]) sc[nr][t][i] = -__builtin_inff();
+                        if (key < lo || key >= hi) sc[t][i] = -__builtin_inff();
                     }
             // keys that no row sees may hold anything
 #pragma unroll
@@ -220,38 +215,37 @@ __global__ __launch_bounds__(kWaves * kWave, 1) void k_attn_rows(AttnCall a) {
                     }
                 }
         }
-        bf16x8_t p[NR][2][NS];
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
+        bf16x8_t p[2][NS];
+        {
             float top = -__builtin_inff();
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[nr][t][i]);
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[t][i]);
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
-            const float m_new = fmaxf(m[nr], top * c);
-            if (__any(m_new > m[nr] + kSlack)) {
-                const float shrink = __builtin_amdgcn_exp2f(m[nr] - (m_new == -__builtin_inff() ? 0.0f : m_new));
-                l[nr] *= shrink;
+            const float m_new = fmaxf(m, top * c);
+            if (__any(m_new > m + kSlack)) {
+                const float shrink = __builtin_amdgcn_exp2f(m - (m_new == -__builtin_inff() ? 0.0f : m_new));
+                l *= shrink;
 #pragma unroll
-                for (int u = 0; u < U; ++u) o[nr][u] *= shrink;
-                m[nr] = m_new;
+                for (int u = 0; u < U; ++u) o[u] *= shrink;
+                m = m_new;
             }
-            const float ref = m[nr] == -__builtin_inff() ? 0.0f : m[nr];
+            const float ref = m == -__builtin_inff() ? 0.0f : m;
             float sum = 0.0f;
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float e = __builtin_amdgcn_exp2f(fmaf(sc[nr][t][i], c, -ref));
+                    const float e = __builtin_amdgcn_exp2f(fmaf(sc[t][i], c, -ref));
                     sum += e;
                     __bf16 part[NS];
                     split_bf16<NS>(e, part);
 #pragma unroll
-                    for (int n = 0; n < NS; ++n) p[nr][t / 2][n][(t & 1) * 4 + i] = part[n];
+                    for (int n = 0; n < NS; ++n) p[t / 2][n][(t & 1) * 4 + i] = part[n];
                 }
-            l[nr] += sum;
+            l += sum;
         }
         // O^T += V^T P^T; column of output tile u in lane col: col * U + u
 #pragma unroll
@@ -272,10 +266,8 @@ __global__ __launch_bounds__(kWaves * kWave, 1) void k_attn_rows(AttnCall a) {
                     const bf16x8_t v = codes_to_bf16(x[b], y[b], va, vb);
                     const int u = 4 * w + b;
 #pragma unroll
-                    for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
                         for (int n = NS - 1; n >= 0; --n)
-                            o[nr][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[nr][t2][n], o[nr][u], 0, 0, 0);
+                            o[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[t2][n], o[u], 0, 0, 0);
                 }
             }
         }
@@ -284,7 +276,7 @@ __global__ __launch_bounds__(kWaves * kWave, 1) void k_attn_rows(AttnCall a) {
 
     if (__any(saw_nan != 0)) {
         for (int step = 0; step < steps; ++step) {
-            const int kb = k0 + (step * kWaves + wave) * kBlock;
+            const int kb = k0 + (step * KG + wave) * kBlock;
             if (kb >= all_lo && kb + kBlock <= all_hi) continue;
             for (int j = kb; j < kb + kBlock && j < any_hi; ++j) {
                 const int page = page_of(a, r, j);
@@ -296,81 +288,81 @@ __global__ __launch_bounds__(kWaves * kWave, 1) void k_attn_rows(AttnCall a) {
                     for (int w = 0; w < W; ++w) {
                         const uint32_t nan = nan_bytes(*reinterpret_cast<const uint32_t*>(p + (4 * g4 + i) * U + 4 * w));
 #pragma unroll
-                        for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
                             for (int b = 0; b < 4; ++b)
-                                if (j >= lo[nr] && j < hi[nr] && (nan >> (8 * b + 7) & 1))
-                                    o[nr][4 * w + b][i] = __builtin_nanf("");
+                                if (j >= lo && j < hi && (nan >> (8 * b + 7) & 1))
+                                    o[4 * w + b][i] = __builtin_nanf("");
                     }
             }
         }
     }
 
-    // the four waves' parts, joined in LDS
+    // the key groups' parts, joined in LDS
+    float sum = l + __shfl_xor(l, 16);
+    sum += __shfl_xor(sum, 32);
+    if (lane < 16) {
+        lds_m[rt][wave][col] = m;
+        lds_l[rt][wave][col] = sum;
+    }
 #pragma unroll
-    for (int nr = 0; nr < NR; ++nr) {
-        float sum = l[nr] + __shfl_xor(l[nr], 16);
-        sum += __shfl_xor(sum, 32);
-        if (nr > 0) __syncthreads();
-        if (lane < 16) {
-            lds_m[wave][col] = m[nr];
-            lds_l[wave][col] = sum;
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int u = 0; u < U; u += 4)
+            *reinterpret_cast<float4*>(&lds_o[rt][wave][col][(4 * g4 + i) * U + u]) =
+                make_float4(o[u][i], o[u + 1][i], o[u + 2][i], o[u + 3][i]);
+    __syncthreads();
+    constexpr int TPR = D / 4;  // threads per row
+    for (int x = threadIdx.x; x < 16 * RT * TPR; x += RT * KG * kWave) {
+        const int rr = (x / TPR) & 15, ty = x / (16 * TPR), d = (x % TPR) * 4, row = first + x / TPR;
+        if (row >= rows) break;
+        float top = lds_m[ty][0][rr];
+#pragma unroll
+        for (int w = 1; w < KG; ++w) top = fmaxf(top, lds_m[ty][w][rr]);
+        const float ref = top == -__builtin_inff() ? 0.0f : top;
+        float total = 0.0f;
+        float4 acc = make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int w = 0; w < KG; ++w) {
+            const float f = __builtin_amdgcn_exp2f(lds_m[ty][w][rr] - ref);
+            total = fmaf(f, lds_l[ty][w][rr], total);
+            const float4 v = *reinterpret_cast<const float4*>(&lds_o[ty][w][rr][d]);
+            acc.x = fmaf(f, v.x, acc.x), acc.y = fmaf(f, v.y, acc.y);
+            acc.z = fmaf(f, v.z, acc.z), acc.w = fmaf(f, v.w, acc.w);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int u = 0; u < U; u += 4)
-                *reinterpret_cast<float4*>(&lds_o[wave][col][(4 * g4 + i) * U + u]) =
-                    make_float4(o[nr][u][i], o[nr][u + 1][i], o[nr][u + 2][i], o[nr][u + 3][i]);
-        __syncthreads();
-        constexpr int TPR = D / 4;  // threads per row
-        for (int x = threadIdx.x; x < 16 * TPR; x += kWaves * kWave) {
-            const int rr = x / TPR, d = (x % TPR) * 4, row = row0 + nr * 16 + rr;
-            if (row >= rows) continue;
-            float top = lds_m[0][rr];
-#pragma unroll
-            for (int w = 1; w < kWaves; ++w) top = fmaxf(top, lds_m[w][rr]);
-            const float ref = top == -__builtin_inff() ? 0.0f : top;
-            float total = 0.0f;
-            float4 acc = make_float4(0, 0, 0, 0);
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                const float f = __builtin_amdgcn_exp2f(lds_m[w][rr] - ref);
-                total = fmaf(f, lds_l[w][rr], total);
-                const float4 v = *reinterpret_cast<const float4*>(&lds_o[w][rr][d]);
-                acc.x = fmaf(f, v.x, acc.x), acc.y = fmaf(f, v.y, acc.y);
-                acc.z = fmaf(f, v.z, acc.z), acc.w = fmaf(f, v.w, acc.w);
-            }
-            const int i = row / G, h = head * G + row % G;
-            if (chunks == 1) {
-                const bool none = key_hi(a, s, i) <= key_lo(a, s, i);
-                store_part<NS == 1>(a, s.t0 + i, h, d, D, acc, total, top, none);
-            } else {
-                const int64_t at = ((int64_t)(s.t0 + i) * a.n_q + h) * a.max_chunks + chunk;
-                *reinterpret_cast<float4*>(a.part_o + at * D + d) = acc;
-                if (d == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(top, total);
-            }
+        const int i = row / G, h = head * G + row % G;
+        if (chunks == 1) {
+            const bool none = key_hi(a, s, i) <= key_lo(a, s, i);
+            store_part<NS == 1>(a, s.t0 + i, h, d, D, acc, total, top, none);
+        } else {
+            const int64_t at = ((int64_t)(s.t0 + i) * a.n_q + h) * a.max_chunks + chunk;
+            *reinterpret_cast<float4*>(a.part_o + at * D + d) = acc;
+            if (d == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(top, total);
         }
     }
 }
 
-// The chunks of each row, joined in order: one wave per row.  Rows of requests
-// with up to n_most queries were split by k_attn_rows, the others by k_attn_tiles.
+// The chunks of each row, joined in order: one wave per row, four heads of a
+// token per workgroup.  Rows of requests with up to n_most queries were split by
+// k_attn_rows, the others by k_attn_tiles.
+constexpr int kJoinWaves = 4;
+
 template <int D, bool BF16>
-__global__ __launch_bounds__(kWaves * kWave) void k_attn_join(AttnCall a) {
-    int64_t id = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave;
-    const int h = (int)(id % a.n_q);
-    id /= a.n_q;
-    const int i = (int)(id % a.join_q), r = (int)(id / a.join_q);
-    if (r >= a.R) return;
+__global__ __launch_bounds__(kJoinWaves * kWave) void k_attn_join(AttnCall a) {
+    const int lane = lane_id(), groups = (a.n_q + kJoinWaves - 1) / kJoinWaves;
+    const int t = (int)blockIdx.x / groups;
+    const int h = (int)blockIdx.x % groups * kJoinWaves + (int)threadIdx.x / kWave;
+    if (h >= a.n_q) return;
+    int r = -1;  // the last request that begins at or before the token
+    for (int b = 0; b < a.R; b += kWave) r += __popcll(__ballot(b + lane < a.R && a.cu_q[b + lane] <= t));
+    if (r < 0) return;
     const ReqSpan s = req_span(a, r);
-    if (i >= s.n || s.n > a.join_q) return;
-    const int per = s.n <= a.n_most ? a.rows_per_tile : a.tile_rows, row = i * a.group + h % a.group;
+    const int i = t - s.t0;
+    if (i < 0 || i >= s.n) return;
+    const bool few = s.n <= a.n_most;
+    const int per = few ? a.rows_per_tile : a.tile_rows, row = i * a.group + h % a.group;
     const int row0 = row / per * per, row1 = row0 + per < s.n * a.group ? row0 + per : s.n * a.group;
-    const int chunks = tile_keys(a, s, row0, row1, s.n <= a.n_most ? a.chunk : a.tile_chunk).chunks;
+    const int chunks = tile_keys(a, s, row0, row1, few ? a.chunk : a.tile_chunk).chunks;
     if (chunks == 1) return;
-    const int lane = lane_id();
-    const int64_t at = ((int64_t)(s.t0 + i) * a.n_q + h) * a.max_chunks;
+    const int64_t at = ((int64_t)t * a.n_q + h) * a.max_chunks;
     float top = -__builtin_inff();
     for (int c = lane; c < chunks; c += kWave) top = fmaxf(top, a.part_ml[2 * (at + c)]);
     top = wave_max_f32(top);
@@ -389,7 +381,7 @@ __global__ __launch_bounds__(kWaves * kWave) void k_attn_join(AttnCall a) {
     }
     const bool none = key_hi(a, s, i) <= key_lo(a, s, i);
     const float inv = none ? 0.0f : 1.0f / total;
-    const int64_t out = (int64_t)(s.t0 + i) * a.out_stride + (int64_t)h * D;
+    const int64_t out = (int64_t)t * a.out_stride + (int64_t)h * D;
 #pragma unroll
     for (int e = 0; e < D / kWave; ++e) {
         const float v = none ? 0.0f : acc[e] * inv;
@@ -397,42 +389,44 @@ __global__ __launch_bounds__(kWaves * kWave) void k_attn_join(AttnCall a) {
         else static_cast<float*>(a.out)[out + e * kWave + lane] = v;
     }
     if (a.lse && lane == 0)
-        a.lse[(int64_t)(s.t0 + i) * a.n_q + h] = none ? -__builtin_inff() : (top + __builtin_amdgcn_logf(total)) * kLn2;
+        a.lse[(int64_t)t * a.n_q + h] = none ? -__builtin_inff() : (top + __builtin_amdgcn_logf(total)) * kLn2;
 }
 
-template <int D, int NS, int NR>
+template <int D, int NS, int RT>
 hipError_t launch_rows(const AttnCall& a, hipStream_t s) {
     const int64_t grid = (int64_t)a.n_kv * a.row_tiles * a.R * a.row_chunks;
     if (grid >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;
-    k_attn_rows<D, NS, NR><<<(unsigned)grid, kWaves * kWave, 0, s>>>(a);
+    k_attn_rows<D, NS, RT><<<(unsigned)grid, (RT == 3 ? 3 : 4) * kWave, 0, s>>>(a);
     return hipGetLastError();
+}
+
+template <int D, int NS>
+hipError_t launch_d(const AttnCall& a, int rt, hipStream_t s) {
+    switch (rt) {
+        case 1: return launch_rows<D, NS, 1>(a, s);
+        case 2: return launch_rows<D, NS, 2>(a, s);
+        case 3: return launch_rows<D, NS, 3>(a, s);
+        default: return launch_rows<D, NS, 4>(a, s);
+    }
 }
 
 template <int D>
 hipError_t join_d(const AttnCall& a, bool bf16, hipStream_t s) {
-    const int64_t rows = (int64_t)a.R * a.join_q * a.n_q, grid = (rows + kWaves - 1) / kWaves;
+    const int64_t grid = (int64_t)a.T * ((a.n_q + kJoinWaves - 1) / kJoinWaves);
     if (grid >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;
-    if (bf16) k_attn_join<D, true><<<(unsigned)grid, kWaves * kWave, 0, s>>>(a);
-    else k_attn_join<D, false><<<(unsigned)grid, kWaves * kWave, 0, s>>>(a);
+    if (bf16) k_attn_join<D, true><<<(unsigned)grid, kJoinWaves * kWave, 0, s>>>(a);
+    else k_attn_join<D, false><<<(unsigned)grid, kJoinWaves * kWave, 0, s>>>(a);
     return hipGetLastError();
-}
-
-template <int D>
-hipError_t launch_d(const AttnCall& a, bool bf16, int nr, hipStream_t s) {
-    if (!bf16) return launch_rows<D, 3, 1>(a, s);
-    if constexpr (D < 256) {
-        if (nr == 4) return launch_rows<D, 1, 4>(a, s);
-    }
-    return nr >= 2 ? launch_rows<D, 1, 2>(a, s) : launch_rows<D, 1, 1>(a, s);
 }
 
 }  // namespace
 
-hipError_t launch_attn_rows(const AttnCall& a, int head_dim, bool bf16, int nr, hipStream_t s) {
+hipError_t launch_attn_rows(const AttnCall& a, int head_dim, bool bf16, hipStream_t s) {
+    const int rt = a.rows_per_tile / 16;
     switch (head_dim) {
-        case 64: return launch_d<64>(a, bf16, nr, s);
-        case 128: return launch_d<128>(a, bf16, nr, s);
-        default: return launch_d<256>(a, bf16, nr, s);
+        case 64: return bf16 ? launch_d<64, 1>(a, rt, s) : launch_d<64, 3>(a, rt, s);
+        case 128: return bf16 ? launch_d<128, 1>(a, rt, s) : launch_d<128, 3>(a, rt, s);
+        default: return bf16 ? launch_d<256, 1>(a, rt, s) : launch_d<256, 3>(a, rt, s);
     }
 }
 

@@ -462,11 +462,6 @@ hipError_t launch(const AttnCall& a, hipStream_t s) {
     static_assert(bytes <= 160 * 1024, "LDS");
     const int64_t grid = (int64_t)a.n_kv * a.tile_slots * a.tile_chunks;
     if (grid >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;
-    if (bytes > 64 * 1024) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attn_tiles<D, NW, RB>),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-        if (e != hipSuccess) return e;
-    }
     k_attn_tiles<D, NW, RB><<<(unsigned)grid, NW * kWave, bytes, s>>>(a);
     return hipGetLastError();
 }

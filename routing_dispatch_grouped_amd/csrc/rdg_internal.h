@@ -267,9 +267,8 @@ struct AttnCall {
     int n_most, rows_per_tile, row_tiles, chunk, row_chunks;
     // longer ones: tile_slots places for tiles of tile_rows rows, tile_chunk keys a workgroup
     int tile_rows, tile_slots, tile_chunk, tile_chunks;
-    int join_q;  // queries of the longest request whose parts are joined
 };
-hipError_t launch_attn_rows(const AttnCall& a, int head_dim, bool bf16, int nr, hipStream_t s);
+hipError_t launch_attn_rows(const AttnCall& a, int head_dim, bool bf16, hipStream_t s);
 hipError_t launch_attn_tiles(const AttnCall& a, int head_dim, hipStream_t s);
 hipError_t launch_attn_join(const AttnCall& a, int head_dim, bool bf16, hipStream_t s);
 inline int attn_tile_rows(int head_dim) { return head_dim == 256 ? 128 : 256; }
