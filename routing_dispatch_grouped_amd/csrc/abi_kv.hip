@@ -42,14 +42,14 @@ constexpr int kChunkMin = 256;                    // keys: one 64-key step of ea
 constexpr int kWaveKeys = 1024;                   // keys whose pages the lanes of a k_attn_rows wave hold
 constexpr int kRowUnits = 1024;                   // k_attn_rows workgroups wanted: four per CU
 constexpr int kTileUnits = 512;                   // k_attn_tiles workgroups wanted: two per CU
-constexpr int kTileChunkMin = 512;
+constexpr int kTileChunkMin = 512;                // keys: fewer do not pay for the parts' way through memory
 
 // How a call's work is split.  span: the longest run of keys that one request's
 // queries see together.
 struct AttnPlan {
     int rt;  // 16-row tiles per workgroup of k_attn_rows
     int n_most, row_tiles, chunk, row_chunks;
-    int tile_slots, tile_chunk, tile_chunks;  // tile_slots 0: no k_attn_tiles
+    int tile_rows, tile_slots, tile_chunk, tile_chunks;  // tile_slots 0: no k_attn_tiles
     int max_chunks;
 };
 
@@ -68,13 +68,16 @@ AttnPlan plan_attn(int T, int R, int n_kv, int group, int head_dim, bool bf16, i
         p.n_most = 64 / group;
         // no request is that short if even max_q for all the others leaves more
         if ((int64_t)T - (int64_t)(R - 1) * max_q > p.n_most) p.n_most = 0;
-        const int bm = attn_tile_rows(head_dim);
-        p.tile_slots = (int)((int64_t)T * group / bm + R);
-        const double units = (double)n_kv * ceil((double)T * group / bm);
-        double want = ceil(span * units / kTileUnits / 64) * 64;
+        // Tiles of 256 rows convert each key's codes half as often (4% on a long
+        // prefill), tiles of 128 fill the chip sooner and waste less on short requests.
+        const auto units_of = [&](int bm) { return (double)n_kv * ceil((double)T * group / bm); };
+        p.tile_rows = head_dim == 256 || units_of(256) < kTileUnits ? 128 : 256;
+        p.tile_slots = (int)((int64_t)T * group / p.tile_rows + R);
+        const double units = units_of(p.tile_rows);
+        double want = span + 64.0;
+        if (units < kTileUnits / 2) want = ceil(span * units / kTileUnits / 64) * 64;
         if (want < kTileChunkMin) want = kTileChunkMin;
-        if (want > span + 63.0) want = (span + 63) / 64 * 64 + 64;
-        p.tile_chunk = (int)want;
+        p.tile_chunk = (int)((want + 63) / 64) * 64;
         p.tile_chunks = chunks_of(span, p.tile_chunk);
         p.max_chunks = p.tile_chunks;
     }
@@ -222,7 +225,7 @@ int rdg_paged_attention(const void* q, int dtype, int64_t q_stride, int T, int n
     if (p.n_most > 0) fit(&p.chunk, &p.row_chunks);
     a.max_chunks = p.tile_chunks > p.row_chunks ? p.tile_chunks : p.row_chunks;
     a.n_most = p.n_most, a.rows_per_tile = 16 * p.rt, a.row_tiles = p.row_tiles, a.chunk = p.chunk;
-    a.row_chunks = p.row_chunks, a.tile_rows = attn_tile_rows(D), a.tile_slots = p.tile_slots;
+    a.row_chunks = p.row_chunks, a.tile_rows = p.tile_rows, a.tile_slots = p.tile_slots;
     a.tile_chunk = p.tile_chunk, a.tile_chunks = p.tile_chunks;
     if (a.max_chunks > 1) {
         a.part_o = static_cast<float*>(work);

@@ -94,6 +94,25 @@ __device__ __forceinline__ void transpose4(const uint32_t (&r)[4], uint32_t (&ou
     out[3] = __builtin_amdgcn_perm(d, c, 0x07060302u);
 }
 
+// Reductions across the wave's halves and quarters, in the vector unit
+// (v_permlane*_swap with one value as both operands leaves both sides' values).
+__device__ __forceinline__ float max_halves(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_halves(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float max_quarters(float x) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return max_halves(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+__device__ __forceinline__ float sum_quarters(float x) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return sum_halves(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+}
+
 // NaN in V.  0 * NaN would carry a key's NaN into rows that do not see it, so in
 // tiles that some row does not see whole, NaN codes go into the product as zeros;
 // where there were any, the rows that do see them get their NaN at the end.

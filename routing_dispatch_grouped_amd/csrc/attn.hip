@@ -222,8 +222,7 @@ __global__ __launch_bounds__((RT == 3 ? 3 : 4) * kWave, 1) void k_attn_rows(Attn
             for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[t][i]);
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
+            top = max_quarters(top);
             const float m_new = fmaxf(m, top * c);
             if (__any(m_new > m + kSlack)) {
                 const float shrink = __builtin_amdgcn_exp2f(m - (m_new == -__builtin_inff() ? 0.0f : m_new));
@@ -297,8 +296,7 @@ __global__ __launch_bounds__((RT == 3 ? 3 : 4) * kWave, 1) void k_attn_rows(Attn
     }
 
     // the key groups' parts, joined in LDS
-    float sum = l + __shfl_xor(l, 16);
-    sum += __shfl_xor(sum, 32);
+    const float sum = sum_quarters(l);
     if (lane < 16) {
         lds_m[rt][wave][col] = m;
         lds_l[rt][wave][col] = sum;

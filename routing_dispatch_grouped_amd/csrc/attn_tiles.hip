@@ -52,7 +52,7 @@ __device__ __forceinline__ int k_piece(int key, int c) {
 __device__ __forceinline__ int v_piece(int d, int c) { return c ^ (((d >> 1) & 7) ^ ((d >> 4) & 1)); }
 
 template <int D, int NW, int RB>
-__global__ __launch_bounds__(NW * kWave, 1) void k_attn_tiles(AttnCall a) {
+__global__ __launch_bounds__(NW * kWave, NW == 4 && D < 256 ? 2 : 1) void k_attn_tiles(AttnCall a) {
     constexpr int NT = NW * kWave, BM = 32 * RB * NW;
     constexpr int KS = D / 16, DB = D / 32;  // reduction steps of S^T, 32-row blocks of O^T
     // Staging, per thread: KU pieces of 16 K codes, VU of 8 keys x 4 columns of V.
@@ -128,30 +128,31 @@ __global__ __launch_bounds__(NW * kWave, 1) void k_attn_tiles(AttnCall a) {
         const int pg = __shfl(page, g & (kWave - 1));
         return codes + ((((int64_t)pg * a.n_kv + head) << a.page_shift) + (key & in_page)) * D;
     };
-    uint4 kraw[KU];
-    uint32_t vraw[VU][8];
-    float kscale[KU], vscale[VU];
+    uint4 kraw[2][KU];  // the second set for the first tile only
+    uint32_t vraw[2][VU][8];
+    float vscale[2][VU];
     // Loads of one step: V of tile t - 1, then K of tile t, whose pages may be the next set.
-    const auto fetch = [&](int t) {
+    const auto fetch = [&](int t, auto set) {
+        constexpr int F = decltype(set)::value;
 #pragma unroll
         for (int u = 0; u < VU; ++u) {
             const int x = tid + u * NT, c = (x / (D / 4)) & 7, dq = x % (D / 4), g = (t - 1) * 4 + c / 2;
-            vscale[u] = __shfl(vs, g & (kWave - 1));
+            vscale[F][u] = __shfl(vs, g & (kWave - 1));
             const uint8_t* p = row_at(a.v_codes, g, k0 + (t - 1) * kTile + 16 * (c / 2) + 4 * (c & 1)) + 4 * dq;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) vraw[u][i] = *reinterpret_cast<const uint32_t*>(p + (8 * (i / 4) + (i & 3)) * D);
+            for (int i = 0; i < 8; ++i) vraw[F][u][i] = *reinterpret_cast<const uint32_t*>(p + (8 * (i / 4) + (i & 3)) * D);
         }
         if ((t & 15) == 0) load_pages(t / 16);
 #pragma unroll
         for (int u = 0; u < KU; ++u) {
             const int x = tid + u * NT, key = (x / (D / 16)) & (kTile - 1), c = x % (D / 16), g = t * 4 + key / 16;
-            kscale[u] = __shfl(ks, g & (kWave - 1));
-            kraw[u] = *reinterpret_cast<const uint4*>(row_at(a.k_codes, g, k0 + t * kTile + key) + 16 * c);
+            kraw[F][u] = *reinterpret_cast<const uint4*>(row_at(a.k_codes, g, k0 + t * kTile + key) + 16 * c);
         }
     };
     // V codes of tile t before their conversion: keys that no row sees may hold
     // anything, and a NaN that only some see is kept out of the product.
-    const auto clean = [&](int t) {
+    const auto clean = [&](int t, auto set) {
+        constexpr int F = decltype(set)::value;
         const int t0 = k0 + t * kTile;
         if (t0 >= wg_all_lo && t0 + kTile <= wg_all_hi) return;
         uint32_t saw = 0;
@@ -161,25 +162,31 @@ __global__ __launch_bounds__(NW * kWave, 1) void k_attn_tiles(AttnCall a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int j = key + 8 * (i / 4) + (i & 3);
-                if (j < any_lo || j >= any_hi) vraw[u][i] = 0;
-                const uint32_t nan = nan_bytes(vraw[u][i]);
-                vraw[u][i] = without_nan(vraw[u][i], nan);
+                if (j < any_lo || j >= any_hi) vraw[F][u][i] = 0;
+                const uint32_t nan = nan_bytes(vraw[F][u][i]);
+                vraw[F][u][i] = without_nan(vraw[F][u][i], nan);
                 saw |= nan;
             }
         }
         if (saw) lds.nan = 1;
     };
-    const auto stage_k = [&](uint16_t* to_k, int u, int part) {  // half of K unit u
+    const auto stage_k = [&](uint16_t* to_k, int t, int u, auto set) {  // unit u of tile t, whose pages are the ones held
+        constexpr int F = decltype(set)::value;
         const int x = tid + u * NT, key = (x / (D / 16)) & (kTile - 1), c = x % (D / 16);
-        if (KP % NT == 0 || x < KP)
-            *reinterpret_cast<bf16x8_t*>(to_k + key * D + 8 * k_piece<D>(key, 2 * c + part)) =
-                part == 0 ? codes_to_bf16(kraw[u].x, kraw[u].y, kscale[u], kscale[u])
-                          : codes_to_bf16(kraw[u].z, kraw[u].w, kscale[u], kscale[u]);
+        const float scale = __shfl(ks, (t * 4 + key / 16) & (kWave - 1));
+        if (KP % NT == 0 || x < KP) {
+            uint16_t* row = to_k + key * D;
+            *reinterpret_cast<bf16x8_t*>(row + 8 * k_piece<D>(key, 2 * c)) =
+                codes_to_bf16(kraw[F][u].x, kraw[F][u].y, scale, scale);
+            *reinterpret_cast<bf16x8_t*>(row + 8 * k_piece<D>(key, 2 * c + 1)) =
+                codes_to_bf16(kraw[F][u].z, kraw[F][u].w, scale, scale);
+        }
     };
-    const auto stage_v = [&](uint16_t* to_v, int u) {
+    const auto stage_v = [&](uint16_t* to_v, int u, auto set) {
+        constexpr int F = decltype(set)::value;
         const int x = tid + u * NT, c = (x / (D / 4)) & 7, dq = x % (D / 4);
-        const uint32_t in0[4] = {vraw[u][0], vraw[u][1], vraw[u][2], vraw[u][3]};
-        const uint32_t in1[4] = {vraw[u][4], vraw[u][5], vraw[u][6], vraw[u][7]};
+        const uint32_t in0[4] = {vraw[F][u][0], vraw[F][u][1], vraw[F][u][2], vraw[F][u][3]};
+        const uint32_t in1[4] = {vraw[F][u][4], vraw[F][u][5], vraw[F][u][6], vraw[F][u][7]};
         uint32_t x0[4], x1[4];
         transpose4(in0, x0);
         transpose4(in1, x1);
@@ -188,7 +195,7 @@ __global__ __launch_bounds__(NW * kWave, 1) void k_attn_tiles(AttnCall a) {
             const int d = 4 * dq + b;
             if (VP % NT == 0 || x < VP)
                 *reinterpret_cast<bf16x8_t*>(to_v + d * kTile + 8 * v_piece(d, c)) =
-                    codes_to_bf16(x0[b], x1[b], vscale[u], vscale[u]);
+                    codes_to_bf16(x0[b], x1[b], vscale[F][u], vscale[F][u]);
         }
     };
 
@@ -241,7 +248,7 @@ __global__ __launch_bounds__(NW * kWave, 1) void k_attn_tiles(AttnCall a) {
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[rb][kb][i]);
-        return fmaxf(top, __shfl_xor(top, 32)) * scale;
+        return max_halves(top) * scale;
     };
     const auto raise = [&](const float (&top)[RB]) {
         bool grows = false;
@@ -264,6 +271,7 @@ __global__ __launch_bounds__(NW * kWave, 1) void k_attn_tiles(AttnCall a) {
     const auto tile = [&](f32x16_t (&sc)[RB][2], f32x16_t (&next)[RB][2], int t, auto parity) {
         constexpr int B = decltype(parity)::value;
         constexpr int KG = KS / 4;
+        const std::integral_constant<int, 0> set0;
         const uint16_t *k_next = lds.k[1 - B], *v_now = lds.v[B];
         bf16x8_t p[RB][4];
         float sum[RB], ref[RB];
@@ -325,7 +333,7 @@ __global__ __launch_bounds__(NW * kWave, 1) void k_attn_tiles(AttnCall a) {
         for (int rb = 0; rb < RB; ++rb) l[rb] += sum[rb];
         if (t + 1 < tiles) {
             mask(next, t + 1);
-            clean(t + 1);
+            clean(t + 1, set0);
         }
         __builtin_amdgcn_s_setprio(0);
         float top[RB];
@@ -346,20 +354,17 @@ __global__ __launch_bounds__(NW * kWave, 1) void k_attn_tiles(AttnCall a) {
             // staged past the last tile: never read
 #pragma unroll
             for (int u = 0; u < VU; ++u)
-                if (g == u % G2) stage_v(lds.v[1 - B], u);
+                if (g == u % G2) stage_v(lds.v[1 - B], u, set0);
 #pragma unroll
             for (int u = 0; u < KU; ++u)
-                if (g == (1 + u) % G2) {
-                    stage_k(lds.k[B], u, 0);
-                    stage_k(lds.k[B], u, 1);
-                }
+                if (g == (1 + u) % G2) stage_k(lds.k[B], t + 2, u, set0);
             if (g == G2 - 1)
 #pragma unroll
                 for (int rb = 0; rb < RB; ++rb) top[rb] = row_top(next, rb);
         }
         __builtin_amdgcn_sched_barrier(0);
         if (t + 1 < tiles) raise(top);
-        fetch(t + 3);
+        fetch(t + 3, set0);
         lds_barrier();
     };
 
@@ -368,23 +373,18 @@ __global__ __launch_bounds__(NW * kWave, 1) void k_attn_tiles(AttnCall a) {
     if (tiles > 0) {
         f32x16_t s0[RB][2], s1[RB][2];
         float top[RB];
-        load_pages(0);
-        const auto fill = [&](int t, uint16_t* to_k, uint16_t* to_v) {
-            if (to_v) clean(t - 1);
+        const std::integral_constant<int, 0> even;
+        const std::integral_constant<int, 1> odd;
+        fetch(0, odd);
+        fetch(1, even);
+        clean(0, even);
 #pragma unroll
-            for (int u = 0; u < VU; ++u)
-                if (to_v) stage_v(to_v, u);
+        for (int u = 0; u < KU; ++u) stage_k(lds.k[0], 0, u, odd);
 #pragma unroll
-            for (int u = 0; u < KU; ++u) {
-                stage_k(to_k, u, 0);
-                stage_k(to_k, u, 1);
-            }
-        };
-        fetch(0);
-        fill(0, lds.k[0], nullptr);
-        fetch(1);
-        fill(1, lds.k[1], lds.v[0]);
-        fetch(2);
+        for (int u = 0; u < KU; ++u) stage_k(lds.k[1], 1, u, even);
+#pragma unroll
+        for (int u = 0; u < VU; ++u) stage_v(lds.v[0], u, even);
+        fetch(2, even);
         lds_barrier();
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
@@ -406,9 +406,9 @@ __global__ __launch_bounds__(NW * kWave, 1) void k_attn_tiles(AttnCall a) {
         raise(top);
         lds_barrier();  // the first tile's K buffer takes the third tile
         for (int t = 0;;) {
-            tile(s0, s1, t, std::integral_constant<int, 0>{});
+            tile(s0, s1, t, even);
             if (++t >= tiles) break;
-            tile(s1, s0, t, std::integral_constant<int, 1>{});
+            tile(s1, s0, t, odd);
             if (++t >= tiles) break;
         }
     }
@@ -437,7 +437,7 @@ __global__ __launch_bounds__(NW * kWave, 1) void k_attn_tiles(AttnCall a) {
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
         const int row = row0 + (wave * RB + rb) * 32 + col;
-        const float total = l[rb] + __shfl_xor(l[rb], 32);
+        const float total = sum_halves(l[rb]);
         if (row >= rows) continue;
         const int i = row / G, h = head * G + row % G;
         const bool none = hi[rb] <= lo[rb];
@@ -468,11 +468,10 @@ hipError_t launch(const AttnCall& a, hipStream_t s) {
 
 }  // namespace
 
-// a.tile_rows = attn_tile_rows(head_dim)
 hipError_t launch_attn_tiles(const AttnCall& a, int head_dim, hipStream_t s) {
     switch (head_dim) {
-        case 64: return launch<64, 8, 1>(a, s);
-        case 128: return launch<128, 8, 1>(a, s);
+        case 64: return a.tile_rows == 256 ? launch<64, 8, 1>(a, s) : launch<64, 4, 1>(a, s);
+        case 128: return a.tile_rows == 256 ? launch<128, 8, 1>(a, s) : launch<128, 4, 1>(a, s);
         default: return launch<256, 4, 1>(a, s);
     }
 }

@@ -271,6 +271,5 @@ struct AttnCall {
 hipError_t launch_attn_rows(const AttnCall& a, int head_dim, bool bf16, hipStream_t s);
 hipError_t launch_attn_tiles(const AttnCall& a, int head_dim, hipStream_t s);
 hipError_t launch_attn_join(const AttnCall& a, int head_dim, bool bf16, hipStream_t s);
-inline int attn_tile_rows(int head_dim) { return head_dim == 256 ? 128 : 256; }
 
 }  // namespace rdg
