@@ -525,8 +525,8 @@ int rdg_qk_norm_rope_store(const void* qkv, int dtype, int64_t qkv_stride, int T
  *   q, out   [T, q_stride] / [T, out_stride], n_q heads of head_dim (RDG_F32 or
  *            RDG_BF16); query head h reads key head h / (n_q / n_kv)
  *   max_q, max_kv  host bounds of the requests' new and cached tokens: grids
- *            and workspace are sized by them.  A request past max_kv is cut to it (RDG_EDATA);
- *            rows past max_q are not computed
+ *            and workspace are sized by them.  A request of more cached tokens is cut to
+ *            max_kv, one of more new tokens than max_q left out (both RDG_EDATA, with the request)
  *   lse      [T, n_q] fp32 or NULL
  *   work     rdg_paged_attention_workspace_bytes(...) bytes (NULL when that is 0)
  * Softmax, sums and products are fp32; with RDG_BF16 the probabilities are

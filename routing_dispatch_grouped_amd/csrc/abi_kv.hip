@@ -206,7 +206,7 @@ int rdg_paged_attention(const void* q, int dtype, int64_t q_stride, int T, int n
     a.max_blocks = S->max_blocks, a.n_pages = C->n_pages, a.page_shift = page_shift_of(C->page_rows);
     const int64_t table = (int64_t)S->max_blocks * C->page_rows;
     a.kv_cap = table < max_kv ? (int)table : max_kv;
-    a.window = window, a.causal = causal != 0;
+    a.max_q = max_q, a.window = window, a.causal = causal != 0;
     const bool bf16 = dtype == RDG_BF16;
     // The workspace is sized for all max_kv keys.  A window leaves a shorter run,
     // which may be cut finer than the workspace holds parts for: then coarser.

@@ -33,6 +33,11 @@ __device__ __forceinline__ ReqSpan req_span(const AttnCall& a, int r) {
     s.t0 = t0;
     s.n = t1 - t0;
     s.kv = kv;
+    // grids and parts are sized for max_q queries: a longer request is left out
+    if (s.n > a.max_q) {
+        if (threadIdx.x == 0) set_status(a.status, RDG_EDATA, r);
+        s.n = 0;
+    }
     return s;
 }
 

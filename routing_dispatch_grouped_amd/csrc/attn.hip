@@ -32,6 +32,8 @@
 namespace rdg {
 namespace {
 
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
 constexpr int kBlock = 64;  // keys per wave and step
 
 template <int D>
@@ -67,8 +69,12 @@ template <int D, int NS, int RT>
 __global__ __launch_bounds__((RT == 3 ? 3 : 4) * kWave, 1) void k_attn_rows(AttnCall a) {
     constexpr int KJ = D / 64, W = VWords<D>::n, U = D / 16;
     constexpr int KG = RT == 1 ? 4 : RT == 2 ? 2 : 1;
-    __shared__ float lds_o[RT][KG][16][D + 4];
+    // RT > 1: the codes of two steps of each key group; then the parts to be joined
+    constexpr int kCodes = RT > 1 ? KG * 2 * 2 * kBlock * D : 0;
+    constexpr int kParts = RT * KG * 16 * (D + 4) * 4;
+    __shared__ __attribute__((aligned(16))) uint8_t lds_raw[kCodes > kParts ? kCodes : kParts];
     __shared__ float lds_m[RT][KG][16], lds_l[RT][KG][16];
+    auto& lds_o = *reinterpret_cast<float(*)[RT][KG][16][D + 4]>(lds_raw);
     const int lane = lane_id(), w_id = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int rt = w_id / KG, wave = w_id % KG;  // row tile, key group
     const int col = lane & 15, g4 = lane >> 4;
@@ -92,17 +98,9 @@ __global__ __launch_bounds__((RT == 3 ? 3 : 4) * kWave, 1) void k_attn_rows(Attn
     const int i_first = (row0 < rows ? row0 : rows - 1) / G, i_last = (row0 + 15 < rows ? row0 + 15 : rows - 1) / G;
     const int all_lo = key_lo(a, s, i_last), all_hi = key_hi(a, s, i_first);
     const int any_lo = key_lo(a, s, i_first), any_hi = key_hi(a, s, i_last);
-    const int k1 = any_hi < k0 + a.chunk ? any_hi : k0 + a.chunk;
-
-    // page and scales of each of this wave's 16-key groups, one per lane
-    const int my_key = k0 + ((lane >> 2) * KG + wave) * kBlock + (lane & 3) * 16;
-    int my_page = 0;
-    float my_ks = 1.0f, my_vs = 1.0f;
-    if (my_key < k1) {
-        my_page = page_of(a, r, my_key);
-        my_ks = pow2_scale(a.k_scale[(int64_t)my_page * a.n_kv + head]);
-        my_vs = pow2_scale(a.v_scale[(int64_t)my_page * a.n_kv + head]);
-    }
+    // one row tile: this wave's last key; more: the workgroup's, whose waves step together
+    const int end = RT > 1 ? keys.end : any_hi;
+    const int k1 = end < k0 + a.chunk ? end : k0 + a.chunk;
 
     // queries: lane (row col, reduction group g4)
     bf16x8_t q[2 * KJ][NS];
@@ -134,17 +132,29 @@ __global__ __launch_bounds__((RT == 3 ? 3 : 4) * kWave, 1) void k_attn_rows(Attn
             }
     }
 
+    // page and scales of each of this wave's 16-key groups, one per lane
+    const int my_key = k0 + ((lane >> 2) * KG + wave) * kBlock + (lane & 3) * 16;
+    int my_page = 0;
+    float my_ks = 1.0f, my_vs = 1.0f;
+    if (my_key < k1) {
+        my_page = page_of(a, r, my_key);
+        my_ks = pow2_scale(a.k_scale[(int64_t)my_page * a.n_kv + head]);
+        my_vs = pow2_scale(a.v_scale[(int64_t)my_page * a.n_kv + head]);
+    }
+
     f32x4_t o[U];
     float m = -__builtin_inff(), l = 0.0f;
 #pragma unroll
     for (int u = 0; u < U; ++u) o[u] = f32x4_t{0, 0, 0, 0};
 
+    const int in_page = (1 << a.page_shift) - 1;
+    // RT = 1: codes straight into the registers that the products take them from
     uint4 kreg[4][KJ];
     uint32_t vreg[4][4][W];
     const auto row_base = [&](int step, int t) -> int64_t {  // first code of a 16-key group's first row
         const int page = __builtin_amdgcn_readlane(my_page, step * 4 + t);
         const int key = k0 + (step * KG + wave) * kBlock + t * 16;
-        return ((((int64_t)page * a.n_kv + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1))) * D;
+        return ((((int64_t)page * a.n_kv + head) << a.page_shift) + (key & in_page)) * D;
     };
     const auto load_k = [&](int step) {
 #pragma unroll
@@ -162,16 +172,76 @@ __global__ __launch_bounds__((RT == 3 ? 3 : 4) * kWave, 1) void k_attn_rows(Attn
             for (int i = 0; i < 4; ++i) load_words<W>(p + i * D, vreg[t][i]);
         }
     };
+    // RT > 1: the key group's waves share the loads, 16 bytes a lane along the rows, and
+    // pass them on through LDS; K's 16-byte pieces are swizzled by row and V's
+    // rows interleaved, so that the operands' reads fall into different banks
+    constexpr int PK = kBlock * D / 16, ST = RT * kWave, NP = (2 * PK + ST - 1) / ST;
+    const int sid = rt * kWave + lane;
+    u32x4_t stg[NP];
+    uint8_t* const lds_codes = lds_raw + wave * (2 * 2 * kBlock * D);
+    const auto k_place = [&](int key, int piece) {
+        const int turn = D == 64 ? (key >> 2) & 3 : D == 128 ? (key >> 1) & 7 : key & 15;
+        return key * D + 16 * (piece ^ turn);
+    };
+    const auto v_row = [&](int key) { return (key & ~15) | ((key & 3) << 2) | ((key >> 2) & 3); };
+    const auto fetch = [&](int step) {
+        const int kb = k0 + (step * KG + wave) * kBlock;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const int x = sid + p * ST, y = x % PK, key = y / (D / 16);
+            const int page = __shfl(my_page, step * 4 + key / 16);
+            const uint8_t* from = x < PK ? a.k_codes : a.v_codes;
+            if (2 * PK % ST == 0 || x < 2 * PK)
+                stg[p] = *reinterpret_cast<const u32x4_t*>(
+                    from + ((((int64_t)page * a.n_kv + head) << a.page_shift) + ((kb + key) & in_page)) * D +
+                    16 * (y % (D / 16)));
+        }
+    };
+    const auto pass_on = [&](int step) {
+        uint8_t* buf = lds_codes + (step & 1) * (2 * kBlock * D);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const int x = sid + p * ST, y = x % PK, key = y / (D / 16), piece = y % (D / 16);
+            if (2 * PK % ST == 0 || x < 2 * PK)
+                *reinterpret_cast<u32x4_t*>(buf + (x < PK ? k_place(key, piece) : kBlock * D + v_row(key) * D + 16 * piece)) =
+                    stg[p];
+        }
+    };
+    const auto take_k = [&](int step) {
+        const uint8_t* buf = lds_codes + (step & 1) * (2 * kBlock * D);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int j = 0; j < KJ; ++j)
+                kreg[t][j] = *reinterpret_cast<const uint4*>(buf + k_place(16 * t + col, 4 * j + g4));
+    };
+    const auto take_v = [&](int step) {
+        const uint8_t* buf = lds_codes + (step & 1) * (2 * kBlock * D) + kBlock * D;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                load_words<W>(buf + v_row(16 * t + 4 * g4 + i) * D + col * (D / 16), vreg[t][i]);
+    };
 
-    const int steps = k1 > k0 + wave * kBlock ? (k1 - k0 - wave * kBlock + KG * kBlock - 1) / (KG * kBlock) : 0;
+    const int span = k1 - k0 - (RT > 1 ? 0 : wave * kBlock);
+    const int steps = span > 0 ? (span + KG * kBlock - 1) / (KG * kBlock) : 0;
     if (steps > 0) {
-        load_k(0);
-        load_v(0);
+        if constexpr (RT > 1) {
+            fetch(0);
+            pass_on(0);
+            if (steps > 1) fetch(1);
+            __syncthreads();
+        } else {
+            load_k(0);
+            load_v(0);
+        }
     }
     const float c = a.scale_log2;
     uint32_t saw_nan = 0;
     for (int step = 0; step < steps; ++step) {
         const int kb = k0 + (step * KG + wave) * kBlock;
+        if constexpr (RT > 1) take_k(step);
         f32x4_t sc[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -188,7 +258,11 @@ __global__ __launch_bounds__((RT == 3 ? 3 : 4) * kWave, 1) void k_attn_rows(Attn
                     }
             }
         }
-        if (step + 1 < steps) load_k(step + 1);
+        if constexpr (RT > 1) {
+            take_v(step);
+        } else {
+            if (step + 1 < steps) load_k(step + 1);
+        }
 
         const bool masked = kb < all_lo || kb + kBlock > all_hi;
         if (masked) {
@@ -270,7 +344,13 @@ __global__ __launch_bounds__((RT == 3 ? 3 : 4) * kWave, 1) void k_attn_rows(Attn
                 }
             }
         }
-        if (step + 1 < steps) load_v(step + 1);
+        if constexpr (RT > 1) {
+            if (step + 1 < steps) pass_on(step + 1);
+            if (step + 2 < steps) fetch(step + 2);
+            __syncthreads();
+        } else {
+            if (step + 1 < steps) load_v(step + 1);
+        }
     }
 
     if (__any(saw_nan != 0)) {
@@ -295,8 +375,26 @@ __global__ __launch_bounds__((RT == 3 ? 3 : 4) * kWave, 1) void k_attn_rows(Attn
         }
     }
 
-    // the key groups' parts, joined in LDS
     const float sum = sum_quarters(l);
+    if constexpr (KG == 1) {  // no other wave has a part of these rows: out of the registers
+        const int row = row0 + col;
+        if (row >= rows) return;
+        const int i = row / G, h = head * G + row % G;
+        const bool none = key_hi(a, s, i) <= key_lo(a, s, i);
+        const int64_t at = ((int64_t)(s.t0 + i) * a.n_q + h) * a.max_chunks + chunk;
+        if (chunks > 1 && g4 == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(m, sum);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int u = 0; u < U; u += 4) {
+                const int d = (4 * g4 + x) * U + u;
+                const float4 v = make_float4(o[u][x], o[u + 1][x], o[u + 2][x], o[u + 3][x]);
+                if (chunks == 1) store_part<NS == 1>(a, s.t0 + i, h, d, D, v, sum, m, none);
+                else *reinterpret_cast<float4*>(a.part_o + at * D + d) = v;
+            }
+        return;
+    }
+    // the key groups' parts, joined in LDS
     if (lane < 16) {
         lds_m[rt][wave][col] = m;
         lds_l[rt][wave][col] = sum;

@@ -260,7 +260,7 @@ struct AttnCall {
     int32_t* status;
     int64_t q_stride, out_stride;  // elements
     float scale_log2;              // softmax scale times log2(e)
-    int T, R, n_q, n_kv, group, max_blocks, n_pages, page_shift, kv_cap, window;
+    int T, R, n_q, n_kv, group, max_blocks, n_pages, page_shift, kv_cap, max_q, window;
     bool causal;
     int max_chunks;  // parts that the workspace has for each row
     // requests of up to n_most queries: tiles of rows_per_tile rows, chunk keys a workgroup

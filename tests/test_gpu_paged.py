@@ -543,6 +543,22 @@ def test_bad_tables_and_lengths_are_reported():
     assert torch.equal(out[1], ref[1])
 
 
+@pytest.mark.parametrize("q,max_q", [([2, 3], 2), ([9, 90], 40), ([90, 9], 40)])
+def test_requests_past_max_q_are_left_out(q, max_q):
+    """And nothing of them stays behind: the same buffers then give the right results."""
+    c = attn_case([700, 700], q, 16, 4, 2, 64, "bf16", 99)
+    m = c["m"]
+    ref, _ = call(c, 0.1)
+    out, _ = call(c, 0.1, max_q=max_q)
+    long = 1 if q[1] > max_q else 0
+    assert m.rdg_check_status(c["step"]) == (m.RDG_EDATA, long)
+    t0 = q[0] if long else 0
+    assert (out[t0:t0 + q[long]] == 7).all()
+    keep = slice(0, q[0]) if long else slice(q[0], None)
+    assert torch.equal(out[keep], ref[keep]) or torch.allclose(out[keep].float(), ref[keep].float(), atol=2.0 ** -7)
+    assert torch.equal(call(c, 0.1)[0], ref)
+
+
 @pytest.mark.parametrize("q", [1, 130])
 def test_offsets_past_32_bits(q):
     """A cache of more than 4 GiB of codes whose requests live in its last pages."""
