@@ -11,7 +11,7 @@
 //
 // Bound by latency: a step writes 8 bytes per token and reads 8 per request,
 // a few microseconds' worth of one launch.  Every workgroup therefore scans
-// all the requests by itself in LDS (12 bytes a request) instead of waiting
+// all the requests by itself in LDS (16 bytes a request) instead of waiting
 // for another launch or workgroup, and then expands its own 1024 tokens.
 // The last workgroup to finish (a ticket in S.work) writes what a caller may
 // pass as input and output at once: kv_len, the free count, the status.
@@ -56,6 +56,45 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* part, uint3
     return sat_add(before, exc);
 }
 
+// The same of two values at once; part holds two words per wave.
+__device__ __forceinline__ void block_scan2(uint32_t u, uint32_t v, uint32_t* part, uint32_t* u_before, uint32_t* v_before,
+                                            uint32_t* u_all, uint32_t* v_all) {
+    const int lane = lane_id(), wave = (int)threadIdx.x / kWave;
+    uint32_t a = u, b = v;
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) {
+        const uint32_t oa = __shfl_up(a, off), ob = __shfl_up(b, off);
+        if (lane >= off) {
+            a = sat_add(a, oa);
+            b = sat_add(b, ob);
+        }
+    }
+    __syncthreads();  // part may still be read from the scan before
+    if (lane == kWave - 1) {
+        part[wave] = a;
+        part[kThreads / kWave + wave] = b;
+    }
+    a = __shfl_up(a, 1);
+    b = __shfl_up(b, 1);
+    if (lane == 0) a = b = 0;
+    __syncthreads();
+    uint32_t ua = 0, va = 0, ub = 0, vb = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / kWave; ++w) {
+        const uint32_t x = part[w], y = part[kThreads / kWave + w];
+        if (w < wave) {
+            ub = sat_add(ub, x);
+            vb = sat_add(vb, y);
+        }
+        ua = sat_add(ua, x);
+        va = sat_add(va, y);
+    }
+    *u_before = sat_add(ub, a);
+    *v_before = sat_add(vb, b);
+    *u_all = ua;
+    *v_all = va;
+}
+
 // Last i in [0, n) with begin[i] <= t (begin[0] = 0, ascending).
 __device__ __forceinline__ int find_row(const uint32_t* begin, int n, uint32_t t) {
     int lo = 0, hi = n;
@@ -71,11 +110,14 @@ __device__ __forceinline__ int find_row(const uint32_t* begin, int n, uint32_t t
 // ticket is then 0 again for the next launch.
 __device__ __forceinline__ bool last_block(int32_t* ticket) {
     __shared__ int last;
-    __syncthreads();  // every wave has used what it read
+    // every wave has used what it read, and what it noted has been noted: the
+    // ticket orders nothing else, so it needs no fence
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
     if (threadIdx.x == 0) {
         last = 1;
         if (gridDim.x > 1) {
-            last = __hip_atomic_fetch_add(ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
+            last = __hip_atomic_fetch_add(ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
             if (last) __hip_atomic_store(ticket, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
     }
@@ -119,39 +161,53 @@ __device__ __forceinline__ Lens lens_of(const int32_t* kv_len, const int32_t* q_
     return l;
 }
 
+// PER: consecutive requests per thread, whose lengths are loaded together.
+template <int PER>
 __global__ __launch_bounds__(kThreads) void k_kv_plan(rdg_kv_step S, int shift, const int32_t* kv_len,
                                                       const int32_t* q_len, const int32_t* __restrict__ free_list,
                                                       const int32_t* n_free, int32_t* n_free_out) {
     extern __shared__ uint32_t lds[];
-    __shared__ uint32_t part[kThreads / kWave];
+    __shared__ uint32_t part[2 * kThreads / kWave];
     __shared__ uint32_t used;        // pages taken
     __shared__ uint32_t failed[2];   // first request that did not fit / had bad lengths
     const int R = S.n_req, P1 = S.page_rows - 1, tid = (int)threadIdx.x;
-    uint32_t* cu = lds;              // [R + 1] first token
+    uint32_t* cu = lds;                        // [R + 1] first token
     int32_t* page0 = (int32_t*)(lds + R + 1);  // [R] place on the free stack, -1: not admitted
     uint32_t* seg0 = lds + 2 * R + 1;          // [R] first segment
+    int32_t* kv0 = (int32_t*)(lds + 3 * R + 1);  // [R] cached tokens
     if (tid == 0) {
         used = 0;
         failed[0] = failed[1] = 0xffffffffu;
         cu[0] = 0;
     }
+    const int r0 = tid * PER;
+    Lens len[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        len[i] = {0, 0, false};
+        if (r0 + i < R) len[i] = lens_of(kv_len, q_len, r0 + i);
+    }
     int nf = n_free[0];
     nf = nf < 0 ? 0 : nf > S.n_pages ? S.n_pages : nf;
-    const int per = (R + kThreads - 1) / kThreads;
-    const int r0 = tid * per < R ? tid * per : R, r1 = r0 + per < R ? r0 + per : R;
 
     uint32_t q_sum = 0, need_sum = 0;
-    for (int r = r0; r < r1; ++r) {
-        const Lens l = lens_of(kv_len, q_len, r);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const Lens l = len[i];
         const int old_b = (l.kv + P1) >> shift, new_b = (int)(((uint32_t)l.kv + l.q + P1) >> shift);
         q_sum = sat_add(q_sum, l.q);
         need_sum = sat_add(need_sum, new_b > S.max_blocks ? 0 : new_b - old_b);
     }
     uint32_t n_tok, n_seg, all;
-    uint32_t tok = block_scan(q_sum, part, &n_tok), pg = block_scan(need_sum, part, &all);
-    uint32_t seg_sum = 0;
-    for (int r = r0; r < r1; ++r) {
-        const Lens l = lens_of(kv_len, q_len, r);
+    uint32_t tok, pg;
+    block_scan2(q_sum, need_sum, part, &tok, &pg, &n_tok, &all);
+    uint32_t seg_sum = 0, seg[PER], took = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int r = r0 + i;
+        const Lens l = len[i];
+        seg[i] = seg_sum;
+        if (r >= R) continue;
         const int old_b = (l.kv + P1) >> shift, new_b = (int)(((uint32_t)l.kv + l.q + P1) >> shift);
         const bool fits = new_b <= S.max_blocks;
         const uint32_t need = fits ? new_b - old_b : 0;
@@ -160,49 +216,62 @@ __global__ __launch_bounds__(kThreads) void k_kv_plan(rdg_kv_step S, int shift, 
         pg = sat_add(pg, need);
         const bool ok = !l.bad && fits && tok <= (uint32_t)S.t_cap && (need == 0 || pg <= (uint32_t)nf);
         cu[r + 1] = tok;
+        kv0[r] = l.kv;
         page0[r] = ok ? (need ? (int)begin : 0) : -1;
-        uint32_t segs = 0;
-        if (ok && l.q > 0) segs = ((l.kv + l.q - 1) >> shift) - (l.kv >> shift) + 1;
-        seg0[r] = seg_sum;
-        seg_sum += segs;
-        if (ok && need) atomicMax(&used, pg);
+        if (ok && l.q > 0) seg_sum += ((l.kv + l.q - 1) >> shift) - (l.kv >> shift) + 1;
+        if (ok && need) took = pg;  // ascending over the requests
         if (!ok) atomicMin(&failed[l.bad ? 1 : 0], (uint32_t)r);
     }
+#pragma unroll
+    for (int off = kWave / 2; off >= 1; off >>= 1) {
+        const uint32_t o = __shfl_xor(took, off);
+        took = o > took ? o : took;
+    }
+    if (lane_id() == 0) atomicMax(&used, took);
     const uint32_t seg_before = block_scan(seg_sum, part, &n_seg);
-    for (int r = r0; r < r1; ++r) seg0[r] += seg_before;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (r0 + i < R) seg0[r0 + i] = seg[i] + seg_before;
     __syncthreads();
 
     // tokens: kTokPerThread consecutive ones per thread
     const uint32_t total = n_tok < (uint32_t)S.t_cap ? n_tok : (uint32_t)S.t_cap;
     const int t0 = ((int)blockIdx.x * kThreads + tid) * kTokPerThread;
     if (t0 < S.t_cap) {
-        int32_t slot[kTokPerThread], pos[kTokPerThread];
+        int32_t slot[kTokPerThread], pos[kTokPerThread], req[kTokPerThread], page[kTokPerThread];
+        bool stored[kTokPerThread], fresh[kTokPerThread];
         int r = (uint32_t)t0 < total ? find_row(cu, R, t0) : 0;
 #pragma unroll
         for (int i = 0; i < kTokPerThread; ++i) {
             const uint32_t t = t0 + i;
-            slot[i] = -1;
+            stored[i] = fresh[i] = false;
             pos[i] = 0;
-            if (t >= total) continue;
-            while (cu[r + 1] <= t) ++r;
-            const int kv = lens_of(kv_len, q_len, r).kv, base = page0[r];
-            const int p = kv + (int)(t - cu[r]), blk = p >> shift;
-            pos[i] = p;
-            if (base < 0) continue;
-            const int old_b = (kv + P1) >> shift;
-            int32_t* entry = S.block_table + (int64_t)r * S.max_blocks + blk;
-            int page;
-            if (blk < old_b) {
-                page = *entry;
-            } else {
-                page = free_list[nf - 1 - base - (blk - old_b)];
-                if ((p & P1) == 0) *entry = page;
+            page[i] = -1;
+            if (t < total) {
+                while (cu[r + 1] <= t) ++r;
+                const int kv = kv0[r], base = page0[r];
+                pos[i] = kv + (int)(t - cu[r]);
+                stored[i] = base >= 0;
+                if (stored[i]) {  // the four tokens' loads are in flight together
+                    const int blk = pos[i] >> shift, back = blk - ((kv + P1) >> shift);
+                    fresh[i] = back >= 0;
+                    page[i] = fresh[i] ? free_list[nf - 1 - base - back] : S.block_table[(int64_t)r * S.max_blocks + blk];
+                }
             }
-            if ((unsigned)page < (unsigned)S.n_pages) slot[i] = (page << shift) + (p & P1);
-            else note_bad(S.work, r);
-            if (p == kv || (p & P1) == 0) {
-                const uint32_t s = seg0[r] + (blk - (kv >> shift));
-                if (s < (uint32_t)S.seg_cap) S.seg_tok[s] = (int)t;
+            req[i] = r;
+        }
+#pragma unroll
+        for (int i = 0; i < kTokPerThread; ++i) {
+            slot[i] = -1;
+            if (!stored[i]) continue;
+            const int blk = pos[i] >> shift, kv = kv0[req[i]];
+            const bool starts = (pos[i] & P1) == 0;
+            if (fresh[i] && starts) S.block_table[(int64_t)req[i] * S.max_blocks + blk] = page[i];
+            if ((unsigned)page[i] < (unsigned)S.n_pages) slot[i] = (page[i] << shift) + (pos[i] & P1);
+            else note_bad(S.work, req[i]);
+            if (pos[i] == kv || starts) {
+                const uint32_t place = seg0[req[i]] + (blk - (kv >> shift));
+                if (place < (uint32_t)S.seg_cap) S.seg_tok[place] = t0 + i;
             }
         }
         if (t0 + kTokPerThread <= S.t_cap) {
@@ -294,8 +363,14 @@ hipError_t launch_kv_plan(const rdg_kv_step& S, const int32_t* kv_len, const int
                           const int32_t* n_free, int32_t* n_free_out, hipStream_t s) {
     const int per_block = kThreads * kTokPerThread;
     const int blocks = S.t_cap > 0 ? (S.t_cap + per_block - 1) / per_block : 1;
-    const size_t bytes = sizeof(uint32_t) * (3 * (size_t)S.n_req + 1);
-    k_kv_plan<<<blocks, kThreads, bytes, s>>>(S, log2_of(S.page_rows), kv_len, q_len, free_list, n_free, n_free_out);
+    const size_t bytes = sizeof(uint32_t) * (4 * (size_t)S.n_req + 1);
+    const int shift = log2_of(S.page_rows);
+    if (S.n_req <= kThreads)
+        k_kv_plan<1><<<blocks, kThreads, bytes, s>>>(S, shift, kv_len, q_len, free_list, n_free, n_free_out);
+    else if (S.n_req <= 4 * kThreads)
+        k_kv_plan<4><<<blocks, kThreads, bytes, s>>>(S, shift, kv_len, q_len, free_list, n_free, n_free_out);
+    else
+        k_kv_plan<16><<<blocks, kThreads, bytes, s>>>(S, shift, kv_len, q_len, free_list, n_free, n_free_out);
     return hipGetLastError();
 }
 

@@ -226,7 +226,7 @@ hipError_t launch_combine_finish(const void* y, int y_dt, const int32_t* pos, in
                                  int rows_per_sig, hipStream_t s);
 
 // Paged key/value cache: step plan, query/key norm and store, attention.
-constexpr int kMaxRequests = 4096;  // per step: the plan scans them in LDS, 12 bytes each
+constexpr int kMaxRequests = 4096;  // per step: the plan scans them in LDS, 16 bytes each, 16 a thread
 hipError_t launch_kv_plan(const rdg_kv_step& S, const int32_t* kv_len, const int32_t* q_len, const int32_t* free_list,
                           const int32_t* n_free, int32_t* n_free_out, hipStream_t s);
 hipError_t launch_kv_trim(const rdg_kv_step& S, const int32_t* new_len, const int32_t* kv_len, int32_t* free_list,
