@@ -71,7 +71,7 @@ AttnPlan plan_attn(int T, int R, int n_kv, int group, int head_dim, bool bf16, i
         // Tiles of 256 rows convert each key's codes half as often (4% on a long
         // prefill), tiles of 128 fill the chip sooner and waste less on short requests.
         const auto units_of = [&](int bm) { return (double)n_kv * ceil((double)T * group / bm); };
-        p.tile_rows = head_dim == 256 || units_of(256) < kTileUnits ? 128 : 256;
+        p.tile_rows = head_dim == 256 || p.n_most > 0 || units_of(256) < kTileUnits ? 128 : 256;
         p.tile_slots = (int)((int64_t)T * group / p.tile_rows + R);
         const double units = units_of(p.tile_rows);
         double want = span + 64.0;
@@ -83,7 +83,7 @@ AttnPlan plan_attn(int T, int R, int n_kv, int group, int head_dim, bool bf16, i
     }
     if (p.n_most > 0) {
         const int64_t rows = (int64_t)p.n_most * group;
-        p.rt = rows <= 64 ? (int)((rows + 15) / 16) : 4;
+        p.rt = rows <= 64 && !tiles ? (int)((rows + 15) / 16) : 4;
         p.row_tiles = (int)((rows + 16 * p.rt - 1) / (16 * p.rt));
         const int most = kWaveKeys * (p.rt == 1 ? 4 : p.rt == 2 ? 2 : 1);
         const double units = (double)R * n_kv * p.row_tiles;
@@ -231,9 +231,7 @@ int rdg_paged_attention(const void* q, int dtype, int64_t q_stride, int T, int n
         a.part_o = static_cast<float*>(work);
         a.part_ml = a.part_o + (size_t)T * n_q * D * a.max_chunks;
     }
-    hipError_t e = hipSuccess;
-    if (p.tile_slots > 0) e = launch_attn_tiles(a, D, stream);
-    if (e == hipSuccess && p.n_most > 0) e = launch_attn_rows(a, D, bf16, stream);
+    hipError_t e = p.tile_slots > 0 ? launch_attn_tiles(a, D, stream) : launch_attn_rows(a, D, bf16, stream);
     if (e == hipSuccess && a.max_chunks > 1) e = launch_attn_join(a, D, bf16, stream);
     return hip_rc(e);
 }

@@ -1,0 +1,453 @@
+// Attention over the 8-bit paged cache, few query rows per request: decode,
+// drafted tokens, fp32 queries.
+//
+//   o_i = sum_j softmax_j(scale * q_i . k_j) v_j     lse_i = log sum_j exp(scale * q_i . k_j)
+//
+// over the keys that query i sees, in one pass with a running maximum and sum
+// (fp32, base-2 exponents).  Bound by HBM: every code is read once, 2 * head_dim
+// bytes per key and key head, and the G = n_q / n_kv query heads of a key head
+// share the read: the rows of a tile are (query token, head of the group).
+//
+// Nothing goes through LDS on the way in.  A wave computes
+//   S^T = K Q^T   16 keys x 16 rows per v_mfma_f32_16x16x32_bf16
+//   O^T = V^T P^T 16 columns x 16 rows, 32 keys per MFMA
+// and takes both operands from registers as the cache holds them: the order of
+// the reduction index is free, so a lane's 16 consecutive K codes serve two
+// MFMA steps, and the keys that S^T leaves in a lane (4 of each 16) are the
+// ones that its P^T operand holds, with V's 4-byte columns transposed by byte
+// permutes to match.  The codes become bf16 exactly, times their page's power
+// of two (v_cvt_scalef32_pk_bf16_fp8).  fp32 queries and probabilities go in as
+// three bf16 parts each, which carries 24 bits.
+//
+// A workgroup's waves are RT row tiles x KG key groups (4 x 1, 3 x 1, 2 x 2 or 1 x
+// 4): the key groups take the 64-key blocks of one chunk of one request's keys in
+// turn and join in LDS; the row tiles read the same blocks, which the first brings
+// into the caches (tiles held in one wave's registers instead ran 64 rows at half the speed).
+// Chunks of one row are joined by a second launch, in chunk order, so results
+// do not depend on scheduling.  A wave's next K block is in flight while its
+// softmax and V product run, and its next V block during the K product: 16 KB
+// a wave at head_dim 128.
+#pragma once
+#include "attn.h"
+
+namespace rdg {
+namespace {
+
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kBlock = 64;  // keys per wave and step
+
+template <int D>
+struct VWords {
+    static constexpr int n = D / 64;  // dwords of V per key and lane (D / 16 codes)
+};
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+    if constexpr (N == 1) {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (N == 2) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        w[0] = u.x, w[1] = u.y;
+    } else {
+        const uint4 u = *reinterpret_cast<const uint4*>(p);
+        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    }
+}
+
+// x as NS bf16 parts that sum to it (NS = 1: x rounded).
+template <int NS>
+__device__ __forceinline__ void split_bf16(float x, __bf16 (&part)[NS]) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        part[i] = (__bf16)x;
+        if (i + 1 < NS) x -= (float)part[i];
+    }
+}
+
+// NS = 1: bf16 queries and output; 3: fp32.  RT: 16-row tiles per workgroup.
+template <int RT>
+constexpr int key_groups() {
+    return RT == 1 ? 4 : RT == 2 ? 2 : 1;
+}
+
+template <int D, int RT>
+struct RowsLds {
+    // RT > 1: the codes of two steps of each key group; then the parts to be joined
+    static constexpr int KG = key_groups<RT>();
+    static constexpr int kCodes = RT > 1 ? KG * 2 * 2 * kBlock * D : 0, kParts = RT * KG * 16 * (D + 4) * 4;
+    uint8_t raw[kCodes > kParts ? kCodes : kParts];
+    float m[RT][KG][16], l[RT][KG][16];
+};
+
+// Workgroup `id` of RT * key_groups<RT>() waves.
+template <int D, int NS, int RT>
+__device__ __forceinline__ void attn_rows(const AttnCall& a, int id, RowsLds<D, RT>& lds) {
+    constexpr int KJ = D / 64, W = VWords<D>::n, U = D / 16;
+    constexpr int KG = key_groups<RT>();
+    auto& lds_raw = lds.raw;
+    auto& lds_m = lds.m;
+    auto& lds_l = lds.l;
+    auto& lds_o = *reinterpret_cast<float(*)[RT][KG][16][D + 4]>(lds_raw);
+    const int lane = lane_id(), w_id = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+    const int rt = w_id / KG, wave = w_id % KG;  // row tile, key group
+    const int col = lane & 15, g4 = lane >> 4;
+    const int head = id % a.n_kv;
+    id /= a.n_kv;
+    const int tile = id % a.row_tiles;
+    id /= a.row_tiles;
+    const int r = id % a.R, chunk = id / a.R;
+    const ReqSpan s = req_span(a, r);
+    const int G = a.group, rows = s.n * G, first = tile * 16 * RT;
+    if (first >= rows || s.n > a.n_most) return;
+    const int last = first + 16 * RT < rows ? first + 16 * RT - 1 : rows - 1;
+    const TileKeys keys = tile_keys(a, s, first, last + 1, a.chunk);
+    const int chunks = keys.chunks;
+    if (chunk >= chunks) return;
+    const int k0 = keys.begin + chunk * a.chunk;
+    // this wave's rows (none: those of the last row, not stored), keys that every one
+    // of them sees, and that any does
+    const int row0 = first + rt * 16;
+    const int i_first = (row0 < rows ? row0 : rows - 1) / G, i_last = (row0 + 15 < rows ? row0 + 15 : rows - 1) / G;
+    const int all_lo = key_lo(a, s, i_last), all_hi = key_hi(a, s, i_first);
+    const int any_lo = key_lo(a, s, i_first), any_hi = key_hi(a, s, i_last);
+    // one row tile: this wave's last key; more: the workgroup's, whose waves step together
+    const int end = RT > 1 ? keys.end : any_hi;
+    const int k1 = end < k0 + a.chunk ? end : k0 + a.chunk;
+
+    // queries: lane (row col, reduction group g4)
+    bf16x8_t q[2 * KJ][NS];
+    int hi, lo;
+    {
+        const int row = row0 + col;
+        const bool live = row < rows;
+        const int i = live ? row / G : 0, h = head * G + (live ? row % G : 0);
+        hi = key_hi(a, s, live ? i : i_last);
+        lo = key_lo(a, s, live ? i : i_last);
+        const int64_t at = (int64_t)(s.t0 + i) * a.q_stride + (int64_t)h * D + 16 * g4;
+#pragma unroll
+        for (int j = 0; j < KJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if constexpr (NS == 1) {
+                    bf16x8_t v = *reinterpret_cast<const bf16x8_t*>(static_cast<const uint16_t*>(a.q) + at + 64 * j + 8 * e);
+                    q[2 * j + e][0] = v;
+                } else {
+                    const float* f = static_cast<const float*>(a.q) + at + 64 * j + 8 * e;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        __bf16 part[NS];
+                        split_bf16<NS>(f[c], part);
+#pragma unroll
+                        for (int n = 0; n < NS; ++n) q[2 * j + e][n][c] = part[n];
+                    }
+                }
+            }
+    }
+
+    // page and scales of each of this wave's 16-key groups, one per lane
+    const int my_key = k0 + ((lane >> 2) * KG + wave) * kBlock + (lane & 3) * 16;
+    int my_page = 0;
+    float my_ks = 1.0f, my_vs = 1.0f;
+    if (my_key < k1) {
+        my_page = page_of(a, r, my_key);
+        my_ks = pow2_scale(a.k_scale[(int64_t)my_page * a.n_kv + head]);
+        my_vs = pow2_scale(a.v_scale[(int64_t)my_page * a.n_kv + head]);
+    }
+
+    f32x4_t o[U];
+    float m = -__builtin_inff(), l = 0.0f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) o[u] = f32x4_t{0, 0, 0, 0};
+
+    const int in_page = (1 << a.page_shift) - 1;
+    // RT = 1: codes straight into the registers that the products take them from
+    uint4 kreg[4][KJ];
+    uint32_t vreg[4][4][W];
+    const auto row_base = [&](int step, int t) -> int64_t {  // first code of a 16-key group's first row
+        const int page = __builtin_amdgcn_readlane(my_page, step * 4 + t);
+        const int key = k0 + (step * KG + wave) * kBlock + t * 16;
+        return ((((int64_t)page * a.n_kv + head) << a.page_shift) + (key & in_page)) * D;
+    };
+    const auto load_k = [&](int step) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const uint8_t* p = a.k_codes + row_base(step, t) + col * D + 16 * g4;
+#pragma unroll
+            for (int j = 0; j < KJ; ++j) kreg[t][j] = *reinterpret_cast<const uint4*>(p + 64 * j);
+        }
+    };
+    const auto load_v = [&](int step) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const uint8_t* p = a.v_codes + row_base(step, t) + 4 * g4 * D + col * (D / 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) load_words<W>(p + i * D, vreg[t][i]);
+        }
+    };
+    // RT > 1: the key group's waves share the loads, 16 bytes a lane along the rows, and
+    // pass them on through LDS; K's 16-byte pieces are swizzled by row and V's
+    // rows interleaved, so that the operands' reads fall into different banks
+    constexpr int PK = kBlock * D / 16, ST = RT * kWave, NP = (2 * PK + ST - 1) / ST;
+    const int sid = rt * kWave + lane;
+    u32x4_t stg[NP];
+    uint8_t* const lds_codes = lds_raw + wave * (2 * 2 * kBlock * D);
+    const auto k_place = [&](int key, int piece) {
+        const int turn = D == 64 ? (key >> 2) & 3 : D == 128 ? (key >> 1) & 7 : key & 15;
+        return key * D + 16 * (piece ^ turn);
+    };
+    const auto v_row = [&](int key) { return (key & ~15) | ((key & 3) << 2) | ((key >> 2) & 3); };
+    const auto fetch = [&](int step) {
+        const int kb = k0 + (step * KG + wave) * kBlock;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const int x = sid + p * ST, y = x % PK, key = y / (D / 16);
+            const int page = __shfl(my_page, step * 4 + key / 16);
+            const uint8_t* from = x < PK ? a.k_codes : a.v_codes;
+            if (2 * PK % ST == 0 || x < 2 * PK)
+                stg[p] = *reinterpret_cast<const u32x4_t*>(
+                    from + ((((int64_t)page * a.n_kv + head) << a.page_shift) + ((kb + key) & in_page)) * D +
+                    16 * (y % (D / 16)));
+        }
+    };
+    const auto pass_on = [&](int step) {
+        uint8_t* buf = lds_codes + (step & 1) * (2 * kBlock * D);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const int x = sid + p * ST, y = x % PK, key = y / (D / 16), piece = y % (D / 16);
+            if (2 * PK % ST == 0 || x < 2 * PK)
+                *reinterpret_cast<u32x4_t*>(buf + (x < PK ? k_place(key, piece) : kBlock * D + v_row(key) * D + 16 * piece)) =
+                    stg[p];
+        }
+    };
+    const auto take_k = [&](int step) {
+        const uint8_t* buf = lds_codes + (step & 1) * (2 * kBlock * D);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int j = 0; j < KJ; ++j)
+                kreg[t][j] = *reinterpret_cast<const uint4*>(buf + k_place(16 * t + col, 4 * j + g4));
+    };
+    const auto take_v = [&](int step) {
+        const uint8_t* buf = lds_codes + (step & 1) * (2 * kBlock * D) + kBlock * D;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                load_words<W>(buf + v_row(16 * t + 4 * g4 + i) * D + col * (D / 16), vreg[t][i]);
+    };
+
+    const int span = k1 - k0 - (RT > 1 ? 0 : wave * kBlock);
+    const int steps = span > 0 ? (span + KG * kBlock - 1) / (KG * kBlock) : 0;
+    if (steps > 0) {
+        if constexpr (RT > 1) {
+            fetch(0);
+            pass_on(0);
+            if (steps > 1) fetch(1);
+            __syncthreads();
+        } else {
+            load_k(0);
+            load_v(0);
+        }
+    }
+    const float c = a.scale_log2;
+    uint32_t saw_nan = 0;
+    for (int step = 0; step < steps; ++step) {
+        const int kb = k0 + (step * KG + wave) * kBlock;
+        if constexpr (RT > 1) take_k(step);
+        f32x4_t sc[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const float ks = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_ks), step * 4 + t));
+            sc[t] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < KJ; ++j) {
+                const bf16x8_t k_lo = codes_to_bf16(kreg[t][j].x, kreg[t][j].y, ks, ks);
+                const bf16x8_t k_hi = codes_to_bf16(kreg[t][j].z, kreg[t][j].w, ks, ks);
+#pragma unroll
+                    for (int n = NS - 1; n >= 0; --n) {  // small parts first
+                        sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k_lo, q[2 * j][n], sc[t], 0, 0, 0);
+                        sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k_hi, q[2 * j + 1][n], sc[t], 0, 0, 0);
+                    }
+            }
+        }
+        if constexpr (RT > 1) {
+            take_v(step);
+        } else {
+            if (step + 1 < steps) load_k(step + 1);
+        }
+
+        const bool masked = kb < all_lo || kb + kBlock > all_hi;
+        if (masked) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = kb + 16 * t + 4 * g4 + i;
+                        if (key < lo || key >= hi) sc[t][i] = -__builtin_inff();
+                    }
+            // keys that no row sees may hold anything
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int key = kb + 16 * t + 4 * g4 + i;
+                    const bool any = key >= any_lo && key < any_hi;
+#pragma unroll
+                    for (int w = 0; w < W; ++w) {
+                        vreg[t][i][w] = any ? vreg[t][i][w] : 0;
+                        const uint32_t nan = nan_bytes(vreg[t][i][w]);
+                        vreg[t][i][w] = without_nan(vreg[t][i][w], nan);
+                        saw_nan |= nan;
+                    }
+                }
+        }
+        bf16x8_t p[2][NS];
+        {
+            float top = -__builtin_inff();
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[t][i]);
+            top = max_quarters(top);
+            const float m_new = fmaxf(m, top * c);
+            if (__any(m_new > m + kSlack)) {
+                const float shrink = __builtin_amdgcn_exp2f(m - (m_new == -__builtin_inff() ? 0.0f : m_new));
+                l *= shrink;
+#pragma unroll
+                for (int u = 0; u < U; ++u) o[u] *= shrink;
+                m = m_new;
+            }
+            const float ref = m == -__builtin_inff() ? 0.0f : m;
+            float sum = 0.0f;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float e = __builtin_amdgcn_exp2f(fmaf(sc[t][i], c, -ref));
+                    sum += e;
+                    __bf16 part[NS];
+                    split_bf16<NS>(e, part);
+#pragma unroll
+                    for (int n = 0; n < NS; ++n) p[t / 2][n][(t & 1) * 4 + i] = part[n];
+                }
+            l += sum;
+        }
+        // O^T += V^T P^T; column of output tile u in lane col: col * U + u
+#pragma unroll
+        for (int t2 = 0; t2 < 2; ++t2) {
+            const float va = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_vs), step * 4 + 2 * t2));
+            const float vb = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_vs), step * 4 + 2 * t2 + 1));
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                uint32_t in[4], x[4], y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) in[i] = vreg[2 * t2][i][w];
+                transpose4(in, x);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) in[i] = vreg[2 * t2 + 1][i][w];
+                transpose4(in, y);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const bf16x8_t v = codes_to_bf16(x[b], y[b], va, vb);
+                    const int u = 4 * w + b;
+#pragma unroll
+                        for (int n = NS - 1; n >= 0; --n)
+                            o[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[t2][n], o[u], 0, 0, 0);
+                }
+            }
+        }
+        if constexpr (RT > 1) {
+            if (step + 1 < steps) pass_on(step + 1);
+            if (step + 2 < steps) fetch(step + 2);
+            __syncthreads();
+        } else {
+            if (step + 1 < steps) load_v(step + 1);
+        }
+    }
+
+    if (__any(saw_nan != 0)) {
+        for (int step = 0; step < steps; ++step) {
+            const int kb = k0 + (step * KG + wave) * kBlock;
+            if (kb >= all_lo && kb + kBlock <= all_hi) continue;
+            for (int j = kb; j < kb + kBlock && j < any_hi; ++j) {
+                const int page = page_of(a, r, j);
+                const uint8_t* p = a.v_codes +
+                    ((((int64_t)page * a.n_kv + head) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * D;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int w = 0; w < W; ++w) {
+                        const uint32_t nan = nan_bytes(*reinterpret_cast<const uint32_t*>(p + (4 * g4 + i) * U + 4 * w));
+#pragma unroll
+                            for (int b = 0; b < 4; ++b)
+                                if (j >= lo && j < hi && (nan >> (8 * b + 7) & 1))
+                                    o[4 * w + b][i] = __builtin_nanf("");
+                    }
+            }
+        }
+    }
+
+    const float sum = sum_quarters(l);
+    if constexpr (KG == 1) {  // no other wave has a part of these rows: out of the registers
+        const int row = row0 + col;
+        if (row >= rows) return;
+        const int i = row / G, h = head * G + row % G;
+        const bool none = key_hi(a, s, i) <= key_lo(a, s, i);
+        const int64_t at = ((int64_t)(s.t0 + i) * a.n_q + h) * a.max_chunks + chunk;
+        if (chunks > 1 && g4 == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(m, sum);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int u = 0; u < U; u += 4) {
+                const int d = (4 * g4 + x) * U + u;
+                const float4 v = make_float4(o[u][x], o[u + 1][x], o[u + 2][x], o[u + 3][x]);
+                if (chunks == 1) store_part<NS == 1>(a, s.t0 + i, h, d, D, v, sum, m, none);
+                else *reinterpret_cast<float4*>(a.part_o + at * D + d) = v;
+            }
+        return;
+    }
+    // the key groups' parts, joined in LDS
+    if (lane < 16) {
+        lds_m[rt][wave][col] = m;
+        lds_l[rt][wave][col] = sum;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int u = 0; u < U; u += 4)
+            *reinterpret_cast<float4*>(&lds_o[rt][wave][col][(4 * g4 + i) * U + u]) =
+                make_float4(o[u][i], o[u + 1][i], o[u + 2][i], o[u + 3][i]);
+    __syncthreads();
+    constexpr int TPR = D / 4;  // threads per row
+    for (int x = threadIdx.x; x < 16 * RT * TPR; x += RT * KG * kWave) {
+        const int rr = (x / TPR) & 15, ty = x / (16 * TPR), d = (x % TPR) * 4, row = first + x / TPR;
+        if (row >= rows) break;
+        float top = lds_m[ty][0][rr];
+#pragma unroll
+        for (int w = 1; w < KG; ++w) top = fmaxf(top, lds_m[ty][w][rr]);
+        const float ref = top == -__builtin_inff() ? 0.0f : top;
+        float total = 0.0f;
+        float4 acc = make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int w = 0; w < KG; ++w) {
+            const float f = __builtin_amdgcn_exp2f(lds_m[ty][w][rr] - ref);
+            total = fmaf(f, lds_l[ty][w][rr], total);
+            const float4 v = *reinterpret_cast<const float4*>(&lds_o[ty][w][rr][d]);
+            acc.x = fmaf(f, v.x, acc.x), acc.y = fmaf(f, v.y, acc.y);
+            acc.z = fmaf(f, v.z, acc.z), acc.w = fmaf(f, v.w, acc.w);
+        }
+        const int i = row / G, h = head * G + row % G;
+        if (chunks == 1) {
+            const bool none = key_hi(a, s, i) <= key_lo(a, s, i);
+            store_part<NS == 1>(a, s.t0 + i, h, d, D, acc, total, top, none);
+        } else {
+            const int64_t at = ((int64_t)(s.t0 + i) * a.n_q + h) * a.max_chunks + chunk;
+            *reinterpret_cast<float4*>(a.part_o + at * D + d) = acc;
+            if (d == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(top, total);
+        }
+    }
+}
+
+}  // namespace
+}  // namespace rdg

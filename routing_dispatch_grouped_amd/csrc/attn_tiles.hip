@@ -21,7 +21,7 @@
 // from a request's last to its first, longest work first.
 #include <type_traits>
 
-#include "attn.h"
+#include "attn_rows.h"
 
 namespace rdg {
 namespace {
@@ -51,19 +51,16 @@ __device__ __forceinline__ int k_piece(int key, int c) {
 }
 __device__ __forceinline__ int v_piece(int d, int c) { return c ^ (((d >> 1) & 7) ^ ((d >> 4) & 1)); }
 
+// Workgroup `id` of NW waves.
 template <int D, int NW, int RB>
-__global__ __launch_bounds__(NW * kWave, NW == 4 && D < 256 ? 2 : 1) void k_attn_tiles(AttnCall a) {
+__device__ __forceinline__ void attn_tiles(const AttnCall& a, int id, TileLds<D>& lds) {
     constexpr int NT = NW * kWave, BM = 32 * RB * NW;
     constexpr int KS = D / 16, DB = D / 32;  // reduction steps of S^T, 32-row blocks of O^T
     // Staging, per thread: KU pieces of 16 K codes, VU of 8 keys x 4 columns of V.
     constexpr int KP = kTile * D / 16, VP = 8 * D / 4;
     constexpr int KU = (KP + NT - 1) / NT, VU = (VP + NT - 1) / NT;
-    extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
-    auto& lds = *reinterpret_cast<TileLds<D>*>(lds_raw);
-
     const int tid = (int)threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int col = lane & 31, half = lane >> 5;
-    int id = (int)blockIdx.x;
     const int head = id % a.n_kv;
     id /= a.n_kv;
     const int slot = a.tile_slots - 1 - id % a.tile_slots, chunk = id / a.tile_slots;
@@ -456,23 +453,60 @@ __global__ __launch_bounds__(NW * kWave, NW == 4 && D < 256 ? 2 : 1) void k_attn
     }
 }
 
-template <int D, int NW, int RB>
+template <int D, int NW>
+__global__ __launch_bounds__(NW * kWave, NW == 4 && D < 256 ? 2 : 1) void k_attn_tiles(AttnCall a) {
+    extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
+    attn_tiles<D, NW, 1>(a, (int)blockIdx.x, *reinterpret_cast<TileLds<D>*>(lds_raw));
+}
+
+// A mixed batch in one launch: the long requests' tiles, then the short ones'
+// rows, which fill the CUs beside them (one after the other they took 28 + 9 us
+// of a window-1024 batch of 24 chunks and decode rows).
+template <int D>
+__global__ __launch_bounds__(4 * kWave, D < 256 ? 2 : 1) void k_attn_mixed(AttnCall a, int tile_blocks) {
+    extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
+    const int id = (int)blockIdx.x;
+    if (id < tile_blocks) attn_tiles<D, 4, 1>(a, id, *reinterpret_cast<TileLds<D>*>(lds_raw));
+    else attn_rows<D, 1, 4>(a, id - tile_blocks, *reinterpret_cast<RowsLds<D, 4>*>(lds_raw));
+}
+
+int64_t tile_blocks(const AttnCall& a) { return (int64_t)a.n_kv * a.tile_slots * a.tile_chunks; }
+
+template <int D, int NW>
 hipError_t launch(const AttnCall& a, hipStream_t s) {
-    constexpr size_t bytes = sizeof(TileLds<D>);
-    static_assert(bytes <= 160 * 1024, "LDS");
-    const int64_t grid = (int64_t)a.n_kv * a.tile_slots * a.tile_chunks;
+    static_assert(sizeof(TileLds<D>) <= 160 * 1024, "LDS");
+    const int64_t grid = tile_blocks(a);
     if (grid >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;
-    k_attn_tiles<D, NW, RB><<<(unsigned)grid, NW * kWave, bytes, s>>>(a);
+    k_attn_tiles<D, NW><<<(unsigned)grid, NW * kWave, sizeof(TileLds<D>), s>>>(a);
     return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_mixed(const AttnCall& a, hipStream_t s) {
+    constexpr size_t bytes = sizeof(TileLds<D>) > sizeof(RowsLds<D, 4>) ? sizeof(TileLds<D>) : sizeof(RowsLds<D, 4>);
+    const int64_t tiles = tile_blocks(a), grid = tiles + (int64_t)a.n_kv * a.row_tiles * a.R * a.row_chunks;
+    if (grid >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;
+    k_attn_mixed<D><<<(unsigned)grid, 4 * kWave, bytes, s>>>(a, (int)tiles);
+    return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_d(const AttnCall& a, hipStream_t s) {
+    if (a.n_most > 0) return launch_mixed<D>(a, s);
+    if constexpr (D < 256) {
+        if (a.tile_rows == 256) return launch<D, 8>(a, s);
+    }
+    return launch<D, 4>(a, s);
 }
 
 }  // namespace
 
+// With short requests too (n_most > 0): 128-row tiles and 64-row workgroups.
 hipError_t launch_attn_tiles(const AttnCall& a, int head_dim, hipStream_t s) {
     switch (head_dim) {
-        case 64: return a.tile_rows == 256 ? launch<64, 8, 1>(a, s) : launch<64, 4, 1>(a, s);
-        case 128: return a.tile_rows == 256 ? launch<128, 8, 1>(a, s) : launch<128, 4, 1>(a, s);
-        default: return launch<256, 4, 1>(a, s);
+        case 64: return launch_d<64>(a, s);
+        case 128: return launch_d<128>(a, s);
+        default: return launch_d<256>(a, s);
     }
 }
 
