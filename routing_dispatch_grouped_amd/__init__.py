@@ -114,24 +114,22 @@ def _check(rc, what):
         raise RdgError(rc, what)
 
 
-_torch = None
+# torch and its current-stream lookup, bound at the first call: the small calls
+# of a decode step take as long on the host as on the GPU.
+_torch = _stream_of = _device_of = None
 
 
-def _torch_module():
-    """torch, imported once: the small calls of a decode step are timed by their host side."""
-    global _torch
-    if _torch is None:
-        import torch
-        _torch = torch
-    return _torch
+def _bind_torch():
+    global _torch, _stream_of, _device_of
+    import torch
+    _stream_of, _device_of = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _torch = torch
+    return torch
 
 
 def _raw_stream(stream):
     """The HIP stream as an integer (None: torch's current one)."""
-    if stream is not None:
-        return stream.cuda_stream
-    c = _torch_module()._C
-    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+    return _stream_of(_device_of()) if stream is None else stream.cuda_stream
 
 
 # ------------------------------------------------------------------ layout
@@ -167,12 +165,12 @@ class Layout:
         return ctypes.byref(self.c)
 
 
-def _tensor(t, what, dtype, shape):
+def _tensor(t, what, dtype, n):
     """The address of a tensor that the C call reads as it is: refuses another
-    element type or size than the call assumes, and one that is not contiguous."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise RdgError(RDG_EINVAL, "%s: want a contiguous %s tensor of shape %s, got %s %s" %
-                       (what, dtype, list(shape), t.dtype, list(t.shape)))
+    element type or number than the call assumes, and one that is not contiguous."""
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        raise RdgError(RDG_EINVAL, "%s: want a contiguous %s tensor of %d elements, got %s %s" %
+                       (what, dtype, n, t.dtype, list(t.shape)))
     return t.data_ptr()
 
 
@@ -182,15 +180,15 @@ class KvCache:
 
     def __init__(self, k, v, k_scale, v_scale):
         import torch
-        if k.dim() != 4:
-            raise RdgError(RDG_EINVAL, "KvCache: k has to be [n_pages, n_kv, page_rows, head_dim]")
+        if k.dim() != 4 or v.shape != k.shape:
+            raise RdgError(RDG_EINVAL, "KvCache: k and v have to be [n_pages, n_kv, page_rows, head_dim]")
         n_pages, n_kv, page_rows, head_dim = k.shape
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_pages, self.n_kv, self.page_rows, self.head_dim = n_pages, n_kv, page_rows, head_dim
-        self.c = rdg_kv_cache(n_pages, page_rows, n_kv, head_dim, _tensor(k, "KvCache.k", torch.uint8, k.shape),
-                              _tensor(v, "KvCache.v", torch.uint8, k.shape),
-                              _tensor(k_scale, "KvCache.k_scale", torch.float32, (n_pages, n_kv)),
-                              _tensor(v_scale, "KvCache.v_scale", torch.float32, (n_pages, n_kv)))
+        self.c = rdg_kv_cache(n_pages, page_rows, n_kv, head_dim, _tensor(k, "KvCache.k", torch.uint8, k.numel()),
+                              _tensor(v, "KvCache.v", torch.uint8, k.numel()),
+                              _tensor(k_scale, "KvCache.k_scale", torch.float32, n_pages * n_kv),
+                              _tensor(v_scale, "KvCache.v_scale", torch.float32, n_pages * n_kv))
         self.ref = ctypes.byref(self.c)
 
     @classmethod
@@ -394,58 +392,59 @@ def rdg_fill_i32(p, value, stream=None):
 
 def rdg_kv_plan(step, kv_len, q_len, free_list, n_free, n_free_out, stream=None):
     """kv_len, q_len [n_req], free_list [>= n_free], n_free, n_free_out [1]: int32 device tensors."""
-    i32, R = _torch_module().int32, (step.n_req,)
+    i32, R = (_torch or _bind_torch()).int32, step.n_req
     _check(_lib.rdg_kv_plan(step.ref, _tensor(kv_len, "rdg_kv_plan: kv_len", i32, R),
                             _tensor(q_len, "rdg_kv_plan: q_len", i32, R),
-                            _tensor(free_list, "rdg_kv_plan: free_list", i32, (free_list.numel(),)),
-                            _tensor(n_free, "rdg_kv_plan: n_free", i32, (1,)),
-                            _tensor(n_free_out, "rdg_kv_plan: n_free_out", i32, (1,)), _raw_stream(stream)),
+                            _tensor(free_list, "rdg_kv_plan: free_list", i32, free_list.numel()),
+                            _tensor(n_free, "rdg_kv_plan: n_free", i32, 1),
+                            _tensor(n_free_out, "rdg_kv_plan: n_free_out", i32, 1), _raw_stream(stream)),
            "rdg_kv_plan")
 
 
 def rdg_kv_trim(step, kv_len, new_len, free_list, n_free, n_free_out, stream=None):
     """kv_len, new_len [n_req], free_list [n_pages], n_free, n_free_out [1]: int32 device tensors."""
-    i32, R = _torch_module().int32, (step.n_req,)
+    i32, R = (_torch or _bind_torch()).int32, step.n_req
     _check(_lib.rdg_kv_trim(step.ref, _tensor(kv_len, "rdg_kv_trim: kv_len", i32, R),
                             _tensor(new_len, "rdg_kv_trim: new_len", i32, R),
-                            _tensor(free_list, "rdg_kv_trim: free_list", i32, (step.n_pages,)),
-                            _tensor(n_free, "rdg_kv_trim: n_free", i32, (1,)),
-                            _tensor(n_free_out, "rdg_kv_trim: n_free_out", i32, (1,)), _raw_stream(stream)),
+                            _tensor(free_list, "rdg_kv_trim: free_list", i32, step.n_pages),
+                            _tensor(n_free, "rdg_kv_trim: n_free", i32, 1),
+                            _tensor(n_free_out, "rdg_kv_trim: n_free_out", i32, 1), _raw_stream(stream)),
            "rdg_kv_trim")
 
 
 def _rows(t, what, heads, head_dim):
-    """dtype code and token stride of [T, heads * head_dim] or [T, heads, head_dim] rows; tokens may be apart."""
-    torch = _torch_module()
-    code = RDG_BF16 if t.dtype is torch.bfloat16 else RDG_F32 if t.dtype is torch.float32 else None
-    shape, stride = t.shape, t.stride()
+    """(dtype code, tokens, token stride) of [T, heads * head_dim] or [T, heads, head_dim] rows; tokens may be apart."""
+    torch = _torch or _bind_torch()
+    dt, shape, stride = t.dtype, t.shape, t.stride()
+    code = RDG_BF16 if dt is torch.bfloat16 else RDG_F32 if dt is torch.float32 else None
     if len(shape) == 3:
         fits = shape[1] == heads and shape[2] == head_dim and stride[2] == 1 and (stride[1] == head_dim or heads == 1)
     else:
         fits = len(shape) == 2 and shape[1] == heads * head_dim and stride[1] == 1
     if code is None or not fits:
         raise RdgError(RDG_EINVAL, "%s: want bfloat16 or float32 rows of %d heads of %d, got %s %s with strides %s" %
-                       (what, heads, head_dim, t.dtype, list(shape), list(stride)))
-    return code, stride[0] if shape[0] > 1 else heads * head_dim
+                       (what, heads, head_dim, dt, list(shape), list(stride)))
+    T = shape[0]
+    return code, T, stride[0] if T > 1 else heads * head_dim
 
 
 def rdg_qk_norm_rope_store(qkv, n_q, n_kv, head_dim, q_weight, k_weight, eps, cos_sin, rot_dim, neighbours, step, cache,
                            q_out, stream=None):
     """qkv [T, (n_q + 2 n_kv) * head_dim] (token stride free), q_out [T, n_q, head_dim], weights [head_dim] float32
     or None, cos_sin [n_pos, rot_dim] float32 or None; cache None with n_kv = 0."""
-    f32, T = _torch_module().float32, qkv.shape[0]
-    dt, stride = _rows(qkv, "rdg_qk_norm_rope_store: qkv", n_q + 2 * n_kv, head_dim)
+    f32 = (_torch or _bind_torch()).float32
+    dt, T, stride = _rows(qkv, "rdg_qk_norm_rope_store: qkv", n_q + 2 * n_kv, head_dim)
     q_stride, q_ptr, n_pos, cs_ptr = 0, None, 0, None
     if n_q > 0:
-        q_dt, q_stride = _rows(q_out, "rdg_qk_norm_rope_store: q_out", n_q, head_dim)
-        if q_dt != dt or q_out.shape[0] != T:
+        q_dt, q_T, q_stride = _rows(q_out, "rdg_qk_norm_rope_store: q_out", n_q, head_dim)
+        if q_dt != dt or q_T != T:
             raise RdgError(RDG_EINVAL, "rdg_qk_norm_rope_store: q_out differs from qkv in type or tokens")
         q_ptr = q_out.data_ptr()
-    wq = None if q_weight is None else _tensor(q_weight, "rdg_qk_norm_rope_store: q_weight", f32, (head_dim,))
-    wk = None if k_weight is None else _tensor(k_weight, "rdg_qk_norm_rope_store: k_weight", f32, (head_dim,))
+    wq = None if q_weight is None else _tensor(q_weight, "rdg_qk_norm_rope_store: q_weight", f32, head_dim)
+    wk = None if k_weight is None else _tensor(k_weight, "rdg_qk_norm_rope_store: k_weight", f32, head_dim)
     if rot_dim:
         n_pos = cos_sin.shape[0]
-        cs_ptr = _tensor(cos_sin, "rdg_qk_norm_rope_store: cos_sin", f32, (n_pos, rot_dim))
+        cs_ptr = _tensor(cos_sin, "rdg_qk_norm_rope_store: cos_sin", f32, n_pos * rot_dim)
     _check(_lib.rdg_qk_norm_rope_store(qkv.data_ptr(), dt, stride, T, n_q, n_kv, head_dim, wq, wk, eps, cs_ptr, n_pos,
                                        rot_dim, 1 if neighbours else 0, step.ref, None if cache is None else cache.ref,
                                        q_ptr, q_stride, _raw_stream(stream)), "rdg_qk_norm_rope_store")
@@ -459,12 +458,12 @@ def rdg_paged_attention(q, step, cache, max_q, max_kv, scale, out, lse=None, wor
                         stream=None):
     """q, out [T, n_q, head_dim] (token strides free), lse [T, n_q] float32 or None; work: a uint8 tensor of
     rdg_paged_attention_workspace_bytes."""
-    T, n_q = q.shape[0], q.shape[1]
-    dt, q_stride = _rows(q, "rdg_paged_attention: q", n_q, cache.head_dim)
-    out_dt, out_stride = _rows(out, "rdg_paged_attention: out", n_q, cache.head_dim)
-    if out_dt != dt or out.shape[0] != T:
+    n_q = q.shape[1]
+    dt, T, q_stride = _rows(q, "rdg_paged_attention: q", n_q, cache.head_dim)
+    out_dt, out_T, out_stride = _rows(out, "rdg_paged_attention: out", n_q, cache.head_dim)
+    if out_dt != dt or out_T != T:
         raise RdgError(RDG_EINVAL, "rdg_paged_attention: out differs from q in type or tokens")
-    lse_ptr = None if lse is None else _tensor(lse, "rdg_paged_attention: lse", _torch_module().float32, (T, n_q))
+    lse_ptr = None if lse is None else _tensor(lse, "rdg_paged_attention: lse", (_torch or _bind_torch()).float32, T * n_q)
     work_ptr, work_bytes = (None, 0) if work is None else (work.data_ptr(), work.nbytes)
     _check(_lib.rdg_paged_attention(q.data_ptr(), dt, q_stride, T, n_q, step.ref, cache.ref, max_q, max_kv, scale,
                                     1 if causal else 0, window, out.data_ptr(), out_stride, lse_ptr, work_ptr, work_bytes,

@@ -131,7 +131,9 @@ def test_binding_refuses_tensors_it_would_misread():
     with pytest.raises(rdg.RdgError):
         rdg.rdg_kv_trim(step, ok[0], ok[1], torch.zeros(8, **i32), ok[3], ok[4])   # not room for every page
     with pytest.raises(rdg.RdgError):
-        rdg.KvCache(torch.zeros(9, 2, 16, 64, dtype=torch.int8), *[None] * 3)
+        rdg.KvCache(torch.zeros(9, 2, 16, 64, dtype=torch.int8), torch.zeros(9, 2, 16, 64, dtype=torch.int8), None, None)
+    with pytest.raises(rdg.RdgError):
+        rdg.KvCache(torch.zeros(9, 2, 16, 64, dtype=torch.uint8), torch.zeros(9, 2, 64, 16, dtype=torch.uint8), None, None)
     cache = rdg.KvCache.empty(9, 2, 16, 64, "cpu")
     q = torch.zeros(5, 4, 64, dtype=torch.bfloat16)
     for bad_q, bad_out in ((q.half(), q), (q.transpose(1, 2), q), (q, q.float()), (q, q[:4]), (q[..., :32], q)):
