@@ -5,7 +5,7 @@ namespace rdg {
 namespace {
 
 template <int D, int NS, int RT>
-__global__ __launch_bounds__((RT * key_groups<RT>() * kWave), 1) void k_attn_rows(AttnCall a) {
+__global__ __launch_bounds__((RT * key_groups<RT>() * kWave), D < 256 && NS == 1 ? 2 : 1) void k_attn_rows(AttnCall a) {
     __shared__ __attribute__((aligned(16))) RowsLds<D, RT> lds;
     attn_rows<D, NS, RT>(a, (int)blockIdx.x, lds);
 }

@@ -35,7 +35,12 @@ namespace {
 
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kBlock = 64;  // keys per wave and step
+// Keys per wave and step: 64, or 32 of wide heads, whose codes in flight would
+// else take 128 registers.
+template <int D>
+constexpr int step_keys() {
+    return D == 256 ? 32 : 64;
+}
 
 template <int D>
 struct VWords {
@@ -73,9 +78,9 @@ constexpr int key_groups() {
 
 template <int D, int RT>
 struct RowsLds {
-    // RT > 1: the codes of two steps of each key group; then the parts to be joined
+    // the codes of a step (RT > 1: of two) of each key group; then the parts to be joined
     static constexpr int KG = key_groups<RT>();
-    static constexpr int kCodes = RT > 1 ? KG * 2 * 2 * kBlock * D : 0, kParts = RT * KG * 16 * (D + 4) * 4;
+    static constexpr int kCodes = KG * (RT > 1 ? 2 : 1) * 2 * step_keys<D>() * D, kParts = RT * KG * 16 * (D + 4) * 4;
     uint8_t raw[kCodes > kParts ? kCodes : kParts];
     float m[RT][KG][16], l[RT][KG][16];
 };
@@ -84,7 +89,7 @@ struct RowsLds {
 template <int D, int NS, int RT>
 __device__ __forceinline__ void attn_rows(const AttnCall& a, int id, RowsLds<D, RT>& lds) {
     constexpr int KJ = D / 64, W = VWords<D>::n, U = D / 16;
-    constexpr int KG = key_groups<RT>();
+    constexpr int KG = key_groups<RT>(), kBlock = step_keys<D>(), GP = kBlock / 16;  // 16-key groups of a step
     auto& lds_raw = lds.raw;
     auto& lds_m = lds.m;
     auto& lds_l = lds.l;
@@ -146,7 +151,7 @@ __device__ __forceinline__ void attn_rows(const AttnCall& a, int id, RowsLds<D, 
     }
 
     // page and scales of each of this wave's 16-key groups, one per lane
-    const int my_key = k0 + ((lane >> 2) * KG + wave) * kBlock + (lane & 3) * 16;
+    const int my_key = k0 + (lane / GP * KG + wave) * kBlock + lane % GP * 16;
     int my_page = 0;
     float my_ks = 1.0f, my_vs = 1.0f;
     if (my_key < k1) {
@@ -160,38 +165,17 @@ __device__ __forceinline__ void attn_rows(const AttnCall& a, int id, RowsLds<D, 
 #pragma unroll
     for (int u = 0; u < U; ++u) o[u] = f32x4_t{0, 0, 0, 0};
 
-    const int in_page = (1 << a.page_shift) - 1;
-    // RT = 1: codes straight into the registers that the products take them from
-    uint4 kreg[4][KJ];
-    uint32_t vreg[4][4][W];
-    const auto row_base = [&](int step, int t) -> int64_t {  // first code of a 16-key group's first row
-        const int page = __builtin_amdgcn_readlane(my_page, step * 4 + t);
-        const int key = k0 + (step * KG + wave) * kBlock + t * 16;
-        return ((((int64_t)page * a.n_kv + head) << a.page_shift) + (key & in_page)) * D;
-    };
-    const auto load_k = [&](int step) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const uint8_t* p = a.k_codes + row_base(step, t) + col * D + 16 * g4;
-#pragma unroll
-            for (int j = 0; j < KJ; ++j) kreg[t][j] = *reinterpret_cast<const uint4*>(p + 64 * j);
-        }
-    };
-    const auto load_v = [&](int step) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const uint8_t* p = a.v_codes + row_base(step, t) + 4 * g4 * D + col * (D / 16);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) load_words<W>(p + i * D, vreg[t][i]);
-        }
-    };
-    // RT > 1: the key group's waves share the loads, 16 bytes a lane along the rows, and
-    // pass them on through LDS; K's 16-byte pieces are swizzled by row and V's
-    // rows interleaved, so that the operands' reads fall into different banks
+    // The key group's waves share the loads -- 16-key groups are contiguous, so
+    // each instruction reads a KiB in a row -- and pass the codes on through LDS;
+    // K's 16-byte pieces are swizzled by row and V's rows interleaved, so that
+    // the operands' reads fall into different banks.
     constexpr int PK = kBlock * D / 16, ST = RT * kWave, NP = (2 * PK + ST - 1) / ST;
-    const int sid = rt * kWave + lane;
+    constexpr int kBufs = RT > 1 ? 2 : 1;  // a wave on its own reads what it wrote in order
+    const int in_page = (1 << a.page_shift) - 1;
+    uint4 kreg[GP][KJ];
+    uint32_t vreg[GP][4][W];
     u32x4_t stg[NP];
-    uint8_t* const lds_codes = lds_raw + wave * (2 * 2 * kBlock * D);
+    uint8_t* const lds_codes = lds_raw + wave * (kBufs * 2 * kBlock * D);
     const auto k_place = [&](int key, int piece) {
         const int turn = D == 64 ? (key >> 2) & 3 : D == 128 ? (key >> 1) & 7 : key & 15;
         return key * D + 16 * (piece ^ turn);
@@ -201,37 +185,37 @@ __device__ __forceinline__ void attn_rows(const AttnCall& a, int id, RowsLds<D, 
         const int kb = k0 + (step * KG + wave) * kBlock;
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            const int x = sid + p * ST, y = x % PK, key = y / (D / 16);
-            const int page = __shfl(my_page, step * 4 + key / 16);
-            const uint8_t* from = x < PK ? a.k_codes : a.v_codes;
-            if (2 * PK % ST == 0 || x < 2 * PK)
-                stg[p] = *reinterpret_cast<const u32x4_t*>(
-                    from + ((((int64_t)page * a.n_kv + head) << a.page_shift) + ((kb + key) & in_page)) * D +
-                    16 * (y % (D / 16)));
+            const int u = rt * kWave + p * ST;  // of the wave's first lane: one 16-key group for all
+            if (2 * PK % ST == 0 || u < 2 * PK) {
+                const int y = u % PK, g = y / D, page = __builtin_amdgcn_readlane(my_page, step * GP + g);
+                const uint8_t* from = (u < PK ? a.k_codes : a.v_codes) +
+                    ((((int64_t)page * a.n_kv + head) << a.page_shift) + ((kb + 16 * g) & in_page)) * D + y % D * 16;
+                stg[p] = *reinterpret_cast<const u32x4_t*>(from + 16 * lane);
+            }
         }
     };
     const auto pass_on = [&](int step) {
-        uint8_t* buf = lds_codes + (step & 1) * (2 * kBlock * D);
+        uint8_t* buf = lds_codes + step % kBufs * (2 * kBlock * D);
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            const int x = sid + p * ST, y = x % PK, key = y / (D / 16), piece = y % (D / 16);
-            if (2 * PK % ST == 0 || x < 2 * PK)
-                *reinterpret_cast<u32x4_t*>(buf + (x < PK ? k_place(key, piece) : kBlock * D + v_row(key) * D + 16 * piece)) =
+            const int u = rt * kWave + p * ST, y = u % PK + lane, key = y / (D / 16), piece = y % (D / 16);
+            if (2 * PK % ST == 0 || u < 2 * PK)
+                *reinterpret_cast<u32x4_t*>(buf + (u < PK ? k_place(key, piece) : kBlock * D + v_row(key) * D + 16 * piece)) =
                     stg[p];
         }
     };
     const auto take_k = [&](int step) {
-        const uint8_t* buf = lds_codes + (step & 1) * (2 * kBlock * D);
+        const uint8_t* buf = lds_codes + step % kBufs * (2 * kBlock * D);
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < GP; ++t)
 #pragma unroll
             for (int j = 0; j < KJ; ++j)
                 kreg[t][j] = *reinterpret_cast<const uint4*>(buf + k_place(16 * t + col, 4 * j + g4));
     };
     const auto take_v = [&](int step) {
-        const uint8_t* buf = lds_codes + (step & 1) * (2 * kBlock * D) + kBlock * D;
+        const uint8_t* buf = lds_codes + step % kBufs * (2 * kBlock * D) + kBlock * D;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < GP; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 load_words<W>(buf + v_row(16 * t + 4 * g4 + i) * D + col * (D / 16), vreg[t][i]);
@@ -240,25 +224,26 @@ __device__ __forceinline__ void attn_rows(const AttnCall& a, int id, RowsLds<D, 
     const int span = k1 - k0 - (RT > 1 ? 0 : wave * kBlock);
     const int steps = span > 0 ? (span + KG * kBlock - 1) / (KG * kBlock) : 0;
     if (steps > 0) {
+        fetch(0);
         if constexpr (RT > 1) {
-            fetch(0);
             pass_on(0);
             if (steps > 1) fetch(1);
             __syncthreads();
-        } else {
-            load_k(0);
-            load_v(0);
         }
     }
     const float c = a.scale_log2;
     uint32_t saw_nan = 0;
     for (int step = 0; step < steps; ++step) {
         const int kb = k0 + (step * KG + wave) * kBlock;
-        if constexpr (RT > 1) take_k(step);
-        f32x4_t sc[4];
+        if constexpr (RT == 1) {
+            pass_on(step);
+            if (step + 1 < steps) fetch(step + 1);
+        }
+        take_k(step);
+        f32x4_t sc[GP];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const float ks = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_ks), step * 4 + t));
+        for (int t = 0; t < GP; ++t) {
+            const float ks = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_ks), step * GP + t));
             sc[t] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
             for (int j = 0; j < KJ; ++j) {
@@ -271,16 +256,11 @@ __device__ __forceinline__ void attn_rows(const AttnCall& a, int id, RowsLds<D, 
                     }
             }
         }
-        if constexpr (RT > 1) {
-            take_v(step);
-        } else {
-            if (step + 1 < steps) load_k(step + 1);
-        }
-
+        take_v(step);
         const bool masked = kb < all_lo || kb + kBlock > all_hi;
         if (masked) {
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
+                for (int t = 0; t < GP; ++t)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int key = kb + 16 * t + 4 * g4 + i;
@@ -288,7 +268,7 @@ __device__ __forceinline__ void attn_rows(const AttnCall& a, int id, RowsLds<D, 
                     }
             // keys that no row sees may hold anything
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < GP; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int key = kb + 16 * t + 4 * g4 + i;
@@ -302,11 +282,11 @@ __device__ __forceinline__ void attn_rows(const AttnCall& a, int id, RowsLds<D, 
                     }
                 }
         }
-        bf16x8_t p[2][NS];
+        bf16x8_t p[GP / 2][NS];
         {
             float top = -__builtin_inff();
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < GP; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[t][i]);
             top = max_quarters(top);
@@ -321,7 +301,7 @@ __device__ __forceinline__ void attn_rows(const AttnCall& a, int id, RowsLds<D, 
             const float ref = m == -__builtin_inff() ? 0.0f : m;
             float sum = 0.0f;
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < GP; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float e = __builtin_amdgcn_exp2f(fmaf(sc[t][i], c, -ref));
@@ -335,9 +315,9 @@ __device__ __forceinline__ void attn_rows(const AttnCall& a, int id, RowsLds<D, 
         }
         // O^T += V^T P^T; column of output tile u in lane col: col * U + u
 #pragma unroll
-        for (int t2 = 0; t2 < 2; ++t2) {
-            const float va = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_vs), step * 4 + 2 * t2));
-            const float vb = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_vs), step * 4 + 2 * t2 + 1));
+        for (int t2 = 0; t2 < GP / 2; ++t2) {
+            const float va = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_vs), step * GP + 2 * t2));
+            const float vb = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_vs), step * GP + 2 * t2 + 1));
 #pragma unroll
             for (int w = 0; w < W; ++w) {
                 uint32_t in[4], x[4], y[4];
@@ -361,8 +341,6 @@ __device__ __forceinline__ void attn_rows(const AttnCall& a, int id, RowsLds<D, 
             if (step + 1 < steps) pass_on(step + 1);
             if (step + 2 < steps) fetch(step + 2);
             __syncthreads();
-        } else {
-            if (step + 1 < steps) load_v(step + 1);
         }
     }
 
@@ -407,7 +385,8 @@ __device__ __forceinline__ void attn_rows(const AttnCall& a, int id, RowsLds<D, 
             }
         return;
     }
-    // the key groups' parts, joined in LDS
+    // the key groups' parts, joined in LDS where their codes were
+    __syncthreads();
     if (lane < 16) {
         lds_m[rt][wave][col] = m;
         lds_l[rt][wave][col] = sum;
