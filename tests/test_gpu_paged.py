@@ -436,7 +436,12 @@ ATTNS = [
     ([520, 77, 1], [300, 1, 1], 128, 4, 1, 128),
     ([2, 0, 3], [6, 4, 3], 16, 8, 4, 64),               # more queries than keys: the first see nothing
     ([600], [2], 64, 64, 1, 128),
+    ([1300], [1300], 16, 2, 1, 64),                     # more than 1024 keys in one tile's walk
+    ([3000, 40], [40, 40], 32, 8, 2, 128),              # few tiles: their keys are split too
+    ([2100, 1, 0], [33, 1, 0], 128, 4, 1, 256),
 ]
+# long and short requests together, for each width
+MIXES = [([400, 70, 9, 0, 33, 1200], [150, 1, 9, 0, 3, 2], 16, 8, 2, D) for D in (64, 128, 256)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -457,6 +462,50 @@ def test_attention_with_a_window(case, window, dtype):
     out, lse = call(c, 0.1, window=window)
     assert c["m"].rdg_check_status(c["step"]) == (0, 0)
     check(c, out, lse, 0.1, window=window)
+
+
+@pytest.mark.parametrize("window", [0, 50])
+@pytest.mark.parametrize("case", range(len(MIXES)))
+def test_mixed_batches(case, window):
+    c = attn_case(*MIXES[case], "bf16", 70 + case)
+    out, lse = call(c, 0.1, window=window)
+    assert c["m"].rdg_check_status(c["step"]) == (0, 0)
+    check(c, out, lse, 0.1, window=window)
+
+
+def test_more_requests_than_lanes():
+    rng = np.random.default_rng(7)
+    kv = rng.integers(0, 90, 150)
+    q = np.minimum(kv, np.where(rng.random(150) < 0.1, 40, rng.integers(0, 3, 150)))
+    c = attn_case(kv, q, 16, 4, 1, 64, "bf16", 71)
+    out, lse = call(c, 0.1)
+    check(c, out, lse, 0.1)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_prefill(D):
+    """Enough rows for the 256-row tiles: two prompts, checked head by head in float64 on the GPU."""
+    c = attn_case([2500, 1800], [2500, 1800], 64, 32, 8, D, "bf16", 72)
+    out, lse = call(c, D ** -0.5)
+    assert c["m"].rdg_check_status(c["step"]) == (0, 0)
+    scale, t0 = D ** -0.5, 0
+    for r, n in enumerate((2500, 1800)):
+        pages = c["table"][r, :-(-n // 64)]
+        hidden = torch.ones(n, n, dtype=torch.bool, device=DEV).triu_(1)
+        for h in range(0, 32, 5):
+            k, v = (torch.from_numpy(np.nan_to_num(values(a[pages, h // 4], s[pages, h // 4])).reshape(-1, D)[:n]).to(DEV)
+                    for a, s in ((c["k"], c["ks"]), (c["v"], c["vs"])))
+            x = c["x"][t0:t0 + n, h].double()
+            s = (scale * x @ k.T).masked_fill_(hidden, -float("inf"))
+            size = (scale * x.abs() @ k.abs().T).masked_fill_(hidden, 0).amax(-1)
+            p = torch.softmax(s, -1)
+            want, spread = p @ v, p @ v.abs()
+            d = (D + 4) * EPS * size
+            tol = (2 * d + (n + 64) * 2 * EPS + 2.0 ** -8)[:, None] * spread + 2.0 ** -8 * want.abs()
+            assert ((out[t0:t0 + n, h].double() - want).abs() <= tol + n * 2.0 ** -126 * v.abs().max()).all()
+            wl = torch.logsumexp(s, -1)
+            assert ((lse[t0:t0 + n, h].double() - wl).abs() <= d + (n + 64) * 2 * EPS + 8 * EPS * wl.abs()).all()
+        t0 += n
 
 
 @pytest.mark.parametrize("case", [1, 5, 6, 8, 10])
