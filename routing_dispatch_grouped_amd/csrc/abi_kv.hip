@@ -38,11 +38,26 @@ int cache_buffers_rc(const rdg_kv_cache* C) {
     return RDG_OK;
 }
 
-constexpr int kChunkMin = 256;                    // keys: one 64-key step of each of four waves
-constexpr int kWaveKeys = 1024;                   // keys whose pages the lanes of a k_attn_rows wave hold
-constexpr int kRowUnits = 1024;                   // k_attn_rows workgroups wanted: four per CU
-constexpr int kTileUnits = 512;                   // k_attn_tiles workgroups wanted: two per CU
-constexpr int kTileChunkMin = 512;                // keys: fewer do not pay for the parts' way through memory
+// How attention shares out its work.  Times in us at head_dim 128, each as it is
+// against the value named.
+//
+// Keys at least in a k_attn_rows chunk, one 64-key step of each of four waves.  512: two
+// requests of 3 queries, 5000 keys, 8 heads a key head 14.8 against 17.5; 31 requests
+// of 35 rows 39.8 against 46.8.
+constexpr int kChunkMin = 256;
+constexpr int kWaveKeys = 1024;  // keys whose pages the lanes of a k_attn_rows wave hold
+// k_attn_rows workgroups wanted, four per CU.  31 requests of 35 rows 39.8, with 512 46.9,
+// with 2048 44.5; 16 requests of 64 rows 40.6, 40.3 and 49.1; 64 requests of one row 64,
+// 62 and 62.
+constexpr int kRowUnits = 1024;
+// k_attn_tiles workgroups wanted, two per CU; above it rows go in tiles of 256, below
+// half of it keys are split.  Prompts of 32 / 8 heads: 1000 tokens 33, with 256 33, with 1024
+// 47; 2000 tokens 63, 67 and 83; 4000 tokens 163, 153 and 159; 300 tokens on
+// 6000 58, 61 and 66; four times 400 on 3000 99, 100 and 132.
+constexpr int kTileUnits = 512;
+// Keys: fewer do not pay for the parts' way through memory.  1024: 800 tokens on up to
+// 4000, 8 heads sharing one of 256, 45 against 51; 300 on 6000, 58 against 56.
+constexpr int kTileChunkMin = 512;
 
 // How a call's work is split.  span: the longest run of keys that one request's
 // queries see together.
@@ -69,8 +84,10 @@ AttnPlan plan_attn(int T, int R, int n_kv, int group, int head_dim, bool bf16, i
         p.n_most = 64 / group;
         // no request is that short if even max_q for all the others leaves more
         if ((int64_t)T - (int64_t)(R - 1) * max_q > p.n_most) p.n_most = 0;
-        // Tiles of 256 rows convert each key's codes half as often (4% on a long
-        // prefill), tiles of 128 fill the chip sooner and waste less on short requests.
+        // Tiles of 256 rows convert each key's codes half as often: two prompts of 7000 tokens,
+        // 32 / 8 heads, 792 us, with 128 rows 829.  Tiles of 128 fill the chip
+        // sooner and waste less on short requests: one prompt of 1000 33, with 256 rows 46;
+        // four times 400 tokens on 3000 99 and 139.
         const auto units_of = [&](int bm) { return (double)n_kv * ceil((double)T * group / bm); };
         p.tile_rows = head_dim == 256 || p.n_most > 0 || units_of(256) < kTileUnits ? 128 : 256;
         p.tile_slots = (int)((int64_t)T * group / p.tile_rows + R);

