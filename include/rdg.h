@@ -523,7 +523,7 @@ int rdg_qk_norm_rope_store(const void* qkv, int dtype, int64_t qkv_stride, int T
  * over keys j <= position and, with a window, j > position - window; over all kv
  * keys with causal = 0 (window then 0).  A query that sees no key gives 0 and -inf.
  *   q, out   [T, q_stride] / [T, out_stride], n_q heads of head_dim (RDG_F32 or
- *            RDG_BF16); query head h reads key head h / (n_q / n_kv)
+ *            RDG_BF16); query head h reads key head h / (n_q / n_kv); T * n_q < 2^31
  *   max_q, max_kv  host bounds of the requests' new and cached tokens: grids
  *            and workspace are sized by them.  A request of more cached tokens is cut to
  *            max_kv, one of more new tokens than max_q left out (both RDG_EDATA, with the request)

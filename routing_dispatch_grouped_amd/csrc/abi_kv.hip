@@ -192,7 +192,7 @@ int rdg_qk_norm_rope_store(const void* qkv, int dtype, int64_t qkv_stride, int T
 size_t rdg_paged_attention_workspace_bytes(const rdg_kv_cache* C, int T, int n_req, int n_q, int max_q, int max_kv,
                                            int dtype) {
     if (cache_rc(C) != RDG_OK || T <= 0 || n_req <= 0 || n_q < C->n_kv || n_q % C->n_kv != 0 || max_q <= 0 ||
-        max_kv <= 0)
+        max_kv <= 0 || (int64_t)T * n_q >= (int64_t)1 << 31)
         return 0;
     if (max_q > T) max_q = T;
     const AttnPlan p = plan_attn(T, n_req, C->n_kv, n_q / C->n_kv, C->head_dim, dtype == RDG_BF16, max_q, max_kv);
@@ -205,6 +205,7 @@ int rdg_paged_attention(const void* q, int dtype, int64_t q_stride, int T, int n
     if (dtype != RDG_F32 && dtype != RDG_BF16) return RDG_EINVAL;
     if (!step_ok(S) || T < 0 || n_q < 1 || max_q < 0 || max_kv < 0 || window < 0) return RDG_EINVAL;
     if (window > 0 && !causal) return RDG_EINVAL;
+    if (window > 1 << 30) window = 1 << 30;  // as many keys as a request can have: positions less it fit an int
     if (!(scale > 0.0f) || !(scale < INFINITY)) return RDG_EINVAL;
     int rc = cache_rc(C);
     if (rc != RDG_OK) return rc;

@@ -473,6 +473,17 @@ def test_mixed_batches(case, window):
     check(c, out, lse, 0.1, window=window)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("q_heads", [4, 16])
+@pytest.mark.parametrize("window", [1 << 30, (1 << 31) - 1])
+def test_windows_of_any_length(window, q_heads, dtype):
+    """A window longer than any request hides nothing, also where a request has more rows than keys."""
+    c = attn_case([2, 90, 0, 130], [9, 90, 3, 2], 16, q_heads, 2, 64, dtype, 73)
+    out, lse = call(c, 0.1, window=window)
+    assert c["m"].rdg_check_status(c["step"]) == (0, 0)
+    check(c, out, lse, 0.1)
+
+
 def test_more_requests_than_lanes():
     rng = np.random.default_rng(7)
     kv = rng.integers(0, 90, 150)

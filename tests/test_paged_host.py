@@ -114,6 +114,16 @@ def test_attention_refusals():
         assert attn(q=None, **nothing) == rdg.RDG_OK
 
 
+def test_attention_refuses_more_rows_than_an_int_counts():
+    rdg = _rdg()
+    L = rdg._lib
+    c = _cache()
+    for T, n_q, most in ((1 << 29, 4, 0), (1 << 29, 2, 1)):
+        assert (L.rdg_paged_attention_workspace_bytes(ctypes.byref(c), T, 2, n_q, 1, 4000, rdg.RDG_BF16) > 0) == most
+    assert L.rdg_paged_attention(A, rdg.RDG_BF16, 512, 1 << 29, 4, ctypes.byref(_step()), ctypes.byref(c), 1, 100, 0.1, 1,
+                                 0, A, 512, None, A, 1 << 30, None) == rdg.RDG_EINVAL
+
+
 def test_binding_refuses_tensors_it_would_misread():
     import torch
     rdg = _rdg()
