@@ -331,11 +331,12 @@ hipError_t launch_qk_store(QkStoreCall a, int head_dim, bool bf16, int seg_cap, 
     // A wave keeps its token's turn for up to four groups of heads where tokens alone fill
     // the chip: 64 / 8 heads of 128, 2048 tokens 18.4 us (one group a wave: 21.7), 18
     // thousand 159 (209); at 1024 and fewer they are level.
-    a.q_passes = a.T >= 1024 ? (groups < 4 ? groups : 4) : 1;
+    a.q_passes = a.T >= 1024 && groups > 1 ? (groups < 4 ? groups : 4) : 1;
     a.q_chunks = (groups + a.q_passes - 1) / a.q_passes;
     a.q_items = (int64_t)a.T * a.q_chunks;
     const int64_t pages = (int64_t)seg_cap * 2 * a.n_kv, q_blocks = (a.q_items + 3) / 4;
     if (pages + q_blocks >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;
+    if (pages + q_blocks == 0) return hipSuccess;  // neither queries nor keys and values: an empty grid is an error
     a.page_items = (int)pages;
     const unsigned grid = (unsigned)(pages + q_blocks);
     switch (head_dim) {

@@ -1,0 +1,42 @@
+"""The paged-cache operators on the GPU at the ends of what they accept, against the oracle."""
+import numpy as np
+import pytest
+import torch
+
+from harness import DEV, rdg
+from oracle import paged
+from test_gpu_paged import EPS, begin, dev, host
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- norm, rotation, store
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 1023, 1024, 2500])
+def test_store_of_keys_and_values_alone(T, dtype):
+    """No query heads, around and past the number of tokens from which query waves take several heads."""
+    m = rdg()
+    P, n_kv, D = 64, 2, 64
+    step, _, cache, (k, v, ks, vs) = begin(m, [9], [T], P, n_kv, D, T)
+    x = torch.from_numpy(np.random.default_rng(T).standard_normal((T, 2 * n_kv * D))).to(DEV)
+    x = x.to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    m.rdg_qk_norm_rope_store(x, 0, n_kv, D, None, None, 0.0, None, 0, False, step, cache, None)
+    assert m.rdg_check_status(step) == (0, 0)
+    rows, slots, seg = host(x).reshape(T, 2 * n_kv, D), host(step.slots), host(step.seg_tok)
+    for codes, scales, was, part in ((cache.k, cache.k_scale, (k, ks), rows[:, :n_kv]),
+                                     (cache.v, cache.v_scale, (v, vs), rows[:, n_kv:])):
+        want = paged.store(*was, slots, seg, part)
+        assert np.array_equal(host(codes), want[0]) and np.array_equal(host(scales), want[1])
+
+
+@pytest.mark.parametrize("n_q", [1, 3, 40])
+def test_queries_alone_of_many_tokens(n_q):
+    m = rdg()
+    T, D = 1300, 128
+    step = m.KvStep(1, 1, 16, 1, T, DEV)
+    x = torch.randn(T, n_q * D, device=DEV)
+    w = torch.rand(D, device=DEV) + 0.5
+    q = torch.empty(T, n_q, D, device=DEV)
+    m.rdg_qk_norm_rope_store(x, n_q, 0, D, w, None, 1e-6, None, 0, False, step, None, q)
+    want = paged.norm(host(x).reshape(T, n_q, D), host(w), 1e-6)
+    assert (np.abs(host(q) - want) <= 32 * EPS * np.abs(want)).all()
