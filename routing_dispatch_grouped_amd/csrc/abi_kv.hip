@@ -58,6 +58,9 @@ constexpr int kTileUnits = 512;
 // Keys: fewer do not pay for the parts' way through memory.  1024: 800 tokens on up to
 // 4000, 8 heads sharing one of 256, 45 against 51; 300 on 6000, 58 against 56.
 constexpr int kTileChunkMin = 512;
+// The longest request a block table can list (step_ok): bounds and windows above it say no
+// more, and key positions, and a position and a chunk of keys together, stay within an int.
+constexpr int kMaxKeys = 1 << 30;
 
 // How a call's work is split.  span: the longest run of keys that one request's
 // queries see together.
@@ -68,8 +71,9 @@ struct AttnPlan {
     int max_chunks;
 };
 
+// Parts of `chunk` keys that a run of span keys can have, from the 64-key block it begins in.
 int chunks_of(int64_t span, int chunk) {
-    const int64_t n = (span + 63 + chunk - 1) / chunk;
+    const int64_t keys = span + 63 < kMaxKeys ? span + 63 : kMaxKeys, n = (keys + chunk - 1) / chunk;
     return n < 1 ? 1 : (int)n;
 }
 
@@ -95,6 +99,7 @@ AttnPlan plan_attn(int T, int R, int n_kv, int group, int head_dim, bool bf16, i
         double want = span + 64.0;
         if (units < kTileUnits / 2) want = ceil(span * units / kTileUnits / 64) * 64;
         if (want < kTileChunkMin) want = kTileChunkMin;
+        if (want > kMaxKeys) want = kMaxKeys;
         p.tile_chunk = (int)((want + 63) / 64) * 64;
         p.tile_chunks = chunks_of(span, p.tile_chunk);
         p.max_chunks = p.tile_chunks;
@@ -195,6 +200,7 @@ size_t rdg_paged_attention_workspace_bytes(const rdg_kv_cache* C, int T, int n_r
         max_kv <= 0 || (int64_t)T * n_q >= (int64_t)1 << 31)
         return 0;
     if (max_q > T) max_q = T;
+    if (max_kv > kMaxKeys) max_kv = kMaxKeys;
     const AttnPlan p = plan_attn(T, n_req, C->n_kv, n_q / C->n_kv, C->head_dim, dtype == RDG_BF16, max_q, max_kv);
     return p.max_chunks > 1 ? align256(part_bytes(T, n_q, C->head_dim) * p.max_chunks) : 0;
 }
@@ -205,7 +211,8 @@ int rdg_paged_attention(const void* q, int dtype, int64_t q_stride, int T, int n
     if (dtype != RDG_F32 && dtype != RDG_BF16) return RDG_EINVAL;
     if (!step_ok(S) || T < 0 || n_q < 1 || max_q < 0 || max_kv < 0 || window < 0) return RDG_EINVAL;
     if (window > 0 && !causal) return RDG_EINVAL;
-    if (window > 1 << 30) window = 1 << 30;  // as many keys as a request can have: positions less it fit an int
+    if (window > kMaxKeys) window = kMaxKeys;
+    if (max_kv > kMaxKeys) max_kv = kMaxKeys;
     if (!(scale > 0.0f) || !(scale < INFINITY)) return RDG_EINVAL;
     int rc = cache_rc(C);
     if (rc != RDG_OK) return rc;
@@ -238,7 +245,8 @@ int rdg_paged_attention(const void* q, int dtype, int64_t q_stride, int T, int n
     const int64_t room = need > 0 ? (int64_t)(need / part) : 1;
     const auto fit = [&](int* chunk, int* chunks) {
         if (*chunks <= room) return;
-        *chunk = (int)((((int64_t)span + 63 + room - 1) / room + kChunkMin - 1) / kChunkMin * kChunkMin);
+        const int64_t keys = span + 63 < kMaxKeys ? span + 63 : kMaxKeys;
+        *chunk = (int)(((keys + room - 1) / room + kChunkMin - 1) / kChunkMin * kChunkMin);
         *chunks = chunks_of(span, *chunk);
     };
     if (p.tile_slots > 0) fit(&p.tile_chunk, &p.tile_chunks);

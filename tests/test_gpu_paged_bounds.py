@@ -5,7 +5,7 @@ import torch
 
 from harness import DEV, rdg
 from oracle import paged
-from test_gpu_paged import EPS, begin, dev, host
+from test_gpu_paged import EPS, attn_case, begin, call, check, dev, host
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +40,17 @@ def test_queries_alone_of_many_tokens(n_q):
     m.rdg_qk_norm_rope_store(x, n_q, 0, D, w, None, 1e-6, None, 0, False, step, None, q)
     want = paged.norm(host(x).reshape(T, n_q, D), host(w), 1e-6)
     assert (np.abs(host(q) - want) <= 32 * EPS * np.abs(want)).all()
+
+
+# ---------------------------------------------------------------- attention
+@pytest.mark.parametrize("max_kv", [1 << 30, 2147480000, 2147483000, (1 << 31) - 1])
+def test_prefill_with_a_bound_of_any_size(max_kv):
+    """max_kv far above every request: rows that fill the chip, whose keys are not split, and few rows, whose are."""
+    c = attn_case([5000, 700], [1500, 548], 64, 32, 8, 64, "bf16", 110)
+    ref, ref_lse = call(c, 0.1)
+    out, lse = call(c, 0.1, max_kv=max_kv)
+    assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+    c = attn_case([3000], [100], 64, 8, 2, 64, "bf16", 111)
+    out, lse = call(c, 0.1, max_kv=max_kv)
+    assert c["m"].rdg_check_status(c["step"]) == (0, 0)
+    check(c, out, lse, 0.1)
