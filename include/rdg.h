@@ -475,7 +475,8 @@ int rdg_kv_seg_cap(int t_cap, int n_req, int page_rows);
  * fit -- too few free pages, more than max_blocks pages, tokens past t_cap --
  * gets none, nor does a later one that needs a page: its tokens' slots are -1, its
  * kv_len stays, and status is RDG_ECAPACITY with the first such request as detail.  Negative lengths and page ids
- * outside the cache give RDG_EDATA, with the request.  Deterministic; nothing
+ * outside the cache give RDG_EDATA, with the request: one of a negative q_len keeps its kv_len and gets
+ * nothing, a negative kv_len becomes 0.  (Lengths above 2^30 count as negative.)  Deterministic; nothing
  * waits for the host, so a step can be captured with the kernels that read it. */
 int rdg_kv_plan(const rdg_kv_step* S, const int32_t* kv_len, const int32_t* q_len, const int32_t* free_list,
                 const int32_t* n_free, int32_t* n_free_out, rdg_stream_t stream);

@@ -34,7 +34,7 @@ def kv_plan(kv_len, q_len, table, free_list, n_free, page_rows, t_cap, seg_cap):
         ok = True
         if kv < 0 or q < 0:
             bad = r if bad is None else bad
-            kv, q, ok = 0, 0, False
+            kv, q, ok = max(kv, 0), 0, False
         need = pages_of(kv + q, P) - pages_of(kv, P)
         if ok and pages_of(kv + q, P) > max_blocks:
             need, ok = 0, False

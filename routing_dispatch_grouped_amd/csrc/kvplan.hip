@@ -154,12 +154,14 @@ struct Lens {
     bool bad;
 };
 
-// A request's lengths, made safe: negative ones count as 0 and are reported.
+// A request's lengths, made safe: with one of them out of range it has no new
+// tokens and is reported.  Its cached ones stay, unless theirs is the bad length.
 __device__ __forceinline__ Lens lens_of(const int32_t* kv_len, const int32_t* q_len, int r) {
     Lens l = {kv_len[r], q_len[r], false};
-    if (l.kv < 0 || l.q < 0 || l.kv > (int)kSat || l.q > (int)kSat) {
+    const bool bad_kv = l.kv < 0 || l.kv > (int)kSat;
+    if (bad_kv || l.q < 0 || l.q > (int)kSat) {
         l.bad = true;
-        l.kv = 0;
+        l.kv = bad_kv ? 0 : l.kv;
         l.q = 0;
     }
     return l;

@@ -10,6 +10,29 @@ from test_gpu_paged import EPS, attn_case, begin, call, check, dev, host
 pytestmark = pytest.mark.gpu
 
 
+# ---------------------------------------------------------------- plan
+@pytest.mark.parametrize("bad_q", [-3, -(1 << 31), (1 << 30) + 1, (1 << 31) - 1])
+def test_plan_keeps_the_cached_tokens_of_a_request_with_a_bad_length(bad_q):
+    """In place, as a serving loop plans: the request keeps its length, table and pages, and its next step goes on."""
+    m = rdg()
+    P, n_pages = 16, 12
+    step = m.KvStep(3, 6, P, n_pages, 60, DEV)
+    free, n = dev(np.arange(n_pages)), dev([n_pages])
+    m.rdg_kv_plan(step, step.kv_len, dev([10, 40, 5]), free, n, n)
+    assert m.rdg_check_status(step) == (0, 0)
+    table = host(step.block_table)
+    m.rdg_kv_plan(step, step.kv_len, dev(np.array([1, bad_q, 2], np.int32)), free, n, n)
+    assert m.rdg_check_status(step) == (m.RDG_EDATA, 1)
+    assert list(host(step.kv_len)) == [11, 40, 7] and list(host(step.cu_q)) == [0, 1, 1, 3]
+    assert np.array_equal(host(step.block_table), table) and host(n)[0] == n_pages - 5
+    m.rdg_kv_plan(step, step.kv_len, dev([0, 9, 0]), free, n, n)
+    assert m.rdg_check_status(step) == (0, 0)
+    want = [table[1, 2] * P + 8 + i for i in range(8)] + [host(step.block_table)[1, 3] * P]
+    assert list(host(step.slots)[:9]) == want and host(n)[0] == n_pages - 6
+    m.rdg_kv_trim(step, step.kv_len, dev([0, 0, 0]), free, n, n)
+    assert host(n)[0] == n_pages and sorted(host(free)) == list(range(n_pages))     # every page is back
+
+
 # ---------------------------------------------------------------- norm, rotation, store
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T", [1, 1023, 1024, 2500])
