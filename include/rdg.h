@@ -476,7 +476,9 @@ int rdg_kv_seg_cap(int t_cap, int n_req, int page_rows);
  * gets none, nor does a later one that needs a page: its tokens' slots are -1, its
  * kv_len stays, and status is RDG_ECAPACITY with the first such request as detail.  Negative lengths and page ids
  * outside the cache give RDG_EDATA, with the request: one of a negative q_len keeps its kv_len and gets
- * nothing, a negative kv_len becomes 0.  (Lengths above 2^30 count as negative.)  Deterministic; nothing
+ * nothing, a negative kv_len becomes 0.  (Lengths above 2^30 count as negative.)  Where a page id is the fault, the page's
+ * tokens have slot -1 and, if it was to be a new page, its table entry is -1; kv_len counts them, so that
+ * rdg_kv_trim hands back the request's other pages.  Deterministic; nothing
  * waits for the host, so a step can be captured with the kernels that read it. */
 int rdg_kv_plan(const rdg_kv_step* S, const int32_t* kv_len, const int32_t* q_len, const int32_t* free_list,
                 const int32_t* n_free, int32_t* n_free_out, rdg_stream_t stream);
@@ -487,7 +489,8 @@ int rdg_kv_plan(const rdg_kv_step* S, const int32_t* kv_len, const int32_t* q_le
  *   new_len   [n_req] tokens to keep, at most kv_len; a request with a length out
  *             of range is left as it is, with status RDG_EDATA
  *   free_list [n_pages] the freed pages are added behind the first *n_free, in request
- *             and block order; their table entries become -1
+ *             and block order; their table entries become -1.  An entry that is no page of
+ *             the cache becomes -1 and is not added: status RDG_EDATA, with the request
  * S->kv_len becomes new_len.  More pages than the list can hold: no request is
  * changed and status is RDG_ECAPACITY, with their number. */
 int rdg_kv_trim(const rdg_kv_step* S, const int32_t* kv_len, const int32_t* new_len, int32_t* free_list,

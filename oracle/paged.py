@@ -19,13 +19,13 @@ def pages_of(tokens, page_rows):
     return (tokens + page_rows - 1) // page_rows
 
 
-def kv_plan(kv_len, q_len, table, free_list, n_free, page_rows, t_cap, seg_cap):
+def kv_plan(kv_len, q_len, table, free_list, n_free, page_rows, t_cap, seg_cap, n_pages=1 << 31):
     """One step: (table, cu_q, kv_len, slots, positions, seg_tok, n_free, status)."""
     P, table = page_rows, np.array(table)
     R, max_blocks = table.shape
     slots, positions = np.full(t_cap, -1), np.zeros(t_cap, int)
     segs, cu, out_len = [], [0], []
-    bad = full = None
+    bad = full = bad_page = None
     taken, left = 0, n_free
     stop = False            # a request ran out of pages: no later one gets any
     t = 0
@@ -47,7 +47,8 @@ def kv_plan(kv_len, q_len, table, free_list, n_free, page_rows, t_cap, seg_cap):
             full = r if full is None else full
         if ok:
             for i in range(need):
-                table[r, pages_of(kv, P) + i] = free_list[n_free - 1 - taken - i]
+                page = free_list[n_free - 1 - taken - i]
+                table[r, pages_of(kv, P) + i] = page if 0 <= page < n_pages else -1
             taken += need
             left = n_free - taken
         for i in range(q):
@@ -56,7 +57,11 @@ def kv_plan(kv_len, q_len, table, free_list, n_free, page_rows, t_cap, seg_cap):
             p = kv + i
             positions[t + i] = p
             if ok:
-                slots[t + i] = table[r, p // P] * P + p % P
+                page = table[r, p // P]
+                if 0 <= page < n_pages:
+                    slots[t + i] = page * P + p % P
+                else:
+                    bad_page = r if bad_page is None else bad_page
                 if i == 0 or p % P == 0:
                     segs.append(t + i)
         t += q
@@ -64,16 +69,17 @@ def kv_plan(kv_len, q_len, table, free_list, n_free, page_rows, t_cap, seg_cap):
         out_len.append(kv + q if ok else kv)
     seg = np.full(seg_cap, -1)
     seg[:len(segs)] = segs
-    status = (EDATA, bad) if bad is not None else (ECAPACITY, full) if full is not None else (OK, 0)
+    status = ((EDATA, bad) if bad is not None else (ECAPACITY, full) if full is not None else
+              (EDATA, bad_page) if bad_page is not None else (OK, 0))
     return table, np.array(cu), np.array(out_len), slots, positions, seg, left, status
 
 
 def kv_trim(kv_len, new_len, table, free_list, n_free, page_rows):
-    """(table, kv_len, free_list, n_free, status)."""
-    P, table, free = page_rows, np.array(table), list(free_list[:n_free])
+    """(table, kv_len, free_list, n_free, status); free_list has a place for every page."""
+    P, table, free, n_pages = page_rows, np.array(table), list(free_list[:n_free]), len(free_list)
     R, max_blocks = table.shape
     before = np.array(table), np.array(kv_len), list(free)
-    out, bad, freed = [], None, 0
+    out, bad, bad_page, freed = [], None, None, 0
     for r in range(R):
         kv, to = int(kv_len[r]), int(new_len[r])
         if kv < 0 or kv > max_blocks * P or to < 0 or to > kv:
@@ -81,12 +87,16 @@ def kv_trim(kv_len, new_len, table, free_list, n_free, page_rows):
             out.append(kv)
             continue
         for b in range(pages_of(to, P), pages_of(kv, P)):
-            free.append(table[r, b])
+            if 0 <= table[r, b] < n_pages:
+                free.append(table[r, b])
+            else:
+                bad_page = r if bad_page is None else bad_page
             table[r, b] = -1
             freed += 1
         out.append(to)
-    if len(free) > len(free_list):
+    if n_free + freed > n_pages:
         return before[0], before[1], before[2], n_free, (EDATA, bad) if bad is not None else (ECAPACITY, freed)
+    bad = bad_page if bad is None else bad
     return table, np.array(out), free, len(free), (EDATA, bad) if bad is not None else (OK, 0)
 
 

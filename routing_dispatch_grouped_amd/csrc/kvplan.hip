@@ -111,29 +111,31 @@ __device__ __forceinline__ int find_row(const uint32_t* begin, int n, uint32_t t
 }
 
 // True in every thread of the last workgroup of the grid to get here; the
-// ticket is then 0 again for the next launch.
+// ticket is then 0 again for the next launch.  READS: the last workgroup reads
+// what the others have written.
+template <bool READS>
 __device__ __forceinline__ bool last_block(int32_t* ticket) {
     __shared__ int last;
     // every wave has used what it read, and what it noted has been noted: the
-    // ticket orders nothing else, so it needs no fence
+    // ticket orders nothing else, so without READS it needs no fence
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
     if (threadIdx.x == 0) {
         last = 1;
         if (gridDim.x > 1) {
+            if (READS) __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
             last = __hip_atomic_fetch_add(ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
             if (last) __hip_atomic_store(ticket, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (READS) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
         }
     }
     __syncthreads();
     return last != 0;
 }
 
-// work[1]: 1 + the first request found with a page id outside the cache.
+// work[1]: kMaxRequests less the first request with a page id outside the cache; 0: none.
 __device__ __forceinline__ void note_bad(int32_t* work, int r) {
-    int32_t none = 0;
-    __hip_atomic_compare_exchange_strong(work + 1, &none, r + 1, __ATOMIC_RELAXED, __ATOMIC_RELAXED,
-                                         __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_fetch_max(work + 1, kMaxRequests - r, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 __device__ __forceinline__ void write_status(int32_t* status, int32_t* work, int code, int detail) {
@@ -142,7 +144,7 @@ __device__ __forceinline__ void write_status(int32_t* status, int32_t* work, int
         __hip_atomic_store(work + 1, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         if (code == RDG_OK) {
             code = RDG_EDATA;
-            detail = bad - 1;
+            detail = kMaxRequests - bad;
         }
     }
     status[0] = code;
@@ -272,8 +274,9 @@ __global__ __launch_bounds__(kThreads) void k_kv_plan(rdg_kv_step S, int shift, 
             if (!stored[i]) continue;
             const int blk = pos[i] >> shift, kv = kv0[req[i]];
             const bool starts = (pos[i] & P1) == 0;
-            if (fresh[i] && starts) S.block_table[(int64_t)req[i] * S.max_blocks + blk] = page[i];
-            if ((unsigned)page[i] < (unsigned)S.n_pages) slot[i] = (page[i] << shift) + (pos[i] & P1);
+            const bool in_cache = (unsigned)page[i] < (unsigned)S.n_pages;
+            if (fresh[i] && starts) S.block_table[(int64_t)req[i] * S.max_blocks + blk] = in_cache ? page[i] : -1;
+            if (in_cache) slot[i] = (page[i] << shift) + (pos[i] & P1);
             else note_bad(S.work, req[i]);
             if (pos[i] == kv || starts) {
                 const uint32_t place = seg0[req[i]] + (blk - (kv >> shift));
@@ -293,7 +296,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_plan(rdg_kv_step S, int shift, 
     for (int s = (int)n_seg + (int)blockIdx.x * kThreads + tid; s < S.seg_cap; s += (int)gridDim.x * kThreads)
         S.seg_tok[s] = -1;
 
-    if (!last_block(S.work)) return;
+    if (!last_block<false>(S.work)) return;
     for (int r = tid; r < R; r += kThreads) {
         const Lens l = lens_of(kv_len, q_len, r);
         S.cu_q[r + 1] = (int)(cu[r + 1] < (uint32_t)S.t_cap ? cu[r + 1] : (uint32_t)S.t_cap);
@@ -348,13 +351,28 @@ __global__ __launch_bounds__(kThreads) void k_kv_trim(rdg_kv_step S, int shift, 
             *entry = -1;
         }
     }
-    if (!last_block(S.work)) return;
+    if (!last_block<true>(S.work)) return;
+    uint32_t freed = fits ? total : 0;
+    const int bad_page = __hip_atomic_load(S.work + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();  // read by all before write_status clears it
+    if (bad_page != 0) {  // ids that no page has: the others move up, in their order
+        freed = 0;
+        for (uint32_t e0 = 0; e0 < total; e0 += kThreads) {
+            const uint32_t e = e0 + tid;
+            const int page = e < total ? free_list[nf + e] : -1;
+            const bool in_cache = (unsigned)page < (unsigned)S.n_pages;
+            uint32_t n;
+            const uint32_t at = block_scan(in_cache ? 1 : 0, part, &n);
+            if (in_cache) free_list[nf + freed + at] = page;
+            freed += n;
+        }
+    }
     for (int r = tid; r < R; r += kThreads) {
         const int kv = kv_len[r], to = new_len[r];
         S.kv_len[r] = (!fits || kv < 0 || kv > limit || to < 0 || to > kv) ? kv : to;
     }
     if (tid == 0) {
-        n_free_out[0] = nf + (fits ? (int)total : 0);
+        n_free_out[0] = nf + (int)freed;
         const bool bad = failed != 0xffffffffu;
         write_status(S.status, S.work, bad ? RDG_EDATA : fits ? RDG_OK : RDG_ECAPACITY,
                      bad ? (int)failed : fits ? 0 : (int)total);

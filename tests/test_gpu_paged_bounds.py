@@ -33,6 +33,70 @@ def test_plan_keeps_the_cached_tokens_of_a_request_with_a_bad_length(bad_q):
     assert host(n)[0] == n_pages and sorted(host(free)) == list(range(n_pages))     # every page is back
 
 
+@pytest.mark.parametrize("R,n_bad", [(5, 1), (5, 4), (300, 40), (4096, 1), (4096, 3000)])
+def test_trim_keeps_ids_of_no_page_off_the_stack(R, n_bad):
+    """Entries outside the cache are reported with the first request that has one and vanish; the other pages come back in
+    their order, from one workgroup (5 requests) and from several; a plan then hands out pages of the cache only."""
+    m = rdg()
+    rng = np.random.default_rng(R + n_bad)
+    P, B = 16, 6
+    n_pages = R * B
+    kv = rng.integers(1, B * P + 1, R)
+    held = paged.pages_of(kv, P)
+    ids = rng.permutation(n_pages)
+    table = np.full((R, B), -1)
+    at = np.concatenate([[0], np.cumsum(held)])
+    for r in range(R):
+        table[r, :held[r]] = ids[at[r]:at[r + 1]]
+    keep = np.where(rng.random(R) < 0.5, 0, np.minimum(kv, rng.integers(0, B * P, R)))
+    keep[0] = 0
+    freed = [(r, b) for r in range(R) for b in range(paged.pages_of(keep[r], P), held[r])]
+    for x in rng.permutation(len(freed))[:n_bad]:
+        table[freed[x]] = rng.choice([-1, n_pages, (1 << 31) - 1, -(1 << 31)])
+    free = np.concatenate([ids[at[-1]:], np.full(at[-1], -1)])
+    n_free = n_pages - at[-1]
+    step = m.KvStep(R, B, P, n_pages, 2 * R, DEV)
+    step.block_table.copy_(dev(table))
+    step.kv_len.copy_(dev(kv))
+    d_free, d_n = dev(free), dev([n_free])
+    m.rdg_kv_trim(step, step.kv_len, dev(keep), d_free, d_n, d_n)
+    w_table, w_kv, w_free, w_n, status = paged.kv_trim(kv, keep, table, free, n_free, P)
+    assert m.rdg_check_status(step) == status and status[0] == m.RDG_EDATA
+    assert np.array_equal(host(step.block_table), w_table) and np.array_equal(host(step.kv_len), w_kv)
+    assert host(d_n)[0] == w_n and np.array_equal(host(d_free)[:w_n], w_free)
+    assert not host(step.work.view(torch.int32)).any()
+    q = np.where(w_kv == 0, 2, 0)
+    m.rdg_kv_plan(step, step.kv_len, dev(q), d_free, d_n, d_n)
+    assert m.rdg_check_status(step) == (0, 0)
+    want = paged.kv_plan(w_kv, q, w_table, w_free, w_n, P, 2 * R, step.seg_tok.numel(), n_pages)
+    assert np.array_equal(host(step.block_table), want[0]) and np.array_equal(host(step.slots), want[3])
+
+
+@pytest.mark.parametrize("R", [4, 300])
+def test_plan_writes_no_id_of_no_page(R):
+    """Ids outside the cache on the stack: their table entries are -1, their tokens have no slot, the first request is named
+    (whichever workgroup comes first), and a trim hands every other page back."""
+    m = rdg()
+    rng = np.random.default_rng(R)
+    P, B = 16, 4
+    n_pages = 3 * R
+    free = rng.permutation(n_pages)
+    bad = rng.permutation(n_pages - 4)[:R // 4] + 4
+    free[bad] = rng.choice([-1, n_pages, (1 << 31) - 1], len(bad))
+    q = np.full(R, 40)
+    step = m.KvStep(R, B, P, n_pages, int(q.sum()), DEV)
+    step.block_table.fill_(1)                                    # of an earlier use
+    d_free, d_n = dev(free), dev([n_pages])
+    m.rdg_kv_plan(step, step.kv_len, dev(q), d_free, d_n, d_n)
+    want = paged.kv_plan([0] * R, q, np.full((R, B), 1), free, n_pages, P, int(q.sum()), step.seg_tok.numel(), n_pages)
+    for got, ref in zip((step.block_table, step.cu_q, step.kv_len, step.slots, step.positions, step.seg_tok, d_n), want):
+        assert np.array_equal(host(got), np.ravel(ref).reshape(got.shape))
+    assert m.rdg_check_status(step) == want[-1] and want[-1][0] == m.RDG_EDATA
+    m.rdg_kv_trim(step, step.kv_len, dev([0] * R), d_free, d_n, d_n)
+    good = np.sort(free[(free >= 0) & (free < n_pages)])
+    assert host(d_n)[0] == len(good) and np.array_equal(np.sort(host(d_free)[:len(good)]), good)
+
+
 # ---------------------------------------------------------------- norm, rotation, store
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T", [1, 1023, 1024, 2500])
