@@ -68,8 +68,15 @@ struct AttnPlan {
     int rt;  // 16-row tiles per workgroup of k_attn_rows
     int n_most, row_tiles, chunk, row_chunks;
     int tile_rows, tile_slots, tile_chunk, tile_chunks;  // tile_slots 0: no k_attn_tiles
-    int max_chunks;
+    // workspace: parts of the short requests' rows by request (row_place each) or by token (0), then the long ones' by token
+    int row_place;
+    size_t row_bytes, tile_bytes;
 };
+
+// Bytes of the parts of every head of `places` tokens, fp32 row, maximum and sum each.
+size_t parts_bytes(int64_t places, int n_q, int head_dim, int chunks) {
+    return chunks > 1 ? align256(sizeof(float) * (size_t)places * n_q * (head_dim + 2) * chunks) : 0;
+}
 
 // Parts of `chunk` keys that a run of span keys can have, from the 64-key block it begins in.
 int chunks_of(int64_t span, int chunk) {
@@ -102,7 +109,7 @@ AttnPlan plan_attn(int T, int R, int n_kv, int group, int head_dim, bool bf16, i
         if (want > kMaxKeys) want = kMaxKeys;
         p.tile_chunk = (int)((want + 63) / 64) * 64;
         p.tile_chunks = chunks_of(span, p.tile_chunk);
-        p.max_chunks = p.tile_chunks;
+        p.tile_bytes = parts_bytes(T, n_kv * group, head_dim, p.tile_chunks);
     }
     if (p.n_most > 0) {
         const int64_t rows = (int64_t)p.n_most * group;
@@ -114,13 +121,13 @@ AttnPlan plan_attn(int T, int R, int n_kv, int group, int head_dim, bool bf16, i
         if (want < kChunkMin) want = kChunkMin;
         p.chunk = want > most ? most : (int)want;
         p.row_chunks = chunks_of(span, p.chunk);
-        if (p.row_chunks > p.max_chunks) p.max_chunks = p.row_chunks;
+        // Beside long requests most tokens are not the short ones': those then have n_most places a request.
+        const int64_t places = (int64_t)R * p.n_most;
+        p.row_place = places < T ? p.n_most : 0;
+        p.row_bytes = parts_bytes(places < T ? places : T, n_kv * group, head_dim, p.row_chunks);
     }
     return p;
 }
-
-// Bytes of one part (fp32 row, maximum and sum) of every row.
-size_t part_bytes(int T, int n_q, int head_dim) { return sizeof(float) * (size_t)T * n_q * (head_dim + 2); }
 
 int key_span(int max_q, int max_kv, int window) {
     const int64_t w = window > 0 ? (int64_t)window + max_q : max_kv;
@@ -202,7 +209,7 @@ size_t rdg_paged_attention_workspace_bytes(const rdg_kv_cache* C, int T, int n_r
     if (max_q > T) max_q = T;
     if (max_kv > kMaxKeys) max_kv = kMaxKeys;
     const AttnPlan p = plan_attn(T, n_req, C->n_kv, n_q / C->n_kv, C->head_dim, dtype == RDG_BF16, max_q, max_kv);
-    return p.max_chunks > 1 ? align256(part_bytes(T, n_q, C->head_dim) * p.max_chunks) : 0;
+    return p.row_bytes + p.tile_bytes;
 }
 
 int rdg_paged_attention(const void* q, int dtype, int64_t q_stride, int T, int n_q, const rdg_kv_step* S,
@@ -238,29 +245,33 @@ int rdg_paged_attention(const void* q, int dtype, int64_t q_stride, int T, int n
     // The workspace is sized for all max_kv keys.  A window leaves a shorter run,
     // which may be cut finer than the workspace holds parts for: then coarser.
     const int span = key_span(max_q, max_kv, window);
+    const AttnPlan most = plan_attn(T, a.R, a.n_kv, a.group, D, bf16, max_q, max_kv);
     AttnPlan p = plan_attn(T, a.R, a.n_kv, a.group, D, bf16, max_q, span);
-    const size_t part = part_bytes(T, n_q, D);
-    const size_t need = rdg_paged_attention_workspace_bytes(C, T, a.R, n_q, max_q, max_kv, dtype);
+    const size_t need = most.row_bytes + most.tile_bytes;
     if (need > 0 && (!work || !aligned16(work) || work_bytes < need)) return RDG_EINVAL;
-    const int64_t room = need > 0 ? (int64_t)(need / part) : 1;
-    const auto fit = [&](int* chunk, int* chunks) {
+    const auto fit = [&](int* chunk, int* chunks, int room) {
         if (*chunks <= room) return;
         const int64_t keys = span + 63 < kMaxKeys ? span + 63 : kMaxKeys;
         *chunk = (int)(((keys + room - 1) / room + kChunkMin - 1) / kChunkMin * kChunkMin);
         *chunks = chunks_of(span, *chunk);
     };
-    if (p.tile_slots > 0) fit(&p.tile_chunk, &p.tile_chunks);
-    if (p.n_most > 0) fit(&p.chunk, &p.row_chunks);
-    a.max_chunks = p.tile_chunks > p.row_chunks ? p.tile_chunks : p.row_chunks;
+    if (p.tile_slots > 0) fit(&p.tile_chunk, &p.tile_chunks, most.tile_chunks);
+    if (p.n_most > 0) fit(&p.chunk, &p.row_chunks, most.row_chunks);
     a.n_most = p.n_most, a.rows_per_tile = 16 * p.rt, a.row_tiles = p.row_tiles, a.chunk = p.chunk;
     a.row_chunks = p.row_chunks, a.tile_rows = p.tile_rows, a.tile_slots = p.tile_slots;
     a.tile_chunk = p.tile_chunk, a.tile_chunks = p.tile_chunks;
-    if (a.max_chunks > 1) {
-        a.part_o = static_cast<float*>(work);
-        a.part_ml = a.part_o + (size_t)T * n_q * D * a.max_chunks;
+    a.row_place = p.row_place;
+    if (p.row_chunks > 1) {
+        const int64_t places = p.row_place > 0 ? (int64_t)a.R * p.row_place : T;
+        a.row_o = static_cast<float*>(work);
+        a.row_ml = a.row_o + (size_t)places * n_q * D * p.row_chunks;
+    }
+    if (p.tile_chunks > 1) {
+        a.tile_o = reinterpret_cast<float*>(static_cast<char*>(work) + most.row_bytes);
+        a.tile_ml = a.tile_o + (size_t)T * n_q * D * p.tile_chunks;
     }
     hipError_t e = p.tile_slots > 0 ? launch_attn_tiles(a, D, stream) : launch_attn_rows(a, D, bf16, stream);
-    if (e == hipSuccess && a.max_chunks > 1) e = launch_attn_join(a, D, bf16, stream);
+    if (e == hipSuccess && (p.row_chunks > 1 || p.tile_chunks > 1)) e = launch_attn_join(a, D, bf16, stream);
     return hip_rc(e);
 }
 

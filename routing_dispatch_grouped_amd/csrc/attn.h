@@ -69,6 +69,12 @@ __device__ __forceinline__ TileKeys tile_keys(const AttnCall& a, const ReqSpan& 
     return k;
 }
 
+// The first part of head h of a request's query i among the short requests' parts.
+__device__ __forceinline__ int64_t row_part(const AttnCall& a, const ReqSpan& s, int r, int i, int h) {
+    const int64_t place = a.row_place > 0 ? (int64_t)r * a.row_place + i : s.t0 + i;
+    return (place * a.n_q + h) * a.row_chunks;
+}
+
 // Page of a key, made safe: ids outside the cache are reported and read page 0.
 __device__ __forceinline__ int page_of(const AttnCall& a, int r, int key) {
     int page = a.block_table[(int64_t)r * a.max_blocks + (key >> a.page_shift)];

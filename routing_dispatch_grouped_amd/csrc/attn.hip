@@ -27,14 +27,15 @@ __global__ __launch_bounds__(kJoinWaves * kWave) void k_attn_join(AttnCall a) {
     const bool few = s.n <= a.n_most;
     if ((few ? a.row_chunks : a.tile_chunks) == 1) return;
     const int per = few ? a.rows_per_tile : a.tile_rows;
+    const float *part_o = few ? a.row_o : a.tile_o, *part_ml = few ? a.row_ml : a.tile_ml;
     for (int h = (int)blockIdx.y * kJoinWaves + (int)threadIdx.x / kWave; h < a.n_q; h += (int)gridDim.y * kJoinWaves) {
         const int row = i * a.group + h % a.group;
         const int row0 = row / per * per, row1 = row0 + per < s.n * a.group ? row0 + per : s.n * a.group;
         const int chunks = tile_keys(a, s, row0, row1, few ? a.chunk : a.tile_chunk).chunks;
         if (chunks == 1) continue;
-        const int64_t at = ((int64_t)t * a.n_q + h) * a.max_chunks;
+        const int64_t at = few ? row_part(a, s, r, i, h) : ((int64_t)t * a.n_q + h) * a.tile_chunks;
         float top = -__builtin_inff();
-        for (int c = lane; c < chunks; c += kWave) top = fmaxf(top, a.part_ml[2 * (at + c)]);
+        for (int c = lane; c < chunks; c += kWave) top = fmaxf(top, part_ml[2 * (at + c)]);
         top = wave_max_f32(top);
         const float ref = top == -__builtin_inff() ? 0.0f : top;
         float total = 0.0f;
@@ -43,11 +44,11 @@ __global__ __launch_bounds__(kJoinWaves * kWave) void k_attn_join(AttnCall a) {
         for (int e = 0; e < D / kWave; ++e) acc[e] = 0.0f;
 #pragma unroll 4
         for (int c = 0; c < chunks; ++c) {
-            const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * (at + c));
+            const float2 ml = *reinterpret_cast<const float2*>(part_ml + 2 * (at + c));
             const float f = __builtin_amdgcn_exp2f(ml.x - ref);
             total = fmaf(f, ml.y, total);
 #pragma unroll
-            for (int e = 0; e < D / kWave; ++e) acc[e] = fmaf(f, a.part_o[(at + c) * D + e * kWave + lane], acc[e]);
+            for (int e = 0; e < D / kWave; ++e) acc[e] = fmaf(f, part_o[(at + c) * D + e * kWave + lane], acc[e]);
         }
         const bool none = key_hi(a, s, i) <= key_lo(a, s, i);
         const float inv = none ? 0.0f : 1.0f / total;

@@ -382,8 +382,8 @@ __device__ __forceinline__ void attn_rows(const AttnCall& a, int id, RowsLds<D, 
         if (row >= rows) return;
         const int i = row / G, h = head * G + row % G;
         const bool none = key_hi(a, s, i) <= key_lo(a, s, i);
-        const int64_t at = ((int64_t)(s.t0 + i) * a.n_q + h) * a.max_chunks + chunk;
-        if (chunks > 1 && g4 == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(m, sum);
+        const int64_t at = row_part(a, s, r, i, h) + chunk;
+        if (chunks > 1 && g4 == 0) *reinterpret_cast<float2*>(a.row_ml + 2 * at) = make_float2(m, sum);
 #pragma unroll
         for (int x = 0; x < 4; ++x)
 #pragma unroll
@@ -391,7 +391,7 @@ __device__ __forceinline__ void attn_rows(const AttnCall& a, int id, RowsLds<D, 
                 const int d = (4 * g4 + x) * U + u;
                 const float4 v = make_float4(o[u][x], o[u + 1][x], o[u + 2][x], o[u + 3][x]);
                 if (chunks == 1) store_part<NS == 1>(a, s.t0 + i, h, d, D, v, sum, m, none);
-                else *reinterpret_cast<float4*>(a.part_o + at * D + d) = v;
+                else *reinterpret_cast<float4*>(a.row_o + at * D + d) = v;
             }
         return;
     }
@@ -431,9 +431,9 @@ __device__ __forceinline__ void attn_rows(const AttnCall& a, int id, RowsLds<D, 
             const bool none = key_hi(a, s, i) <= key_lo(a, s, i);
             store_part<NS == 1>(a, s.t0 + i, h, d, D, acc, total, top, none);
         } else {
-            const int64_t at = ((int64_t)(s.t0 + i) * a.n_q + h) * a.max_chunks + chunk;
-            *reinterpret_cast<float4*>(a.part_o + at * D + d) = acc;
-            if (d == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(top, total);
+            const int64_t at = row_part(a, s, r, i, h) + chunk;
+            *reinterpret_cast<float4*>(a.row_o + at * D + d) = acc;
+            if (d == 0) *reinterpret_cast<float2*>(a.row_ml + 2 * at) = make_float2(top, total);
         }
     }
 }

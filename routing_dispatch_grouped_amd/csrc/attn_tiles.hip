@@ -453,8 +453,8 @@ __device__ __forceinline__ void attn_tiles(const AttnCall& a, int id, TileLds<D>
         if (row >= rows) continue;
         const int i = row / G, h = head * G + row % G;
         const bool none = hi[rb] <= lo[rb];
-        const int64_t at = ((int64_t)(s.t0 + i) * a.n_q + h) * a.max_chunks + chunk;
-        if (keys.chunks > 1 && half == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(m[rb], total);
+        const int64_t at = ((int64_t)(s.t0 + i) * a.n_q + h) * a.tile_chunks + chunk;
+        if (keys.chunks > 1 && half == 0) *reinterpret_cast<float2*>(a.tile_ml + 2 * at) = make_float2(m[rb], total);
 #pragma unroll
         for (int db = 0; db < DB; ++db)
 #pragma unroll
@@ -463,7 +463,7 @@ __device__ __forceinline__ void attn_tiles(const AttnCall& a, int id, TileLds<D>
                 const float4 v =
                     make_float4(o[rb][db][4 * j], o[rb][db][4 * j + 1], o[rb][db][4 * j + 2], o[rb][db][4 * j + 3]);
                 if (keys.chunks == 1) store_part<true>(a, s.t0 + i, h, d, D, v, total, m[rb], none);
-                else *reinterpret_cast<float4*>(a.part_o + at * D + d) = v;
+                else *reinterpret_cast<float4*>(a.tile_o + at * D + d) = v;
             }
     }
 }

@@ -253,7 +253,11 @@ hipError_t launch_qk_store(QkStoreCall a, int head_dim, bool bf16, int seg_cap, 
 struct AttnCall {
     const void* q;
     void* out;
-    float *lse, *part_o, *part_ml;  // parts of rows whose keys are split: [T, n_q, max_chunks] x (D, 2)
+    float* lse;
+    // parts of rows whose keys are split, [places, n_q, chunks] x (D, 2): a token of a short request
+    // has place r * row_place + i (row_place 0: its number t), one of a long request t
+    float *row_o, *row_ml, *tile_o, *tile_ml;
+    int row_place;
     const int32_t *block_table, *cu_q, *kv_len;
     const uint8_t *k_codes, *v_codes;
     const float *k_scale, *v_scale;
@@ -262,7 +266,6 @@ struct AttnCall {
     float scale_log2;              // softmax scale times log2(e)
     int T, R, n_q, n_kv, group, max_blocks, n_pages, page_shift, kv_cap, max_q, window;
     bool causal;
-    int max_chunks;  // parts that the workspace has for each row
     // requests of up to n_most queries: tiles of rows_per_tile rows, chunk keys a workgroup
     int n_most, rows_per_tile, row_tiles, chunk, row_chunks;
     // longer ones: tile_slots places for tiles of tile_rows rows, tile_chunk keys a workgroup
