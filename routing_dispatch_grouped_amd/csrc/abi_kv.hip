@@ -45,11 +45,18 @@ int cache_buffers_rc(const rdg_kv_cache* C) {
 // requests of 3 queries, 5000 keys, 8 heads a key head 14.8 against 17.5; 31 requests
 // of 35 rows 39.8 against 46.8.
 constexpr int kChunkMin = 256;
-constexpr int kWaveKeys = 1024;  // keys whose pages the lanes of a k_attn_rows wave hold
+constexpr int kWaveKeys = 1024;  // keys whose pages the lanes of a k_attn_rows wave hold at a time
 // k_attn_rows workgroups wanted, four per CU.  31 requests of 35 rows 39.8, with 512 46.9,
 // with 2048 44.5; 16 requests of 64 rows 40.6, 40.3 and 49.1; 64 requests of one row 64,
 // 62 and 62.
 constexpr int kRowUnits = 1024;
+// Bytes of parts that k_attn_rows may leave to be joined; where the longest chunks below come to more,
+// they grow.  That many parts are 4000 workgroups of 64 rows and more, so the chip stays
+// full, but a chunk is also the longest walk beside a batch's long requests.  One chunk of 4096
+// tokens and 31 decode rows of up to 4000 keys under a bound of 32768, 64 / 8 heads: 384, with 128
+// MiB 402, unbounded (4.2 GiB) 384; four fp32 prompts of 2048, whose rows fill the chip: 456
+// without parts, 690 with 4.2 GiB of them.
+constexpr size_t kRowParts = (size_t)256 << 20;
 // k_attn_tiles workgroups wanted, two per CU; above it rows go in tiles of 256, below
 // half of it keys are split.  Prompts of 32 / 8 heads: 1000 tokens 33, with 256 33, with 1024
 // 47; 2000 tokens 63, 67 and 83; 4000 tokens 163, 153 and 159; 300 tokens on
@@ -82,6 +89,14 @@ size_t parts_bytes(int64_t places, int n_q, int head_dim, int chunks) {
 int chunks_of(int64_t span, int chunk) {
     const int64_t keys = span + 63 < kMaxKeys ? span + 63 : kMaxKeys, n = (keys + chunk - 1) / chunk;
     return n < 1 ? 1 : (int)n;
+}
+
+// Chunks that a run of span keys fills `room` times at most.
+void coarsen(int* chunk, int* chunks, int span, int64_t room) {
+    if (*chunks <= room) return;
+    const int64_t keys = span + 63 < kMaxKeys ? span + 63 : kMaxKeys;
+    *chunk = (int)(((keys + room - 1) / room + kChunkMin - 1) / kChunkMin * kChunkMin);
+    *chunks = chunks_of(span, *chunk);
 }
 
 AttnPlan plan_attn(int T, int R, int n_kv, int group, int head_dim, bool bf16, int max_q, int span) {
@@ -122,9 +137,11 @@ AttnPlan plan_attn(int T, int R, int n_kv, int group, int head_dim, bool bf16, i
         p.chunk = want > most ? most : (int)want;
         p.row_chunks = chunks_of(span, p.chunk);
         // Beside long requests most tokens are not the short ones': those then have n_most places a request.
-        const int64_t places = (int64_t)R * p.n_most;
-        p.row_place = places < T ? p.n_most : 0;
-        p.row_bytes = parts_bytes(places < T ? places : T, n_kv * group, head_dim, p.row_chunks);
+        const int64_t by_request = (int64_t)R * p.n_most, places = by_request < T ? by_request : T;
+        p.row_place = by_request < T ? p.n_most : 0;
+        const size_t room = kRowParts / (sizeof(float) * (size_t)places * n_kv * group * (head_dim + 2));
+        coarsen(&p.chunk, &p.row_chunks, span, room > 0 ? (int64_t)room : 1);
+        p.row_bytes = parts_bytes(places, n_kv * group, head_dim, p.row_chunks);
     }
     return p;
 }
@@ -249,14 +266,8 @@ int rdg_paged_attention(const void* q, int dtype, int64_t q_stride, int T, int n
     AttnPlan p = plan_attn(T, a.R, a.n_kv, a.group, D, bf16, max_q, span);
     const size_t need = most.row_bytes + most.tile_bytes;
     if (need > 0 && (!work || !aligned16(work) || work_bytes < need)) return RDG_EINVAL;
-    const auto fit = [&](int* chunk, int* chunks, int room) {
-        if (*chunks <= room) return;
-        const int64_t keys = span + 63 < kMaxKeys ? span + 63 : kMaxKeys;
-        *chunk = (int)(((keys + room - 1) / room + kChunkMin - 1) / kChunkMin * kChunkMin);
-        *chunks = chunks_of(span, *chunk);
-    };
-    if (p.tile_slots > 0) fit(&p.tile_chunk, &p.tile_chunks, most.tile_chunks);
-    if (p.n_most > 0) fit(&p.chunk, &p.row_chunks, most.row_chunks);
+    if (p.tile_slots > 0) coarsen(&p.tile_chunk, &p.tile_chunks, span, most.tile_chunks);
+    if (p.n_most > 0) coarsen(&p.chunk, &p.row_chunks, span, most.row_chunks);
     a.n_most = p.n_most, a.rows_per_tile = 16 * p.rt, a.row_tiles = p.row_tiles, a.chunk = p.chunk;
     a.row_chunks = p.row_chunks, a.tile_rows = p.tile_rows, a.tile_slots = p.tile_slots;
     a.tile_chunk = p.tile_chunk, a.tile_chunks = p.tile_chunks;

@@ -160,15 +160,20 @@ __device__ __forceinline__ void attn_rows(const AttnCall& a, int id, RowsLds<D, 
             }
     }
 
-    // page and scales of each of this wave's 16-key groups, one per lane
-    const int my_key = k0 + (lane / GP * KG + wave) * kBlock + lane % GP * 16;
+    // page and scales of this wave's 16-key groups, one per lane: those of kHeld steps (1024 keys) from `step` on
+    constexpr int kHeld = kWave / GP;
     int my_page = 0;
     float my_ks = 1.0f, my_vs = 1.0f;
-    if (my_key < k1) {
-        my_page = page_of(a, r, my_key);
-        my_ks = pow2_scale(a.k_scale[(int64_t)my_page * a.n_kv + head]);
-        my_vs = pow2_scale(a.v_scale[(int64_t)my_page * a.n_kv + head]);
-    }
+    const auto load_pages = [&](int step) {
+        const int key = k0 + ((step + lane / GP) * KG + wave) * kBlock + lane % GP * 16;
+        my_page = 0;
+        my_ks = my_vs = 1.0f;
+        if (key < k1) {
+            my_page = page_of(a, r, key);
+            my_ks = pow2_scale(a.k_scale[(int64_t)my_page * a.n_kv + head]);
+            my_vs = pow2_scale(a.v_scale[(int64_t)my_page * a.n_kv + head]);
+        }
+    };
 
     f32x4_t o[U];
     float m = -__builtin_inff(), l = 0.0f;
@@ -191,16 +196,17 @@ __device__ __forceinline__ void attn_rows(const AttnCall& a, int id, RowsLds<D, 
         return key * D + 16 * (piece ^ turn);
     };
     const auto v_row = [&](int key) { return (key & ~15) | ((key & 3) << 2) | ((key >> 2) & 3); };
-    const auto fetch = [&](int step) {
+    const auto fetch = [&](int step, int held) {  // held: the step's first group among those held
         const int kb = k0 + (step * KG + wave) * kBlock;
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
             const int u = rt * kWave + p * ST;  // of the wave's first lane: one 16-key group for all
             if (2 * PK % ST == 0 || u < 2 * PK) {
-                const int y = u % PK, g = y / D, page = __builtin_amdgcn_readlane(my_page, step * GP + g);
+                const int y = u % PK, g = y / D, page = __builtin_amdgcn_readlane(my_page, held + g);
                 const uint8_t* from = (u < PK ? a.k_codes : a.v_codes) +
                     ((((int64_t)page * a.n_kv + head) << a.page_shift) + ((kb + 16 * g) & in_page)) * D + y % D * 16;
                 stg[p] = *reinterpret_cast<const u32x4_t*>(from + 16 * lane);
+                __builtin_amdgcn_sched_barrier(0x38f);  // loads in the order of their use: the waits then go one by one
             }
         }
     };
@@ -233,125 +239,130 @@ __device__ __forceinline__ void attn_rows(const AttnCall& a, int id, RowsLds<D, 
 
     const int span = k1 - k0 - (RT > 1 ? 0 : wave * kBlock);
     const int steps = span > 0 ? (span + KG * kBlock - 1) / (KG * kBlock) : 0;
-    if (steps > 0) {
-        fetch(0);
-        if constexpr (RT > 1) {
-            pass_on(0);
-            if (steps > 1) fetch(1);
-            __syncthreads();
-        }
-    }
     const float c = a.scale_log2;
     uint32_t saw_nan = 0;
-    for (int step = 0; step < steps; ++step) {
-        const int kb = k0 + (step * KG + wave) * kBlock;
-        if constexpr (RT == 1) {
-            pass_on(step);
-            if (step + 1 < steps) fetch(step + 1);
+    // kHeld steps at a time.  The loads do not run ahead from one such run into the next: holding two
+    // sets of pages for that takes registers that four row tiles of 128 do not have at three waves a SIMD.
+    for (int s0 = 0, s1; s0 < steps; s0 = s1) {
+        s1 = s0 + kHeld < steps ? s0 + kHeld : steps;
+        load_pages(s0);
+        fetch(s0, 0);
+        if constexpr (RT > 1) {
+            pass_on(s0);
+            if (s0 + 1 < s1) fetch(s0 + 1, GP);
+            __syncthreads();
         }
-        take_k(step);
-        f32x4_t sc[GP];
-#pragma unroll
-        for (int t = 0; t < GP; ++t) {
-            const float ks = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_ks), step * GP + t));
-            sc[t] = f32x4_t{0, 0, 0, 0};
-#pragma unroll
-            for (int j = 0; j < KJ; ++j) {
-                const bf16x8_t k_lo = codes_to_bf16(kreg[t][j].x, kreg[t][j].y, ks, ks);
-                const bf16x8_t k_hi = codes_to_bf16(kreg[t][j].z, kreg[t][j].w, ks, ks);
-#pragma unroll
-                    for (int n = NS - 1; n >= 0; --n) {  // small parts first
-                        sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k_lo, q[2 * j][n], sc[t], 0, 0, 0);
-                        sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k_hi, q[2 * j + 1][n], sc[t], 0, 0, 0);
-                    }
+        for (int step = s0; step < s1; ++step) {
+            const int kb = k0 + (step * KG + wave) * kBlock, held = (step - s0) * GP;
+            if constexpr (RT == 1) {
+                pass_on(step);
+                if (step + 1 < s1) fetch(step + 1, held + GP);
             }
-        }
-        take_v(step);
-        const bool masked = kb < all_lo || kb + kBlock > all_hi;
-        if (masked) {
+            take_k(step);
+            f32x4_t sc[GP];
+#pragma unroll
+            for (int t = 0; t < GP; ++t) {
+                const float ks = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_ks), held + t));
+                sc[t] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < KJ; ++j) {
+                    const bf16x8_t k_lo = codes_to_bf16(kreg[t][j].x, kreg[t][j].y, ks, ks);
+                    const bf16x8_t k_hi = codes_to_bf16(kreg[t][j].z, kreg[t][j].w, ks, ks);
+#pragma unroll
+                        for (int n = NS - 1; n >= 0; --n) {  // small parts first
+                            sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k_lo, q[2 * j][n], sc[t], 0, 0, 0);
+                            sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k_hi, q[2 * j + 1][n], sc[t], 0, 0, 0);
+                        }
+                }
+            }
+            take_v(step);
+            const bool masked = kb < all_lo || kb + kBlock > all_hi;
+            if (masked) {
+#pragma unroll
+                    for (int t = 0; t < GP; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int key = kb + 16 * t + 4 * g4 + i;
+                            if (key < lo || key >= hi) sc[t][i] = -__builtin_inff();
+                        }
+                // keys that no row sees may hold anything
 #pragma unroll
                 for (int t = 0; t < GP; ++t)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int key = kb + 16 * t + 4 * g4 + i;
-                        if (key < lo || key >= hi) sc[t][i] = -__builtin_inff();
+                        const bool any = key >= any_lo && key < any_hi;
+#pragma unroll
+                        for (int w = 0; w < W; ++w) {
+                            vreg[t][i][w] = any ? vreg[t][i][w] : 0;
+                            const uint32_t nan = nan_bytes(vreg[t][i][w]);
+                            vreg[t][i][w] = without_nan(vreg[t][i][w], nan);
+                            saw_nan |= nan;
+                        }
                     }
-            // keys that no row sees may hold anything
-#pragma unroll
-            for (int t = 0; t < GP; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int key = kb + 16 * t + 4 * g4 + i;
-                    const bool any = key >= any_lo && key < any_hi;
-#pragma unroll
-                    for (int w = 0; w < W; ++w) {
-                        vreg[t][i][w] = any ? vreg[t][i][w] : 0;
-                        const uint32_t nan = nan_bytes(vreg[t][i][w]);
-                        vreg[t][i][w] = without_nan(vreg[t][i][w], nan);
-                        saw_nan |= nan;
-                    }
-                }
-        }
-        bf16x8_t p[GP / 2][NS];
-        {
-            float top = -__builtin_inff();
-#pragma unroll
-            for (int t = 0; t < GP; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[t][i]);
-            top = max_quarters(top);
-            const float m_new = fmaxf(m, top * c);
-            if (__any(m_new > m + kSlack)) {
-                const float shrink = __builtin_amdgcn_exp2f(m - (m_new == -__builtin_inff() ? 0.0f : m_new));
-                l *= shrink;
-#pragma unroll
-                for (int u = 0; u < U; ++u) o[u] *= shrink;
-                m = m_new;
             }
-            const float ref = m == -__builtin_inff() ? 0.0f : m;
-            float sum = 0.0f;
+            bf16x8_t p[GP / 2][NS];
+            {
+                float top = -__builtin_inff();
 #pragma unroll
-            for (int t = 0; t < GP; ++t)
+                for (int t = 0; t < GP; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float e = __builtin_amdgcn_exp2f(fmaf(sc[t][i], c, -ref));
-                    sum += e;
-                    __bf16 part[NS];
-                    split_bf16<NS>(e, part);
+                    for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[t][i]);
+                top = max_quarters(top);
+                const float m_new = fmaxf(m, top * c);
+                if (__any(m_new > m + kSlack)) {
+                    const float shrink = __builtin_amdgcn_exp2f(m - (m_new == -__builtin_inff() ? 0.0f : m_new));
+                    l *= shrink;
 #pragma unroll
-                    for (int n = 0; n < NS; ++n) p[t / 2][n][(t & 1) * 4 + i] = part[n];
+                    for (int u = 0; u < U; ++u) o[u] *= shrink;
+                    m = m_new;
                 }
-            l += sum;
-        }
-        // O^T += V^T P^T; column of output tile u in lane col: col * U + u
+                const float ref = m == -__builtin_inff() ? 0.0f : m;
+                float sum = 0.0f;
 #pragma unroll
-        for (int t2 = 0; t2 < GP / 2; ++t2) {
-            const float va = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_vs), step * GP + 2 * t2));
-            const float vb = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_vs), step * GP + 2 * t2 + 1));
+                for (int t = 0; t < GP; ++t)
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                uint32_t in[4], x[4], y[4];
+                    for (int i = 0; i < 4; ++i) {
+                        const float e = __builtin_amdgcn_exp2f(fmaf(sc[t][i], c, -ref));
+                        sum += e;
+                        __bf16 part[NS];
+                        split_bf16<NS>(e, part);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) in[i] = vreg[2 * t2][i][w];
-                transpose4(in, x);
+                        for (int n = 0; n < NS; ++n) p[t / 2][n][(t & 1) * 4 + i] = part[n];
+                    }
+                l += sum;
+            }
+            // O^T += V^T P^T; column of output tile u in lane col: col * U + u
 #pragma unroll
-                for (int i = 0; i < 4; ++i) in[i] = vreg[2 * t2 + 1][i][w];
-                transpose4(in, y);
+            for (int t2 = 0; t2 < GP / 2; ++t2) {
+                const float va = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_vs), held + 2 * t2));
+                const float vb = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_vs), held + 2 * t2 + 1));
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const bf16x8_t v = codes_to_bf16(x[b], y[b], va, vb);
-                    const int u = 4 * w + b;
+                for (int w = 0; w < W; ++w) {
+                    uint32_t in[4], x[4], y[4];
 #pragma unroll
-                        for (int n = NS - 1; n >= 0; --n)
-                            o[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[t2][n], o[u], 0, 0, 0);
+                    for (int i = 0; i < 4; ++i) in[i] = vreg[2 * t2][i][w];
+                    transpose4(in, x);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) in[i] = vreg[2 * t2 + 1][i][w];
+                    transpose4(in, y);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const bf16x8_t v = codes_to_bf16(x[b], y[b], va, vb);
+                        const int u = 4 * w + b;
+#pragma unroll
+                            for (int n = NS - 1; n >= 0; --n)
+                                o[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[t2][n], o[u], 0, 0, 0);
+                    }
                 }
             }
+            if constexpr (RT > 1) {
+                if (step + 1 < s1) pass_on(step + 1);
+                if (step + 2 < s1) fetch(step + 2, held + 2 * GP);
+                __syncthreads();
+            }
         }
-        if constexpr (RT > 1) {
-            if (step + 1 < steps) pass_on(step + 1);
-            if (step + 2 < steps) fetch(step + 2);
-            __syncthreads();
-        }
+        __builtin_amdgcn_s_waitcnt(0x0f70);  // no load is in flight here: says so, else the next ones wait for the scales
     }
 
     if (__any(saw_nan != 0)) {

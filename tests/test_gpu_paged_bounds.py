@@ -5,7 +5,7 @@ import torch
 
 from harness import DEV, rdg
 from oracle import paged
-from test_gpu_paged import EPS, attn_case, begin, call, check, dev, host
+from test_gpu_paged import ATTNS, EPS, MIXES, attn_case, begin, call, check, dev, host
 
 pytestmark = pytest.mark.gpu
 
@@ -141,3 +141,62 @@ def test_prefill_with_a_bound_of_any_size(max_kv):
     out, lse = call(c, 0.1, max_kv=max_kv)
     assert c["m"].rdg_check_status(c["step"]) == (0, 0)
     check(c, out, lse, 0.1)
+
+
+LONG = [
+    # kv, q, P, n_q, n_kv: few rows a request, whose keys one workgroup walks past the pages that a wave holds at a time
+    ([9000, 4100, 300, 0], [1, 1, 1, 0], 64, 8, 2),
+    ([4500, 2049, 70], [5, 3, 5], 16, 8, 2),
+    ([2500, 1025, 1024], [9, 9, 1], 32, 4, 1),
+    ([2500, 3100, 40], [16, 2, 16], 128, 8, 2),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("case", range(len(LONG)))
+def test_few_rows_with_a_bound_of_any_size(case, D, dtype):
+    """A bound of 2^31 - 1 keys leaves each request one part."""
+    c = attn_case(*LONG[case], D, dtype, 120 + case)
+    for window in (0, 1500):
+        out, lse = call(c, 0.1, window=window, max_kv=(1 << 31) - 1)
+        assert c["m"].rdg_check_status(c["step"]) == (0, 0)
+        check(c, out, lse, 0.1, window=window)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_row_tiles_past_the_pages_held_at_a_time(D):
+    """Long requests' tiles, unsplit under the same bound, whose keys pass two loads of pages."""
+    c = attn_case([2600, 1100, 1024], [40, 100, 33], 16, 8, 2, D, "bf16", 125)
+    for window in (0, 1500):
+        out, lse = call(c, 0.1, window=window, max_kv=(1 << 31) - 1)
+        assert c["m"].rdg_check_status(c["step"]) == (0, 0)
+        check(c, out, lse, 0.1, window=window)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("case", range(len(MIXES)))
+def test_mixed_batches_with_a_bound_of_any_size(case, dtype):
+    c = attn_case(*MIXES[case], dtype, 130 + case)
+    out, lse = call(c, 0.1, max_kv=(1 << 31) - 1)
+    assert c["m"].rdg_check_status(c["step"]) == (0, 0)
+    check(c, out, lse, 0.1)
+
+
+def test_nan_past_the_pages_held_at_a_time():
+    c = attn_case([2600], [16], 16, 4, 1, 64, "bf16", 140)
+    ref, _ = call(c, 0.1, max_kv=(1 << 31) - 1)
+    key = 2590                                                   # seen by the last ten queries
+    c["cache"].v[c["table"][0, key // 16], 0, key % 16, 7] = 0x7f
+    out, _ = call(c, 0.1, max_kv=(1 << 31) - 1)
+    want = torch.zeros_like(out, dtype=torch.bool)
+    want[6:, :, 7] = True
+    assert torch.equal(torch.isnan(out), want) and torch.equal(out[~want], ref[~want])
+
+
+@pytest.mark.parametrize("case", range(len(ATTNS)))
+def test_float_queries_without_a_causal_mask(case):
+    c = attn_case(*ATTNS[case], "f32", 150 + case)
+    out, lse = call(c, 0.1, causal=False)
+    assert c["m"].rdg_check_status(c["step"]) == (0, 0)
+    check(c, out, lse, 0.1, causal=False)

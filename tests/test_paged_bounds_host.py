@@ -41,3 +41,22 @@ def test_workspace_of_a_mixed_batch_is_that_of_its_short_requests(T, max_kv):
     short = 8                                # queries of 8 heads a key head that a 64-row workgroup takes
     alone = workspace(32 * short, 32, 64, 8, 128, short, max_kv, "bf16")
     assert 0 < workspace(T, 32, 64, 8, 128, T - 31, max_kv, "bf16") == alone
+
+
+@pytest.mark.parametrize("T,n_req,n_q,max_q,dtype", [(4127, 32, 64, 4096, "bf16"), (8192, 64, 64, 2048, "bf16"),
+                                                     (256, 256, 64, 1, "bf16"), (4096, 4096, 128, 1, "bf16"),
+                                                     (100, 1, 64, 100, "bf16"), (2048, 64, 32, 1985, "bf16"),
+                                                     (8192, 4, 32, 2048, "f32"), (1000, 9, 32, 500, "f32"), (64, 64, 64, 1, "f32")])
+@pytest.mark.parametrize("head_dim", [64, 128, 256])
+def test_workspace_is_bounded(T, n_req, n_q, max_q, dtype, head_dim):
+    """256 MiB of the short requests' parts, and of the long ones' what 256 workgroups of 128 rows and two parts more
+    a row come to, however long the contexts."""
+    most = (256 << 20) + 256 + (512 + 2 * 256) * 128 * (head_dim + 2) * 4
+    for max_kv in (5000, 32768, 131072, 1 << 20, (1 << 31) - 1):
+        assert workspace(T, n_req, n_q, 8, head_dim, max_q, max_kv, dtype) <= most
+
+
+def test_rows_that_fill_the_chip_leave_no_parts():
+    for max_kv in (32768, 131072):
+        assert workspace(8192, 4, 32, 8, 128, 2048, max_kv, "f32") == 0
+        assert workspace(4096, 1, 64, 8, 128, 4096, max_kv, "bf16") == 0
