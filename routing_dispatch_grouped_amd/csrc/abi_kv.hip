@@ -73,7 +73,7 @@ constexpr int kMaxKeys = 1 << 30;
 // queries see together.
 struct AttnPlan {
     int rt;  // 16-row tiles per workgroup of k_attn_rows
-    int n_most, row_tiles, chunk, row_chunks;
+    int n_most, row_places, chunk, row_chunks;
     int tile_rows, tile_slots, tile_chunk, tile_chunks;  // tile_slots 0: no k_attn_tiles
     // workspace: parts of the short requests' rows by request (row_place each) or by token (0), then the long ones' by token
     int row_place;
@@ -129,9 +129,10 @@ AttnPlan plan_attn(int T, int R, int n_kv, int group, int head_dim, bool bf16, i
     if (p.n_most > 0) {
         const int64_t rows = (int64_t)p.n_most * group;
         p.rt = rows <= 64 && !tiles ? (int)((rows + 15) / 16) : 4;
-        p.row_tiles = (int)((rows + 16 * p.rt - 1) / (16 * p.rt));
+        // one tile a request, or places for the tiles of all (see request_of_place)
+        if (rows > 16 * p.rt) p.row_places = (int)((int64_t)T * group / (16 * p.rt) + R);
         const int most = kWaveKeys * (p.rt == 1 ? 4 : p.rt == 2 ? 2 : 1);
-        const double units = (double)R * n_kv * p.row_tiles;
+        const double units = (double)n_kv * (p.row_places > 0 ? p.row_places : R);
         double want = ceil(span * units / kRowUnits / kChunkMin) * kChunkMin;
         if (want < kChunkMin) want = kChunkMin;
         p.chunk = want > most ? most : (int)want;
@@ -268,7 +269,7 @@ int rdg_paged_attention(const void* q, int dtype, int64_t q_stride, int T, int n
     if (need > 0 && (!work || !aligned16(work) || work_bytes < need)) return RDG_EINVAL;
     if (p.tile_slots > 0) coarsen(&p.tile_chunk, &p.tile_chunks, span, most.tile_chunks);
     if (p.n_most > 0) coarsen(&p.chunk, &p.row_chunks, span, most.row_chunks);
-    a.n_most = p.n_most, a.rows_per_tile = 16 * p.rt, a.row_tiles = p.row_tiles, a.chunk = p.chunk;
+    a.n_most = p.n_most, a.rows_per_tile = 16 * p.rt, a.row_places = p.row_places, a.chunk = p.chunk;
     a.row_chunks = p.row_chunks, a.tile_rows = p.tile_rows, a.tile_slots = p.tile_slots;
     a.tile_chunk = p.tile_chunk, a.tile_chunks = p.tile_chunks;
     a.row_place = p.row_place;

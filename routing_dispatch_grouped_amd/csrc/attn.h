@@ -16,6 +16,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // an exact result costs 0.0017.
 constexpr float kSlack = 8.0f;
 
+// k_attn_rows workgroups for each key head and chunk.
+inline int row_tiles(const AttnCall& a) { return a.row_places > 0 ? a.row_places : a.R; }
+
 // A request's queries and keys.  Query i has position kv - n + i.
 struct ReqSpan {
     int t0, n, kv;
@@ -41,6 +44,27 @@ __device__ __forceinline__ ReqSpan req_span(const AttnCall& a, int r) {
         s.n = 0;
     }
     return s;
+}
+
+// Row tiles of `rows` rows by place: request r's have the places from
+// floor(cu_q[r] * group / rows) + r on, as many as it can need, whatever its
+// neighbours' lengths, so T * group / rows + R places hold every request's.  The
+// request of a place (wave-uniform; -1: none), and the first place of its tiles:
+__device__ __forceinline__ int request_of_place(const AttnCall& a, int place, int rows) {
+    int r = -1;
+    for (int b = 0; b < a.R; b += kWave) {
+        const int i = b + lane_id();
+        bool before = false;
+        if (i < a.R) {
+            const int t = a.cu_q[i];
+            before = (int64_t)(t < 0 ? 0 : t) * a.group / rows + i <= place;
+        }
+        r += __popcll(__ballot(before));
+    }
+    return __builtin_amdgcn_readfirstlane(r);
+}
+__device__ __forceinline__ int first_place(const AttnCall& a, const ReqSpan& s, int r, int rows) {
+    return (int)((int64_t)s.t0 * a.group / rows + r);
 }
 
 // Keys [lo, hi) that query i of the request sees (hi <= lo: none).

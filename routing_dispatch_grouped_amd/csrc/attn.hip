@@ -66,7 +66,7 @@ __global__ __launch_bounds__(kJoinWaves * kWave) void k_attn_join(AttnCall a) {
 
 template <int D, int NS, int RT>
 hipError_t launch_rows(const AttnCall& a, hipStream_t s) {
-    const int64_t grid = (int64_t)a.n_kv * a.row_tiles * a.R * a.row_chunks;
+    const int64_t grid = (int64_t)a.n_kv * row_tiles(a) * a.row_chunks;
     if (grid >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;
     k_attn_rows<D, NS, RT><<<(unsigned)grid, RT * key_groups<RT>() * kWave, 0, s>>>(a);
     return hipGetLastError();

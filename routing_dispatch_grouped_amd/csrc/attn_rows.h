@@ -109,12 +109,21 @@ __device__ __forceinline__ void attn_rows(const AttnCall& a, int id, RowsLds<D, 
     const int col = lane & 15, g4 = lane >> 4;
     const int head = id % a.n_kv;
     id /= a.n_kv;
-    const int tile = id % a.row_tiles;
-    id /= a.row_tiles;
-    const int r = id % a.R, chunk = id / a.R;
+    // bf16 requests have one tile at most here; tiles of longer fp32 ones go by place
+    int r, chunk, place = 0;
+    if (NS > 1 && a.row_places > 0) {
+        place = id % a.row_places;
+        chunk = id / a.row_places;
+        r = request_of_place(a, place, 16 * RT);
+        if (r < 0) return;
+    } else {
+        r = id % a.R;
+        chunk = id / a.R;
+    }
     const ReqSpan s = req_span(a, r);
-    const int G = a.group, rows = s.n * G, first = tile * 16 * RT;
-    if (first >= rows || s.n > a.n_most) return;
+    const int G = a.group, rows = s.n * G;
+    const int first = NS > 1 && a.row_places > 0 ? (place - first_place(a, s, r, 16 * RT)) * 16 * RT : 0;
+    if (first < 0 || first >= rows || s.n > a.n_most) return;
     const int last = first + 16 * RT < rows ? first + 16 * RT - 1 : rows - 1;
     const TileKeys keys = tile_keys(a, s, first, last + 1, a.chunk);
     const int chunks = keys.chunks;

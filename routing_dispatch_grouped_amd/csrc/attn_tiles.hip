@@ -79,23 +79,11 @@ __device__ __forceinline__ void attn_tiles(const AttnCall& a, int id, TileLds<D>
     const int head = id % a.n_kv;
     id /= a.n_kv;
     const int slot = a.tile_slots - 1 - id % a.tile_slots, chunk = id / a.tile_slots;
-    // request r's tiles have the places from floor(cu_q[r] * group / BM) + r on:
-    // as many as it can need, whatever its neighbours' lengths
-    int r = -1;
-    for (int b = 0; b < a.R; b += kWave) {
-        const int i = b + lane;
-        bool before = false;
-        if (i < a.R) {
-            const int t = a.cu_q[i];
-            before = (int64_t)(t < 0 ? 0 : t) * a.group / BM + i <= slot;
-        }
-        r += __popcll(__ballot(before));
-    }
-    r = __builtin_amdgcn_readfirstlane(r);
+    const int r = request_of_place(a, slot, BM);
     if (r < 0) return;
     const ReqSpan s = req_span(a, r);
     const int G = a.group, rows = s.n * G;
-    const int row0 = (slot - (int)((int64_t)s.t0 * G / BM + r)) * BM;
+    const int row0 = (slot - first_place(a, s, r, BM)) * BM;
     if (s.n <= a.n_most || row0 < 0 || row0 >= rows) return;
     const int row1 = row0 + BM < rows ? row0 + BM : rows;
     const TileKeys keys = tile_keys(a, s, row0, row1, a.tile_chunk);
@@ -499,7 +487,7 @@ hipError_t launch(const AttnCall& a, hipStream_t s) {
 template <int D>
 hipError_t launch_mixed(const AttnCall& a, hipStream_t s) {
     constexpr size_t bytes = sizeof(TileLds<D>) > sizeof(RowsLds<D, 4>) ? sizeof(TileLds<D>) : sizeof(RowsLds<D, 4>);
-    const int64_t tiles = tile_blocks(a), grid = tiles + (int64_t)a.n_kv * a.row_tiles * a.R * a.row_chunks;
+    const int64_t tiles = tile_blocks(a), grid = tiles + (int64_t)a.n_kv * row_tiles(a) * a.row_chunks;
     if (grid >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;
     k_attn_mixed<D><<<(unsigned)grid, 4 * kWave, bytes, s>>>(a, (int)tiles);
     return hipGetLastError();

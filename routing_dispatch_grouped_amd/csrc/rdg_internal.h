@@ -266,8 +266,9 @@ struct AttnCall {
     float scale_log2;              // softmax scale times log2(e)
     int T, R, n_q, n_kv, group, max_blocks, n_pages, page_shift, kv_cap, max_q, window;
     bool causal;
-    // requests of up to n_most queries: tiles of rows_per_tile rows, chunk keys a workgroup
-    int n_most, rows_per_tile, row_tiles, chunk, row_chunks;
+    // requests of up to n_most queries: tiles of rows_per_tile rows (one a request, or with
+    // row_places > 0 that many places for them), chunk keys a workgroup
+    int n_most, rows_per_tile, row_places, chunk, row_chunks;
     // longer ones: tile_slots places for tiles of tile_rows rows, tile_chunk keys a workgroup
     int tile_rows, tile_slots, tile_chunk, tile_chunks;
 };

@@ -200,3 +200,24 @@ def test_float_queries_without_a_causal_mask(case):
     out, lse = call(c, 0.1, causal=False)
     assert c["m"].rdg_check_status(c["step"]) == (0, 0)
     check(c, out, lse, 0.1, causal=False)
+
+
+def test_many_float_requests_beside_a_long_one():
+    """4096 requests under a bound of 4395 queries, all but one of a single token: the launch goes by the batch's
+    tokens, not by requests times the bound, which no grid holds."""
+    R, D = 4096, 64
+    q = np.ones(R, int)
+    q[1000] = 300
+    kv = np.where(q > 1, 300, 1 + np.arange(R) % 37)
+    c = attn_case(kv, q, 16, 64, 4, D, "f32", 160)
+    out, lse = call(c, 0.1, max_q=4395)
+    assert c["m"].rdg_check_status(c["step"]) == (0, 0)
+    ref, ref_lse = call(c, 0.1, max_q=300)
+    assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+    some = [0, 36, 999, 1000, 1001, 4095]
+    few = dict(c, kv=kv[some], table=c["table"][some])
+    t0 = np.concatenate([[0], np.cumsum(q)])
+    rows = np.concatenate([np.arange(t0[r], t0[r + 1]) for r in some])
+    few["x"], few["q"] = c["x"][rows], q[some]
+    few["step"] = type("Step", (), dict(cu_q=dev(np.concatenate([[0], np.cumsum(q[some])]))))
+    check(few, out[rows], lse[rows], 0.1)
