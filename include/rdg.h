@@ -424,7 +424,8 @@ int rdg_quantize_fp8_ue8m0(const void* src, int src_dtype, int rows, int cols, i
  *   head_dim   64, 128 or 256 (others: RDG_EUNSUPPORTED)
  *   k, v              [n_pages, n_kv, page_rows, head_dim] codes
  *   k_scale, v_scale  [n_pages, n_kv] fp32 powers of two (only the exponent is used)
- * Nothing needs clearing: rows that no call has stored are never read as values. */
+ * Nothing needs clearing: rows that no call has stored are never read as values.
+ * Calls whose grid no launch holds (2^32 threads and more) return RDG_EUNSUPPORTED. */
 typedef struct rdg_kv_cache {
     int32_t n_pages, page_rows, n_kv, head_dim;
     uint8_t* k;

@@ -8,7 +8,10 @@ using namespace rdg;
 
 namespace {
 
-inline int hip_rc(hipError_t e) { return e == hipSuccess ? RDG_OK : RDG_EHIP; }
+// InvalidConfiguration: sizes whose grid no launch holds.
+inline int hip_rc(hipError_t e) {
+    return e == hipSuccess ? RDG_OK : e == hipErrorInvalidConfiguration ? RDG_EUNSUPPORTED : RDG_EHIP;
+}
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -282,8 +285,10 @@ int rdg_paged_attention(const void* q, int dtype, int64_t q_stride, int T, int n
         a.tile_o = reinterpret_cast<float*>(static_cast<char*>(work) + most.row_bytes);
         a.tile_ml = a.tile_o + (size_t)T * n_q * D * p.tile_chunks;
     }
+    const bool join = p.row_chunks > 1 || p.tile_chunks > 1;
+    if (join && !grid_fits(T, kJoinThreads)) return RDG_EUNSUPPORTED;  // before anything is enqueued
     hipError_t e = p.tile_slots > 0 ? launch_attn_tiles(a, D, stream) : launch_attn_rows(a, D, bf16, stream);
-    if (e == hipSuccess && (p.row_chunks > 1 || p.tile_chunks > 1)) e = launch_attn_join(a, D, bf16, stream);
+    if (e == hipSuccess && join) e = launch_attn_join(a, D, bf16, stream);
     return hip_rc(e);
 }
 

@@ -13,10 +13,10 @@ __global__ __launch_bounds__((RT * key_groups<RT>() * kWave), D < 256 && NS == 1
 // The chunks of each row, joined in order: one wave per row, a workgroup's four
 // waves (and blockIdx.y) taking a token's heads in turn.  Rows of requests with up to n_most queries were split by
 // k_attn_rows, the others by k_attn_tiles.
-constexpr int kJoinWaves = 4;
+constexpr int kJoinWaves = kJoinThreads / kWave;
 
 template <int D, bool BF16>
-__global__ __launch_bounds__(kJoinWaves * kWave) void k_attn_join(AttnCall a) {
+__global__ __launch_bounds__(kJoinThreads) void k_attn_join(AttnCall a) {
     const int lane = lane_id(), t = (int)blockIdx.x;
     int r = -1;  // the last request that begins at or before the token
     for (int b = 0; b < a.R; b += kWave) r += __popcll(__ballot(b + lane < a.R && a.cu_q[b + lane] <= t));
@@ -66,9 +66,10 @@ __global__ __launch_bounds__(kJoinWaves * kWave) void k_attn_join(AttnCall a) {
 
 template <int D, int NS, int RT>
 hipError_t launch_rows(const AttnCall& a, hipStream_t s) {
+    constexpr int threads = RT * key_groups<RT>() * kWave;
     const int64_t grid = (int64_t)a.n_kv * row_tiles(a) * a.row_chunks;
-    if (grid >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;
-    k_attn_rows<D, NS, RT><<<(unsigned)grid, RT * key_groups<RT>() * kWave, 0, s>>>(a);
+    if (!grid_fits(grid, threads)) return hipErrorInvalidConfiguration;
+    k_attn_rows<D, NS, RT><<<(unsigned)grid, threads, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -87,8 +88,8 @@ hipError_t join_d(const AttnCall& a, bool bf16, hipStream_t s) {
     // many tokens fill the chip by themselves, and in a mixed batch most have nothing to join
     const int groups = (a.n_q + kJoinWaves - 1) / kJoinWaves;
     const dim3 grid(a.T, a.T >= 1024 && groups > 2 ? 2 : groups);
-    if (bf16) k_attn_join<D, true><<<grid, kJoinWaves * kWave, 0, s>>>(a);
-    else k_attn_join<D, false><<<grid, kJoinWaves * kWave, 0, s>>>(a);
+    if (bf16) k_attn_join<D, true><<<grid, kJoinThreads, 0, s>>>(a);
+    else k_attn_join<D, false><<<grid, kJoinThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 

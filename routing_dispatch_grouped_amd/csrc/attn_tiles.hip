@@ -479,7 +479,7 @@ template <int D, int NW>
 hipError_t launch(const AttnCall& a, hipStream_t s) {
     static_assert(sizeof(TileLds<D>) <= 160 * 1024, "LDS");
     const int64_t grid = tile_blocks(a);
-    if (grid >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;
+    if (!grid_fits(grid, NW * kWave)) return hipErrorInvalidConfiguration;
     k_attn_tiles<D, NW><<<(unsigned)grid, NW * kWave, sizeof(TileLds<D>), s>>>(a);
     return hipGetLastError();
 }
@@ -488,7 +488,7 @@ template <int D>
 hipError_t launch_mixed(const AttnCall& a, hipStream_t s) {
     constexpr size_t bytes = sizeof(TileLds<D>) > sizeof(RowsLds<D, 4>) ? sizeof(TileLds<D>) : sizeof(RowsLds<D, 4>);
     const int64_t tiles = tile_blocks(a), grid = tiles + (int64_t)a.n_kv * row_tiles(a) * a.row_chunks;
-    if (grid >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;
+    if (!grid_fits(grid, 4 * kWave)) return hipErrorInvalidConfiguration;
     k_attn_mixed<D><<<(unsigned)grid, 4 * kWave, bytes, s>>>(a, (int)tiles);
     return hipGetLastError();
 }

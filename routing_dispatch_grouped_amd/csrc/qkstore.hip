@@ -335,7 +335,7 @@ hipError_t launch_qk_store(QkStoreCall a, int head_dim, bool bf16, int seg_cap, 
     a.q_chunks = (groups + a.q_passes - 1) / a.q_passes;
     a.q_items = (int64_t)a.T * a.q_chunks;
     const int64_t pages = (int64_t)seg_cap * 2 * a.n_kv, q_blocks = (a.q_items + 3) / 4;
-    if (pages + q_blocks >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;
+    if (!grid_fits(pages + q_blocks, kThreads)) return hipErrorInvalidConfiguration;
     if (pages + q_blocks == 0) return hipSuccess;  // neither queries nor keys and values: an empty grid is an error
     a.page_items = (int)pages;
     const unsigned grid = (unsigned)(pages + q_blocks);

@@ -226,6 +226,8 @@ hipError_t launch_combine_finish(const void* y, int y_dt, const int32_t* pos, in
                                  int rows_per_sig, hipStream_t s);
 
 // Paged key/value cache: step plan, query/key norm and store, attention.
+// A launch of 2^32 threads or more in a dimension is cut short without an error.
+inline bool grid_fits(int64_t blocks, int threads) { return blocks * threads < (int64_t)1 << 32; }
 constexpr int kMaxRequests = 4096;  // per step: the plan scans them in LDS, 16 bytes each, 16 a thread
 hipError_t launch_kv_plan(const rdg_kv_step& S, const int32_t* kv_len, const int32_t* q_len, const int32_t* free_list,
                           const int32_t* n_free, int32_t* n_free_out, hipStream_t s);
@@ -272,6 +274,7 @@ struct AttnCall {
     // longer ones: tile_slots places for tiles of tile_rows rows, tile_chunk keys a workgroup
     int tile_rows, tile_slots, tile_chunk, tile_chunks;
 };
+constexpr int kJoinThreads = 256;  // one workgroup a token
 hipError_t launch_attn_rows(const AttnCall& a, int head_dim, bool bf16, hipStream_t s);
 hipError_t launch_attn_tiles(const AttnCall& a, int head_dim, hipStream_t s);
 hipError_t launch_attn_join(const AttnCall& a, int head_dim, bool bf16, hipStream_t s);

@@ -60,3 +60,26 @@ def test_rows_that_fill_the_chip_leave_no_parts():
     for max_kv in (32768, 131072):
         assert workspace(8192, 4, 32, 8, 128, 2048, max_kv, "f32") == 0
         assert workspace(4096, 1, 64, 8, 128, 4096, max_kv, "bf16") == 0
+
+
+def test_grids_that_no_launch_holds_are_refused():
+    """2^32 threads and more (the runtime launches a part of them and reports nothing): refused before anything is enqueued."""
+    import routing_dispatch_grouped_amd as rdg
+    A = 0x100000
+    c = rdg.rdg_kv_cache(4000, 16, 1, 64, A, A, A, A)
+
+    def step(n_req, t_cap, seg_cap):
+        return ctypes.byref(rdg.rdg_kv_step(n_req, 800, 16, 4000, t_cap, seg_cap, *([A] * 8)))
+
+    def store(T, n_q, n_kv, s):
+        return rdg._lib.rdg_qk_norm_rope_store(A, rdg.RDG_BF16, 4096, T, n_q, n_kv, 64, None, None, 0.0, None, 0, 0, 0, s,
+                                               ctypes.byref(c), A, 4096, None)
+
+    def attn(dtype, T, n_q, max_q, max_kv, n_req):
+        return rdg._lib.rdg_paged_attention(A, dtype, n_q * 64, T, n_q, step(n_req, T, T), ctypes.byref(c), max_q, max_kv,
+                                            0.1, 1, 0, A, n_q * 64, None, A, 1 << 30, None)
+
+    assert store(1 << 27, 1, 0, step(3, 1 << 27, 0)) == rdg.RDG_EUNSUPPORTED      # 2^25 workgroups of query waves
+    assert store(5, 0, 1, step(3, 1 << 26, 1 << 23)) == rdg.RDG_EUNSUPPORTED      # 2^24 of segments
+    assert attn(rdg.RDG_F32, 1 << 24, 64, 1 << 24, 5000, 1) == rdg.RDG_EUNSUPPORTED   # 2^24 row tiles
+    assert attn(rdg.RDG_BF16, 1 << 24, 2, 1, 5000, 2) == rdg.RDG_EUNSUPPORTED     # 2^24 tokens to join
