@@ -66,10 +66,10 @@ __device__ __forceinline__ int v_piece(int d, int c) { return c ^ (((d >> 1) & 7
 // Workgroup `id` of NW waves.
 template <int D, int NW>
 __device__ __forceinline__ void attn_tiles(const AttnCall& a, int id, TileLds<D>& lds) {
-    // 32-row blocks per wave.  Two of them halve the LDS reads per product, but at one wave
-    // a SIMD (512 registers) the copies between the register files ate that: the prompts
+    // One 32-row block a wave.  Two halve the LDS reads per product, but at one wave a
+    // SIMD (512 registers) the copies between the register files ate that: the prompts
     // above took 965 us so, 815 then with eight waves of one block each.
-    constexpr int RB = 1, NT = NW * kWave, BM = 32 * RB * NW;
+    constexpr int NT = NW * kWave, BM = 32 * NW;
     constexpr int KS = D / 16, DB = D / 32;  // reduction steps of S^T, 32-row blocks of O^T
     // Staging, per thread: KU pieces of 16 K codes, VU of 8 keys x 4 columns of V.
     constexpr int KP = kTile * D / 16, VP = 8 * D / 4;
@@ -94,20 +94,19 @@ __device__ __forceinline__ void attn_tiles(const AttnCall& a, int id, TileLds<D>
     const int k1 = any_hi < k0 + a.tile_chunk ? any_hi : k0 + a.tile_chunk;
     const int tiles = k1 > k0 ? (k1 - k0 + kTile - 1) / kTile : 0;
 
-    // this wave's rows: RB blocks of 32, one row per lane of either half
-    int lo[RB], hi[RB], all_lo[RB], all_hi[RB];
-    bf16x8_t q[RB][KS];
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-        const int first = row0 + (wave * RB + rb) * 32, row = first + col;
+    // this wave's rows: a block of 32, one per lane of either half
+    int lo, hi, all_lo, all_hi;
+    bf16x8_t q[KS];
+    {
+        const int first = row0 + wave * 32, row = first + col;
         const int i = (row < rows ? row : rows - 1) / G, h = head * G + (row < rows ? row : rows - 1) % G;
-        lo[rb] = key_lo(a, s, i);
-        hi[rb] = key_hi(a, s, i);
-        all_lo[rb] = key_lo(a, s, (first + 31 < rows ? first + 31 : rows - 1) / G);
-        all_hi[rb] = key_hi(a, s, (first < rows ? first : rows - 1) / G);
+        lo = key_lo(a, s, i);
+        hi = key_hi(a, s, i);
+        all_lo = key_lo(a, s, (first + 31 < rows ? first + 31 : rows - 1) / G);
+        all_hi = key_hi(a, s, (first < rows ? first : rows - 1) / G);
         const uint16_t* p = static_cast<const uint16_t*>(a.q) + (int64_t)(s.t0 + i) * a.q_stride + (int64_t)h * D + 8 * half;
 #pragma unroll
-        for (int x = 0; x < KS; ++x) q[rb][x] = *reinterpret_cast<const bf16x8_t*>(p + 16 * x);
+        for (int x = 0; x < KS; ++x) q[x] = *reinterpret_cast<const bf16x8_t*>(p + 16 * x);
     }
 
     // pages and scales of 16-key groups: lane l holds group 64 b + l of this chunk
@@ -199,17 +198,12 @@ __device__ __forceinline__ void attn_tiles(const AttnCall& a, int id, TileLds<D>
         }
     };
 
-    f32x16_t o[RB][DB];
-    float m[RB], l[RB];
+    f32x16_t o[DB];
+    float m = -__builtin_inff(), l = 0.0f;
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-        m[rb] = -__builtin_inff();
-        l[rb] = 0.0f;
+    for (int db = 0; db < DB; ++db)
 #pragma unroll
-        for (int db = 0; db < DB; ++db)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[rb][db][i] = 0.0f;
-    }
+        for (int i = 0; i < 16; ++i) o[db][i] = 0.0f;
     const float scale = a.scale_log2;
 
     // LDS places of this lane's operand pieces: the swizzle touches only the low
@@ -228,58 +222,45 @@ __device__ __forceinline__ void attn_tiles(const AttnCall& a, int id, TileLds<D>
         return *reinterpret_cast<const bf16x8_t*>(v + v_at[x] + db * 32 * kTile);
     };
     // A tile's logits: what the mask hides, then the largest of each row.
-    const auto mask = [&](f32x16_t (&sc)[RB][2], int t) {
+    const auto mask = [&](f32x16_t (&sc)[2], int t) {
         const int t0 = k0 + t * kTile;
+        if (t0 >= all_lo && t0 + kTile <= all_hi) return;
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-            if (t0 >= all_lo[rb] && t0 + kTile <= all_hi[rb]) continue;
+        for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int key = t0 + kb * 32 + 8 * (i / 4) + 4 * half + (i & 3);
-                    if (key < lo[rb] || key >= hi[rb]) sc[rb][kb][i] = -__builtin_inff();
-                }
-        }
+            for (int i = 0; i < 16; ++i) {
+                const int key = t0 + kb * 32 + 8 * (i / 4) + 4 * half + (i & 3);
+                if (key < lo || key >= hi) sc[kb][i] = -__builtin_inff();
+            }
     };
-    const auto row_top = [&](f32x16_t (&sc)[RB][2], int rb) {
+    const auto row_top = [&](f32x16_t (&sc)[2]) {
         float top = -__builtin_inff();
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[rb][kb][i]);
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[kb][i]);
         return max_halves(top) * scale;
     };
-    const auto raise = [&](const float (&top)[RB]) {
-        bool grows = false;
+    const auto raise = [&](float top) {
+        if (__any(top > m + kSlack)) {
+            const float m_new = fmaxf(m, top);
+            const float shrink = __builtin_amdgcn_exp2f(m - (m_new == -__builtin_inff() ? 0.0f : m_new));
+            l *= shrink;
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) grows |= top[rb] > m[rb] + kSlack;
-        if (__any(grows)) {
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb) {
-                const float m_new = fmaxf(m[rb], top[rb]);
-                const float shrink = __builtin_amdgcn_exp2f(m[rb] - (m_new == -__builtin_inff() ? 0.0f : m_new));
-                l[rb] *= shrink;
-#pragma unroll
-                for (int db = 0; db < DB; ++db) o[rb][db] *= shrink;
-                m[rb] = m_new;
-            }
+            for (int db = 0; db < DB; ++db) o[db] *= shrink;
+            m = m_new;
         }
     };
     // One tile: its probabilities beside the next tile's logits; then its V product
     // beside the next maximum and the staging of K(t + 2) and V(t + 1).
-    const auto tile = [&](f32x16_t (&sc)[RB][2], f32x16_t (&next)[RB][2], int t, auto parity) {
+    const auto tile = [&](f32x16_t (&sc)[2], f32x16_t (&next)[2], int t, auto parity) {
         constexpr int B = decltype(parity)::value;
         constexpr int KG = KS / 4;
         const std::integral_constant<int, 0> set0;
         const uint16_t *k_next = lds.k[1 - B], *v_now = lds.v[B];
-        bf16x8_t p[RB][4];
-        float sum[RB], ref[RB];
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-            sum[rb] = 0.0f;
-            ref[rb] = m[rb] == -__builtin_inff() ? 0.0f : m[rb];
-        }
+        bf16x8_t p[4];
+        float sum = 0.0f;
+        const float ref = m == -__builtin_inff() ? 0.0f : m;
         __builtin_amdgcn_s_setprio(1);
         // Nine steps: the products of group g - 1, with their operands read two
         // steps before, beside the exponentials of group g.
@@ -301,42 +282,33 @@ __device__ __forceinline__ void attn_tiles(const AttnCall& a, int id, TileLds<D>
                     vf[g - 7][1] = v_frag(v_now, 0, 2 * (g - 7) + 1);
                 }
                 // past the last tile: of an old buffer, not used
+                if ((w & 3) == 0)
 #pragma unroll
-                for (int rb = 0; rb < RB; ++rb) {
-                    if ((w & 3) == 0)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) next[rb][kb][i] = 0.0f;
-                }
+                    for (int i = 0; i < 16; ++i) next[kb][i] = 0.0f;
 #pragma unroll
                 for (int x = 0; x < KG; ++x)
-#pragma unroll
-                    for (int rb = 0; rb < RB; ++rb)
-                        next[rb][kb] =
-                            __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[w % 3][x], q[rb][(w & 3) * KG + x], next[rb][kb], 0, 0, 0);
+                    next[kb] =
+                        __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[w % 3][x], q[(w & 3) * KG + x], next[kb], 0, 0, 0);
             }
             if (g < 8) {
 #pragma unroll
-                for (int rb = 0; rb < RB; ++rb) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float e = __builtin_amdgcn_exp2f(fmaf(sc[rb][g / 4][4 * (g & 3) + i], scale, -ref[rb]));
-                        sum[rb] += e;
-                        p[rb][g / 2][4 * (g & 1) + i] = (__bf16)e;
-                    }
-                    // summed here and not behind the loop, where all the exponentials would have to be kept
-                    asm volatile("" : "+v"(sum[rb]));
+                for (int i = 0; i < 4; ++i) {
+                    const float e = __builtin_amdgcn_exp2f(fmaf(sc[g / 4][4 * (g & 3) + i], scale, -ref));
+                    sum += e;
+                    p[g / 2][4 * (g & 1) + i] = (__bf16)e;
                 }
+                // summed here and not behind the loop, where all the exponentials would have to be kept
+                asm volatile("" : "+v"(sum));
             }
         }
         __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) l[rb] += sum[rb];
+        l += sum;
         if (t + 1 < tiles) {
             mask(next, t + 1);
             clean(t + 1, set0);
         }
         __builtin_amdgcn_s_setprio(0);
-        float top[RB];
+        float top;
         constexpr int G2 = 2 * DB;
 #pragma unroll
         for (int g = 0; g < G2; ++g) {
@@ -347,10 +319,7 @@ __device__ __forceinline__ void attn_tiles(const AttnCall& a, int id, TileLds<D>
             }
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-#pragma unroll
-                for (int rb = 0; rb < RB; ++rb)
-                    o[rb][g / 2] =
-                        __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[g & 3][x], p[rb][2 * (g & 1) + x], o[rb][g / 2], 0, 0, 0);
+                o[g / 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[g & 3][x], p[2 * (g & 1) + x], o[g / 2], 0, 0, 0);
             // staged past the last tile: never read
 #pragma unroll
             for (int u = 0; u < VU; ++u)
@@ -358,9 +327,7 @@ __device__ __forceinline__ void attn_tiles(const AttnCall& a, int id, TileLds<D>
 #pragma unroll
             for (int u = 0; u < KU; ++u)
                 if (g == (1 + u) % G2) stage_k(lds.k[B], t + 2, u, set0);
-            if (g == G2 - 1)
-#pragma unroll
-                for (int rb = 0; rb < RB; ++rb) top[rb] = row_top(next, rb);
+            if (g == G2 - 1) top = row_top(next);
         }
         __builtin_amdgcn_sched_barrier(0);
         if (t + 1 < tiles) raise(top);
@@ -371,8 +338,7 @@ __device__ __forceinline__ void attn_tiles(const AttnCall& a, int id, TileLds<D>
     if (tid == 0) lds.nan = 0;
     __syncthreads();
     if (tiles > 0) {
-        f32x16_t s0[RB][2], s1[RB][2];
-        float top[RB];
+        f32x16_t s0[2], s1[2];
         const std::integral_constant<int, 0> even;
         const std::integral_constant<int, 1> odd;
         fetch(0, odd);
@@ -389,21 +355,15 @@ __device__ __forceinline__ void attn_tiles(const AttnCall& a, int id, TileLds<D>
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
-            for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) s0[rb][kb][i] = 0.0f;
+            for (int i = 0; i < 16; ++i) s0[kb][i] = 0.0f;
 #pragma unroll
             for (int y = 0; y < KS; ++y) {
                 const bf16x8_t f = k_frag(lds.k[0], kb, y);
-#pragma unroll
-                for (int rb = 0; rb < RB; ++rb)
-                    s0[rb][kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[rb][y], s0[rb][kb], 0, 0, 0);
+                s0[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[y], s0[kb], 0, 0, 0);
             }
         }
         mask(s0, 0);
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) top[rb] = row_top(s0, rb);
-        raise(top);
+        raise(row_top(s0));
         lds_barrier();  // the first tile's K buffer takes the third tile
         for (int t = 0;;) {
             tile(s0, s1, t, even);
@@ -420,40 +380,33 @@ __device__ __forceinline__ void attn_tiles(const AttnCall& a, int id, TileLds<D>
             for (int j = t0; j < t0 + kTile && j < any_hi; ++j) {
                 const int pg = page_of(a, r, j);
                 const uint8_t* p = a.v_codes + ((((int64_t)pg * a.n_kv + head) << a.page_shift) + (j & in_page)) * D;
+                if (j < lo || j >= hi) continue;
 #pragma unroll
-                for (int rb = 0; rb < RB; ++rb) {
-                    if (j < lo[rb] || j >= hi[rb]) continue;
+                for (int db = 0; db < DB; ++db)
 #pragma unroll
-                    for (int db = 0; db < DB; ++db)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if ((p[db * 32 + 8 * (i / 4) + 4 * half + (i & 3)] & 0x7f) == 0x7f)
-                                o[rb][db][i] = __builtin_nanf("");
-                }
+                    for (int i = 0; i < 16; ++i)
+                        if ((p[db * 32 + 8 * (i / 4) + 4 * half + (i & 3)] & 0x7f) == 0x7f)
+                            o[db][i] = __builtin_nanf("");
             }
         }
     }
 
+    const int row = row0 + wave * 32 + col;
+    const float total = sum_halves(l);
+    if (row >= rows) return;
+    const int i = row / G, h = head * G + row % G;
+    const bool none = hi <= lo;
+    const int64_t at = ((int64_t)(s.t0 + i) * a.n_q + h) * a.tile_chunks + chunk;
+    if (keys.chunks > 1 && half == 0) *reinterpret_cast<float2*>(a.tile_ml + 2 * at) = make_float2(m, total);
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-        const int row = row0 + (wave * RB + rb) * 32 + col;
-        const float total = sum_halves(l[rb]);
-        if (row >= rows) continue;
-        const int i = row / G, h = head * G + row % G;
-        const bool none = hi[rb] <= lo[rb];
-        const int64_t at = ((int64_t)(s.t0 + i) * a.n_q + h) * a.tile_chunks + chunk;
-        if (keys.chunks > 1 && half == 0) *reinterpret_cast<float2*>(a.tile_ml + 2 * at) = make_float2(m[rb], total);
+    for (int db = 0; db < DB; ++db)
 #pragma unroll
-        for (int db = 0; db < DB; ++db)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int d = db * 32 + 8 * j + 4 * half;
-                const float4 v =
-                    make_float4(o[rb][db][4 * j], o[rb][db][4 * j + 1], o[rb][db][4 * j + 2], o[rb][db][4 * j + 3]);
-                if (keys.chunks == 1) store_part<true>(a, s.t0 + i, h, d, D, v, total, m[rb], none);
-                else *reinterpret_cast<float4*>(a.tile_o + at * D + d) = v;
-            }
-    }
+        for (int j = 0; j < 4; ++j) {
+            const int d = db * 32 + 8 * j + 4 * half;
+            const float4 v = make_float4(o[db][4 * j], o[db][4 * j + 1], o[db][4 * j + 2], o[db][4 * j + 3]);
+            if (keys.chunks == 1) store_part<true>(a, s.t0 + i, h, d, D, v, total, m, none);
+            else *reinterpret_cast<float4*>(a.tile_o + at * D + d) = v;
+        }
 }
 
 template <int D, int NW>
