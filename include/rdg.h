@@ -473,14 +473,17 @@ int rdg_kv_seg_cap(int t_cap, int n_req, int page_rows);
  *   n_free_out  [1] what is left (may be n_free)
  * Requests are served in order: request r's i-th new page is
  * free_list[*n_free - 1 - (new pages of the requests before it) - i].  One that does not
- * fit -- too few free pages, more than max_blocks pages, tokens past t_cap --
- * gets none, nor does a later one that needs a page: its tokens' slots are -1, its
- * kv_len stays, and status is RDG_ECAPACITY with the first such request as detail.  Negative lengths and page ids
- * outside the cache give RDG_EDATA, with the request: one of a negative q_len keeps its kv_len and gets
- * nothing, a negative kv_len becomes 0.  (Lengths above 2^30 count as negative.)  Where a page id is the fault, the page's
- * tokens have slot -1 and, if it was to be a new page, its table entry is -1; kv_len counts them, so that
- * rdg_kv_trim hands back the request's other pages.  Deterministic; nothing
- * waits for the host, so a step can be captured with the kernels that read it. */
+ * fit gets none: its tokens' slots are -1, its kv_len stays, and status is RDG_ECAPACITY with the
+ * first such request as detail.  Behind too few free pages no later request that needs a
+ * page gets one, behind tokens past t_cap no later request is planned; one of more than
+ * max_blocks pages is left out by itself.  cu_q still holds a refused request's tokens: what
+ * attention gives for them means nothing.  Negative lengths and page ids outside the
+ * cache give RDG_EDATA, with the first request: one of a negative q_len keeps its kv_len
+ * and gets nothing, a negative kv_len becomes 0.  (Lengths above 2^30 count as negative.)
+ * Where a page id is the fault, the page's tokens have slot -1 and, if it was to be a new
+ * page, its table entry is -1; kv_len counts them, so that rdg_kv_trim hands back the
+ * request's other pages.  Deterministic; nothing waits for the host, so a step can be
+ * captured with the kernels that read it. */
 int rdg_kv_plan(const rdg_kv_step* S, const int32_t* kv_len, const int32_t* q_len, const int32_t* free_list,
                 const int32_t* n_free, int32_t* n_free_out, rdg_stream_t stream);
 
@@ -536,7 +539,8 @@ int rdg_qk_norm_rope_store(const void* qkv, int dtype, int64_t qkv_stride, int T
  *   work     rdg_paged_attention_workspace_bytes(...) bytes (NULL when that is 0)
  * Softmax, sums and products are fp32; with RDG_BF16 the probabilities are
  * rounded to bf16 for the product with v.  Deterministic.  A NaN in a row
- * that a query does not see does not reach it. */
+ * that a query does not see does not reach it.  Rows of out and lse past the last
+ * request's tokens are not written. */
 size_t rdg_paged_attention_workspace_bytes(const rdg_kv_cache* C, int T, int n_req, int n_q, int max_q, int max_kv,
                                            int dtype);
 int rdg_paged_attention(const void* q, int dtype, int64_t q_stride, int T, int n_q, const rdg_kv_step* S,

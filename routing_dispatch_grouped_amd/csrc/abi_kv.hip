@@ -114,8 +114,8 @@ AttnPlan plan_attn(int T, int R, int n_kv, int group, int head_dim, bool bf16, i
         // no request is that short if even max_q for all the others leaves more
         if ((int64_t)T - (int64_t)(R - 1) * max_q > p.n_most) p.n_most = 0;
         // Tiles of 256 rows convert each key's codes half as often: two prompts of 7000 tokens,
-        // 32 / 8 heads, 792 us, with 128 rows 829.  Tiles of 128 fill the chip
-        // sooner and waste less on short requests: one prompt of 1000 33, with 256 rows 46;
+        // 32 / 8 heads, 796 us, with 128 rows 831; one of 8000 516 and 555.  Tiles of 128 fill the
+        // chip sooner and waste less on short requests: one prompt of 1000 33, with 256 rows 46;
         // four times 400 tokens on 3000 99 and 139.
         const auto units_of = [&](int bm) { return (double)n_kv * ceil((double)T * group / bm); };
         p.tile_rows = head_dim == 256 || p.n_most > 0 || units_of(256) < kTileUnits ? 128 : 256;

@@ -1,5 +1,5 @@
 // Attention over the 8-bit paged cache, many query rows per request: prefill and
-// prefill chunks in bf16.  The same mathematics as attn.hip's k_attn_rows (one
+// prefill chunks in bf16.  The same mathematics as attn_rows.h (one
 // pass, running maximum and sum in fp32); here the work is matrix products,
 // 4 * head_dim flops per (query row, key), bound by the bf16 matrix rate and by
 // the exponentials beside it.
@@ -24,13 +24,17 @@
 // its first, longest work first.
 //
 // Measured (784 GFLOP: two causal prompts of 6045 and 7691 tokens, 32 / 8 heads of 128):
-// 785 us, 1.0 PFLOP/s, 0.6 of what a large bf16 library product reaches on the
-// card.  The matrix units are busy 49% of the time and the vector units 48% (of a
+// 800 us (785 to 850 with the card's clocks), 1.0 PFLOP/s, 0.6 of what a large bf16
+// library product reaches on the card.  The matrix units are busy 49% of the time and the vector units 48% (of a
 // tile's 200 vector instructions per lane, 32 are exponentials), both at once
 // 18%: what is left is mostly issue and LDS latency at two waves a SIMD.
 // Without the interleaving it took 1174 us; halves of the workgroup in
 // opposite phases with two barriers a step 833, two 128-row workgroups per
 // CU 852.
+// Registers: the eight-wave form of width 128 takes all 256 of a lane, the four-wave one
+// and the mixed launch spill 36 bytes a lane besides.  Width 256 takes 256 and
+// 255 accumulator registers at one wave a SIMD: a prompt of 3400 tokens, 64 / 4 heads, 379
+// GFLOP in 548 us, 0.7 PFLOP/s.
 #include <type_traits>
 
 #include "attn_rows.h"

@@ -329,8 +329,8 @@ hipError_t launch_qk_store(QkStoreCall a, int head_dim, bool bf16, int seg_cap, 
     if (a.T == 0) return hipSuccess;
     const int vpw = kWave * 8 / head_dim, groups = (a.n_q + vpw - 1) / vpw;
     // A wave keeps its token's turn for up to four groups of heads where tokens alone fill
-    // the chip: 64 / 8 heads of 128, 2048 tokens 18.4 us (one group a wave: 21.7), 18
-    // thousand 159 (209); at 1024 and fewer they are level.
+    // the chip: 64 / 8 heads of 128, 2048 tokens 17.7 us (one group a wave: 20.3), 4096 31.9
+    // (40.6), 17614 148 (200); at 1024 and fewer they are level (11.6 and 11.9).
     a.q_passes = a.T >= 1024 && groups > 1 ? (groups < 4 ? groups : 4) : 1;
     a.q_chunks = (groups + a.q_passes - 1) / a.q_passes;
     a.q_items = (int64_t)a.T * a.q_chunks;
