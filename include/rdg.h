@@ -22,6 +22,14 @@
  *                           keys and values into the cache
  *   rdg_paged_attention     attention over the cache, prefill and decode
  *
+ * and what joins the two halves:
+ *
+ *   rdg_add_norm            the residual's addition with the root-mean-square norm, and its
+ *                           output in 8 bits with scales
+ *   rdg_linear              matrix product with bias, activation and residual in its epilogue
+ *   rdg_route_topk          routing by softmax or sigmoid scores, with or without groups, bias
+ *                           and renormalised weights
+ *
  * Page names used in the citations below:
  *   [LEP]  "Large-scale EP: DeepEP, EPLB and two-batch overlap" (SGLang handbook)
  *   [SBO]  "Single Batch Overlap (SBO): Overlaping of Down GEMM with Combine Send"
@@ -69,6 +77,10 @@ enum {
  * scale, the form gfx950's scaled MFMA applies in hardware). */
 enum { RDG_F32 = 0, RDG_BF16 = 1, RDG_FP8_E4M3 = 2, RDG_FP8_E4M3_UE8M0 = 3 };
 enum { RDG_CONTIGUOUS = 0, RDG_MASKED = 1 };            /* layout kinds */
+enum { RDG_SCORE_SIGMOID = 0, RDG_SCORE_SOFTMAX = 1 };  /* routing scores */
+/* activations of rdg_linear: y, max(y, 0), y / (1 + exp(-y)), y Phi(y), and its tanh form
+ * y (1 + tanh(sqrt(2 / pi) (y + 0.044715 y^3))) / 2 */
+enum { RDG_ACT_NONE = 0, RDG_ACT_RELU = 1, RDG_ACT_SILU = 2, RDG_ACT_GELU = 3, RDG_ACT_GELU_TANH = 4 };
 
 /* A dispatch layout ([LEP] DeepEP modes paragraph: the contiguous layout
  * orders tokens by expert for dynamic shapes, the masked layout keeps fixed
@@ -546,6 +558,78 @@ size_t rdg_paged_attention_workspace_bytes(const rdg_kv_cache* C, int T, int n_r
 int rdg_paged_attention(const void* q, int dtype, int64_t q_stride, int T, int n_q, const rdg_kv_step* S,
                         const rdg_kv_cache* C, int max_q, int max_kv, float scale, int causal, int window, void* out,
                         int64_t out_stride, float* lse, void* work, size_t work_bytes, rdg_stream_t stream);
+
+/* ---------------------------------------------------------------- joins of a layer
+ * What a decoder layer computes between its attention and expert halves (not on the
+ * pages).  Strides are in elements; rows start on 16 bytes. */
+
+/* The residual's addition with the root-mean-square norm, and its output in 8 bits, in
+ * one pass:
+ *   s = x + residual,  residual_out = s,  y = s / sqrt(mean(s^2) + eps) * weight,  out = y,
+ *   q, q_scales = e4m3 codes and 1 x 128 block scales of y
+ *   x         [T, x_stride] rows of H elements (RDG_F32 or RDG_BF16)
+ *   residual  [T, res_stride] in res_dtype (RDG_F32 or RDG_BF16), or NULL: s = x
+ *   residual_out  as residual (same type and stride), or NULL; may be residual, or x where
+ *             type and stride are the same
+ *   weight    [H] fp32 or NULL (1)
+ *   out       [T, out_stride] in x's type, or NULL; may be x where the stride is the same
+ *   q         [T, H] e4m3 codes, or NULL; q_scales [T, H/128] fp32, of q_dtype:
+ *             RDG_FP8_E4M3 (amax / 448) or RDG_FP8_E4M3_UE8M0 (the smallest power of two
+ *             not below it), 1 for an all-zero block -- as rdg_quantize_fp8 of y, and what
+ *             rdg_dispatch, rdg_grouped_ffn_gather and rdg_linear read
+ * At least one of out and q.  H is a multiple of 8 (of 128 with q), at most 32768
+ * (RDG_EUNSUPPORTED beyond).  s, the squares and y are fp32 and rounded once each to
+ * residual_out, out and q: the norm takes s, and q takes y, before they are rounded to 16 bits.  Rows
+ * whose squares pass fp32's range, and rows with an infinity, come out as that
+ * arithmetic has them (0, NaN at the infinity); a NaN makes its whole row NaN.  Blocks take
+ * their scale from their finite elements; an infinity is coded as +-448, NaN as 0x7f.  T = 0 is
+ * a no-op. */
+int rdg_add_norm(const void* x, int x_dtype, int64_t x_stride, int T, int H, const void* residual, void* residual_out,
+                 int res_dtype, int64_t res_stride, const float* weight, float eps, void* out, int64_t out_stride,
+                 uint8_t* q, float* q_scales, int q_dtype, rdg_stream_t stream);
+
+/* Matrix product with its epilogue:
+ *   out[t] = act(x[t] W^T + bias) + residual[t]
+ *   x         [T, x_stride] rows of K elements: RDG_F32, RDG_BF16, RDG_FP8_E4M3 or
+ *             RDG_FP8_E4M3_UE8M0 (dtype), with x_scales [T, K/128] fp32 for the last two
+ *   W         [N, K] in dtype, packed by rdg_pack_weights (n_mat = 1), with W_scales
+ *             [ceil(N/128), K/128] for fp8, as rdg_quantize_fp8 with block_rows 128 gives them
+ *   bias      [N] fp32 or NULL
+ *   act       RDG_ACT_*
+ *   residual  [T, res_stride] rows of N elements in out_dtype, or NULL; may be out where
+ *             the stride is the same
+ *   out       [T, out_stride] rows of N elements: RDG_F32 or RDG_BF16 (fp32 operands:
+ *             RDG_F32, else RDG_EUNSUPPORTED)
+ *   work      rdg_linear_workspace_bytes(T, N, K, dtype) bytes (NULL when that is 0); nothing
+ *             in it needs clearing.  Calls that overlap need workspaces of their own
+ * N is a multiple of 16, K of 128.  Products are summed in fp32 (fp8: of every 128,
+ * then scaled by both blocks' scales in fp32), and everything up to the one rounding of out is
+ * fp32.  Deterministic.  out may not be x.  T = 0 is a no-op. */
+size_t rdg_linear_workspace_bytes(int T, int N, int K, int dtype);
+int rdg_linear(const void* x, const float* x_scales, int dtype, int64_t x_stride, int T, int N, int K, const void* W,
+               const float* W_scales, const float* bias, int act, const void* residual, int64_t res_stride, void* out,
+               int out_dtype, int64_t out_stride, void* work, size_t work_bytes, rdg_stream_t stream);
+
+/* Routing to experts by scores, in the forms rdg_route does not have:
+ *   p = softmax(logits) or sigmoid(logits); choice = p + bias; the topk_group groups of the
+ *   largest rank; of their experts the K of the largest choice
+ *   logits    [B, logit_stride] rows of N (RDG_F32 or RDG_BF16)
+ *   score     RDG_SCORE_SOFTMAX (over all N) or RDG_SCORE_SIGMOID (rdg_route's)
+ *   bias      [N] fp32, added for the choice only, or NULL
+ *   n_group   groups of N / n_group consecutive experts (1: no groups), topk_group of them kept
+ *   group_best  a group's rank is its largest choice (1) or the sum of its two largest (2;
+ *             the one where it has one)
+ *   renorm    nonzero: topk_w = p / (sum of the K chosen p) * scale, else p * scale
+ *   topk_ids  [B, K] int32 out, in (choice desc, id asc) order; topk_w [B, K] fp32 out
+ * p is computed in fp64 and rounded once to fp32; the rest is fp32; ties go to the lower index.
+ * A logit of -inf (an expert that is switched off) has softmax score 0, NaN counts as -inf
+ * and +inf as the largest finite value; a NaN choice is the least.  Where the K chosen scores are all 0
+ * (a row of nothing but -inf), the weights are 0.  Sigmoid with group_best = 2 and
+ * renorm gives what rdg_route and rdg_route_biased give.  N <= 1024, K <= 32, K <= topk_group * N /
+ * n_group.  B = 0 is a no-op. */
+int rdg_route_topk(const void* logits, int dtype, int64_t logit_stride, int B, int N, int score, const float* bias,
+                   int n_group, int topk_group, int group_best, int K, int renorm, float scale, int32_t* topk_ids,
+                   float* topk_w, rdg_stream_t stream);
 
 /* Fill n int32 words with value (a kernel, so it is safe inside captured graphs). */
 int rdg_fill_i32(int32_t* p, int32_t value, int64_t n, rdg_stream_t stream);

@@ -14,6 +14,8 @@ LIB_PATH = os.path.join(_HERE, "librdg.so")
 RDG_OK, RDG_EINVAL, RDG_ECAPACITY, RDG_ETIMEOUT, RDG_EHIP, RDG_EUNSUPPORTED, RDG_EDATA = 0, -1, -2, -3, -4, -5, -6
 RDG_F32, RDG_BF16, RDG_FP8_E4M3, RDG_FP8_E4M3_UE8M0 = 0, 1, 2, 3
 RDG_CONTIGUOUS, RDG_MASKED = 0, 1
+RDG_SCORE_SIGMOID, RDG_SCORE_SOFTMAX = 0, 1
+RDG_ACT_NONE, RDG_ACT_RELU, RDG_ACT_SILU, RDG_ACT_GELU, RDG_ACT_GELU_TANH = 0, 1, 2, 3, 4
 
 
 class RdgError(RuntimeError):
@@ -85,6 +87,10 @@ _SIGS = {
     "rdg_qk_norm_rope_store": ([_P, _I, _I64, _I, _I, _I, _I, _P, _P, _F, _P, _I, _I, _I, _SP, _CP, _P, _I64, _P], _I),
     "rdg_paged_attention_workspace_bytes": ([_CP, _I, _I, _I, _I, _I, _I], _SZ),
     "rdg_paged_attention": ([_P, _I, _I64, _I, _I, _SP, _CP, _I, _I, _F, _I, _I, _P, _I64, _P, _P, _SZ, _P], _I),
+    "rdg_add_norm": ([_P, _I, _I64, _I, _I, _P, _P, _I, _I64, _P, _F, _P, _I64, _P, _P, _I, _P], _I),
+    "rdg_linear_workspace_bytes": ([_I, _I, _I, _I], _SZ),
+    "rdg_linear": ([_P, _P, _I, _I64, _I, _I, _I, _P, _P, _P, _I, _P, _I64, _P, _I, _I64, _P, _SZ, _P], _I),
+    "rdg_route_topk": ([_P, _I, _I64, _I, _I, _I, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P], _I),
     "rdg_check_status": ([_P, _P, _P], _I),
     "rdg_strerror": ([_I], ctypes.c_char_p),
     "rdg_version": ([], _I),
@@ -468,6 +474,110 @@ def rdg_paged_attention(q, step, cache, max_q, max_kv, scale, out, lse=None, wor
     _check(_lib.rdg_paged_attention(q.data_ptr(), dt, q_stride, T, n_q, step.ref, cache.ref, max_q, max_kv, scale,
                                     1 if causal else 0, window, out.data_ptr(), out_stride, lse_ptr, work_ptr, work_bytes,
                                     _raw_stream(stream)), "rdg_paged_attention")
+
+
+def _matrix(t, what, T, n):
+    """(address, dtype code, row stride) of [T, n] bfloat16 or float32 rows, which may be apart."""
+    torch = _torch or _bind_torch()
+    dt = t.dtype
+    code = RDG_BF16 if dt is torch.bfloat16 else RDG_F32 if dt is torch.float32 else None
+    if code is None or t.dim() != 2 or t.shape[0] != T or t.shape[1] != n or (n > 1 and t.stride(1) != 1):
+        raise RdgError(RDG_EINVAL, "%s: want bfloat16 or float32 rows [%d, %d], got %s %s with strides %s" %
+                       (what, T, n, dt, list(t.shape), list(t.stride())))
+    return t.data_ptr(), code, t.stride(0) if T > 1 else n
+
+
+def _here(what, *tensors):
+    """Refuses tensors that are not on the current device, whose stream the call goes to."""
+    device = _device_of()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise RdgError(RDG_EINVAL, "%s: a tensor is on %s, the current device is %d" % (what, t.device, device))
+
+
+def rdg_add_norm(x, weight, eps, out=None, residual=None, residual_out=None, q=None, q_scales=None,
+                 q_dtype=RDG_FP8_E4M3, stream=None):
+    """x, out [T, H], residual, residual_out [T, H] of one type (row strides free), weight [H] float32 or None,
+    q [T, H] uint8 and q_scales [T, H/128] float32."""
+    torch = _torch or _bind_torch()
+    if x.dim() != 2:
+        raise RdgError(RDG_EINVAL, "rdg_add_norm: x has to be [T, H]")
+    T, H = x.shape
+    x_ptr, dt, x_stride = _matrix(x, "rdg_add_norm: x", T, H)
+    res_ptr = res_out_ptr = out_ptr = q_ptr = qs_ptr = w_ptr = None
+    res_dt, res_stride, out_stride = dt, 0, 0
+    if residual is not None:
+        res_ptr, res_dt, res_stride = _matrix(residual, "rdg_add_norm: residual", T, H)
+    if residual_out is not None:
+        res_out_ptr, o_dt, o_stride = _matrix(residual_out, "rdg_add_norm: residual_out", T, H)
+        if residual is None or o_dt != res_dt or o_stride != res_stride:
+            raise RdgError(RDG_EINVAL, "rdg_add_norm: residual_out differs from residual in type or stride")
+    if out is not None:
+        out_ptr, o_dt, out_stride = _matrix(out, "rdg_add_norm: out", T, H)
+        if o_dt != dt:
+            raise RdgError(RDG_EINVAL, "rdg_add_norm: out differs from x in type")
+    if weight is not None:
+        w_ptr = _tensor(weight, "rdg_add_norm: weight", torch.float32, H)
+    if q is not None:
+        q_ptr = _tensor(q, "rdg_add_norm: q", torch.uint8, T * H)
+        qs_ptr = _tensor(q_scales, "rdg_add_norm: q_scales", torch.float32, T * (H // 128))
+    _here("rdg_add_norm", x, weight, out, residual, residual_out, q, q_scales)
+    _check(_lib.rdg_add_norm(x_ptr, dt, x_stride, T, H, res_ptr, res_out_ptr, res_dt, res_stride, w_ptr, eps, out_ptr,
+                             out_stride, q_ptr, qs_ptr, q_dtype, _raw_stream(stream)), "rdg_add_norm")
+
+
+def rdg_linear_workspace_bytes(T, N, K, dtype):
+    return int(_lib.rdg_linear_workspace_bytes(T, N, K, dtype))
+
+
+def rdg_linear(x, x_scales, dtype, W, W_scales, out, bias=None, act=RDG_ACT_NONE, residual=None, work=None, stream=None):
+    """x [T, K] (row stride free; fp8 codes as uint8 or float8_e4m3fn) with x_scales [T, K/128] float32, W [N, K] packed
+    with W_scales [ceil(N/128), K/128], out, residual [T, N] bfloat16 or float32 (row strides free), bias [N] float32;
+    work: a uint8 tensor of rdg_linear_workspace_bytes."""
+    torch = _torch or _bind_torch()
+    if x.dim() != 2 or out.dim() != 2:
+        raise RdgError(RDG_EINVAL, "rdg_linear: x has to be [T, K] and out [T, N]")
+    T, K = x.shape
+    N = out.shape[1]
+    kinds = {RDG_F32: (torch.float32,), RDG_BF16: (torch.bfloat16,)}.get(dtype, (torch.uint8, torch.float8_e4m3fn))
+    if x.dtype not in kinds or x.stride(1) != 1:
+        raise RdgError(RDG_EINVAL, "rdg_linear: want x rows of %s, got %s with strides %s" % (kinds, x.dtype, list(x.stride())))
+    if W.dtype not in kinds or W.numel() != N * K or not W.is_contiguous():
+        raise RdgError(RDG_EINVAL, "rdg_linear: want W of %s, %d x %d packed, got %s %s" % (kinds, N, K, W.dtype, list(W.shape)))
+    out_ptr, out_dt, out_stride = _matrix(out, "rdg_linear: out", T, N)
+    xs_ptr = ws_ptr = bias_ptr = res_ptr = None
+    res_stride = 0
+    if len(kinds) > 1:
+        xs_ptr = _tensor(x_scales, "rdg_linear: x_scales", torch.float32, T * (K // 128))
+        ws_ptr = _tensor(W_scales, "rdg_linear: W_scales", torch.float32, (N + 127) // 128 * (K // 128))
+    if bias is not None:
+        bias_ptr = _tensor(bias, "rdg_linear: bias", torch.float32, N)
+    if residual is not None:
+        res_ptr, res_dt, res_stride = _matrix(residual, "rdg_linear: residual", T, N)
+        if res_dt != out_dt:
+            raise RdgError(RDG_EINVAL, "rdg_linear: residual differs from out in type")
+    work_ptr, work_bytes = (None, 0) if work is None else (work.data_ptr(), work.nbytes)
+    _here("rdg_linear", x, x_scales, W, W_scales, out, bias, residual, work)
+    _check(_lib.rdg_linear(x.data_ptr(), xs_ptr, dtype, x.stride(0) if T > 1 else K, T, N, K, W.data_ptr(), ws_ptr,
+                           bias_ptr, act, res_ptr, res_stride, out_ptr, out_dt, out_stride, work_ptr, work_bytes,
+                           _raw_stream(stream)), "rdg_linear")
+
+
+def rdg_route_topk(logits, score, n_group, topk_group, group_best, K, renorm, scale, topk_ids, topk_w, bias=None,
+                   stream=None):
+    """logits [B, N] bfloat16 or float32 (row stride free), topk_ids [B, K] int32, topk_w [B, K] float32, bias [N] float32
+    or None."""
+    torch = _torch or _bind_torch()
+    if logits.dim() != 2:
+        raise RdgError(RDG_EINVAL, "rdg_route_topk: logits has to be [B, N]")
+    B, N = logits.shape
+    l_ptr, dt, stride = _matrix(logits, "rdg_route_topk: logits", B, N)
+    b_ptr = None if bias is None else _tensor(bias, "rdg_route_topk: bias", torch.float32, N)
+    _here("rdg_route_topk", logits, topk_ids, topk_w, bias)
+    _check(_lib.rdg_route_topk(l_ptr, dt, stride, B, N, score, b_ptr, n_group, topk_group, group_best, K,
+                               1 if renorm else 0, scale, _tensor(topk_ids, "rdg_route_topk: topk_ids", torch.int32, B * K),
+                               _tensor(topk_w, "rdg_route_topk: topk_w", torch.float32, B * K), _raw_stream(stream)),
+           "rdg_route_topk")
 
 
 def rdg_check_status(layout_or_status, stream=None):

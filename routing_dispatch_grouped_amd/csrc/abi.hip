@@ -73,7 +73,7 @@ uint64_t wall_ticks_per_us() {
 
 extern "C" {
 
-int rdg_version(void) { return 200; }
+int rdg_version(void) { return 300; }
 
 const char* rdg_strerror(int code) {
     switch (code) {

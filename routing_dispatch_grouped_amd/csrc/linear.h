@@ -1,0 +1,103 @@
+// Matrix product with bias, activation and residual in its epilogue: operands
+// of the matrix instructions and the epilogue, shared by its kernels.
+#pragma once
+#include "rdg_internal.h"
+
+namespace rdg {
+
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+
+// Per type: the reduction elements KS of a matrix instruction, the bytes BLK of a packed
+// 16-row weight tile (pack.hip) and the instruction.
+template <int DT>
+struct LinOp;
+
+template <>
+struct LinOp<RDG_F32> {
+    using op_t = float;
+    static constexpr int KS = 4, ESZ = 4, BLK = 256;
+    __device__ static op_t load_w(const uint8_t* tile, int lane) { return reinterpret_cast<const float*>(tile)[lane]; }
+    __device__ static op_t stream_w(const uint8_t* tile, int lane) {
+        return __builtin_nontemporal_load(reinterpret_cast<const float*>(tile) + lane);
+    }
+    __device__ static op_t load_x(const uint8_t* row, int k, int lane) {
+        return reinterpret_cast<const float*>(row)[k + (lane >> 4)];
+    }
+    __device__ static f32x4_t mma(f32x4_t c, op_t a, op_t b) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
+};
+
+template <>
+struct LinOp<RDG_BF16> {
+    using op_t = bf16x8_t;
+    static constexpr int KS = 32, ESZ = 2, BLK = 1024;
+    __device__ static op_t load_w(const uint8_t* tile, int lane) {
+        return *reinterpret_cast<const bf16x8_t*>(tile + lane * 16);
+    }
+    __device__ static op_t stream_w(const uint8_t* tile, int lane) {
+        return __builtin_nontemporal_load(reinterpret_cast<const bf16x8_t*>(tile + lane * 16));
+    }
+    __device__ static op_t load_x(const uint8_t* row, int k, int lane) {
+        return *reinterpret_cast<const bf16x8_t*>(row + (int64_t)(k + (lane >> 4) * 8) * 2);
+    }
+    __device__ static f32x4_t mma(f32x4_t c, op_t a, op_t b) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+};
+
+template <>
+struct LinOp<RDG_FP8_E4M3> {
+    using op_t = i32x8_t;
+    static constexpr int KS = 128, ESZ = 1, BLK = 2048;  // a step is one block of 128 with its scales
+    __device__ static op_t join(i32x4_t a, i32x4_t b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
+    __device__ static op_t load_w(const uint8_t* tile, int lane) {
+        return join(*reinterpret_cast<const i32x4_t*>(tile + lane * 16), *reinterpret_cast<const i32x4_t*>(tile + 1024 + lane * 16));
+    }
+    __device__ static op_t stream_w(const uint8_t* tile, int lane) {
+        return join(__builtin_nontemporal_load(reinterpret_cast<const i32x4_t*>(tile + lane * 16)),
+                    __builtin_nontemporal_load(reinterpret_cast<const i32x4_t*>(tile + 1024 + lane * 16)));
+    }
+    __device__ static op_t load_x(const uint8_t* row, int k, int lane) {
+        const i32x4_t* p = reinterpret_cast<const i32x4_t*>(row + k + (lane >> 4) * 32);
+        return join(p[0], p[1]);
+    }
+    __device__ static f32x4_t mma(f32x4_t c, op_t a, op_t b) {
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);
+    }
+};
+
+// The activations, in fp32.  gelu is y Phi(y); its tanh form y (1 + tanh(u)) / 2 is
+// y / (1 + exp(-2 u)) with u = sqrt(2 / pi) (y + 0.044715 y^3).
+__device__ __forceinline__ float activate(float y, int act) {
+    switch (act) {
+        case RDG_ACT_RELU: return y < 0.0f ? 0.0f : y;
+        case RDG_ACT_SILU: return y / (1.0f + expf(-y));
+        case RDG_ACT_GELU: return 0.5f * y * erfcf(y * -0.70710678118654752f);
+        case RDG_ACT_GELU_TANH: return y / (1.0f + expf(-1.5957691216057308f * (y + 0.044715f * y * y * y)));
+        default: return y;
+    }
+}
+
+// Features f..f+3 of token t: bias, activation, residual, one rounding to out's type.
+__device__ __forceinline__ void finish4(const LinearCall& a, f32x4_t v, int64_t t, int f) {
+    if (a.bias != nullptr) v += *reinterpret_cast<const f32x4_t*>(a.bias + f);
+    if (a.act != RDG_ACT_NONE) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = activate(v[r], a.act);
+    }
+    if (a.out_bf16) {
+        if (a.residual != nullptr) {
+            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.residual) + t * a.res_stride + f);
+            v[0] += __uint_as_float(u.x << 16), v[1] += __uint_as_float(u.x & 0xffff0000u);
+            v[2] += __uint_as_float(u.y << 16), v[3] += __uint_as_float(u.y & 0xffff0000u);
+        }
+        typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
+        *reinterpret_cast<bf16x4_t*>(static_cast<uint16_t*>(a.out) + t * a.out_stride + f) =
+            __builtin_convertvector(v, bf16x4_t);
+    } else {
+        if (a.residual != nullptr)
+            v += *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(a.residual) + t * a.res_stride + f);
+        *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + t * a.out_stride + f) = v;
+    }
+}
+
+}  // namespace rdg

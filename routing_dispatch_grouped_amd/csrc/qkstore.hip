@@ -25,45 +25,13 @@
 // Measured: 17614 tokens of 64 / 8 heads of 128, bf16: 148 us, 4.7 TB/s, what a large copy
 // reaches on the card.  64 tokens of 32 / 8 heads into begun pages: 6.3 us of
 // latency (segment, slots, rows and scale are read one after the other).
-#include "rdg_internal.h"
+#include "vec8.h"
 
 namespace rdg {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr float kE4m3Max = 448.0f;
-
-template <bool BF16>
-__device__ __forceinline__ void load8(const void* p, int64_t i, float (&x)[8]) {
-    if constexpr (BF16) {
-        const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[2 * j] = __uint_as_float(w[j] << 16);
-            x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-        }
-    } else {
-        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-        const float4 a = f[0], b = f[1];
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    }
-}
-
-template <bool BF16>
-__device__ __forceinline__ void store8(void* p, int64_t i, const float (&x)[8]) {
-    if constexpr (BF16) {
-        bf16x8_t b;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) b[j] = (__bf16)x[j];
-        *reinterpret_cast<bf16x8_t*>(static_cast<uint16_t*>(p) + i) = b;
-    } else {
-        float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-        f[0] = make_float4(x[0], x[1], x[2], x[3]);
-        f[1] = make_float4(x[4], x[5], x[6], x[7]);
-    }
-}
 
 // cos and sin of this lane's 8 elements (elements past rot_dim: not used).
 struct Turn {

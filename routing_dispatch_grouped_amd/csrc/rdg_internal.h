@@ -279,4 +279,44 @@ hipError_t launch_attn_rows(const AttnCall& a, int head_dim, bool bf16, hipStrea
 hipError_t launch_attn_tiles(const AttnCall& a, int head_dim, hipStream_t s);
 hipError_t launch_attn_join(const AttnCall& a, int head_dim, bool bf16, hipStream_t s);
 
+// The joins of a decoder layer.
+constexpr int kNormMax = 32768;  // elements of a row: a workgroup's 1024 threads hold 32 each
+struct AddNormCall {
+    const void *x, *residual;
+    void *residual_out, *out;
+    const float* weight;
+    uint8_t* q;
+    float* q_scales;
+    int64_t x_stride, res_stride, out_stride;  // elements
+    float eps;
+    int T, H;
+    bool x_bf16, res_bf16, pow2;
+};
+hipError_t launch_add_norm(const AddNormCall& a, hipStream_t s);
+
+struct LinearCall {
+    const void *x, *w;
+    const float *x_scales, *w_scales, *bias;
+    const void* residual;
+    void* out;
+    float* parts;                              // the caller's workspace
+    int64_t x_stride, res_stride, out_stride;  // elements
+    int T, N, K, dtype, act;
+    bool out_bf16;
+};
+size_t linear_workspace_bytes(int T, int N, int K, int dtype);
+hipError_t launch_linear(const LinearCall& a, hipStream_t s);
+
+struct RouteCall {
+    const void* logits;
+    const float* bias;
+    int32_t* ids;
+    float* w;
+    int64_t stride;  // elements
+    float scale;
+    int B, N, n_group, topk_group, group_best, K;
+    bool softmax, bf16, renorm;
+};
+hipError_t launch_route_topk(const RouteCall& a, hipStream_t s);
+
 }  // namespace rdg
