@@ -13,7 +13,7 @@ BUILD = os.path.join(PKG, "_build")
 
 SOURCES = ["abi.hip", "route.hip", "dispatch.hip", "quant.hip", "pack.hip", "ffn.hip", "ffn_tiled.hip", "combine.hip",
            "kvplan.hip", "qkstore.hip", "attn.hip", "attn_tiles.hip",
-           "abi_kv.hip", "addnorm.hip", "linear.hip", "route_topk.hip", "abi_layer.hip", "eplb.cpp", "tbo.cpp"]
+           "abi_kv.hip", "addnorm.hip", "linear.hip", "linear_tiled.hip", "abi_layer.hip", "eplb.cpp", "tbo.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
