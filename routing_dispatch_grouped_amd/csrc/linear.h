@@ -1,7 +1,7 @@
 // Matrix product with bias, activation and residual in its epilogue: operands
 // of the matrix instructions and the epilogue, shared by its kernels.
 #pragma once
-#include "rdg_internal.h"
+#include "vec8.h"
 
 namespace rdg {
 
@@ -98,6 +98,25 @@ __device__ __forceinline__ void finish4(const LinearCall& a, f32x4_t v, int64_t 
             v += *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(a.residual) + t * a.res_stride + f);
         *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + t * a.out_stride + f) = v;
     }
+}
+
+// Features f..f+7 of token t, their bias given: as finish4.
+__device__ __forceinline__ void finish8(const LinearCall& a, float (&v)[8], const float (&bias)[8], int64_t t, int f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += bias[e];
+    if (a.act != RDG_ACT_NONE) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = activate(v[e], a.act);
+    }
+    if (a.residual != nullptr) {
+        float r[8];
+        if (a.out_bf16) load8<true>(a.residual, t * a.res_stride + f, r);
+        else load8<false>(a.residual, t * a.res_stride + f, r);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += r[e];
+    }
+    if (a.out_bf16) store8<true>(a.out, t * a.out_stride + f, v);
+    else store8<false>(a.out, t * a.out_stride + f, v);
 }
 
 }  // namespace rdg

@@ -120,7 +120,7 @@ hipError_t launch_dt(const LinearCall& a, hipStream_t s) {
 
 hipError_t launch_linear(const LinearCall& a, hipStream_t s) {
     if (a.T == 0) return hipSuccess;
-    if (a.dtype == RDG_BF16 && a.T > 256) return launch_linear_tiled(a, s);
+    if (a.dtype != RDG_F32 && a.T > 256) return launch_linear_tiled(a, s);
     switch (a.dtype) {
         case RDG_F32: return launch_dt<RDG_F32>(a, s);
         case RDG_BF16: return launch_dt<RDG_BF16>(a, s);
