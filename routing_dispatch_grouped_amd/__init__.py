@@ -123,12 +123,17 @@ def _check(rc, what):
 # torch and its current-stream lookup, bound at the first call: the small calls
 # of a decode step take as long on the host as on the GPU.
 _torch = _stream_of = _device_of = None
+_float_codes, _linear_types = {}, {}  # element types by torch's, and torch's of an rdg_linear operand
 
 
 def _bind_torch():
     global _torch, _stream_of, _device_of
     import torch
     _stream_of, _device_of = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _float_codes.update({torch.bfloat16: RDG_BF16, torch.float32: RDG_F32})
+    codes = (torch.uint8, torch.float8_e4m3fn)
+    _linear_types.update({RDG_F32: (torch.float32,), RDG_BF16: (torch.bfloat16,), RDG_FP8_E4M3: codes,
+                          RDG_FP8_E4M3_UE8M0: codes})
     _torch = torch
     return torch
 
@@ -476,23 +481,36 @@ def rdg_paged_attention(q, step, cache, max_q, max_kv, scale, out, lse=None, wor
                                     _raw_stream(stream)), "rdg_paged_attention")
 
 
-def _matrix(t, what, T, n):
-    """(address, dtype code, row stride) of [T, n] bfloat16 or float32 rows, which may be apart."""
-    torch = _torch or _bind_torch()
-    dt = t.dtype
-    code = RDG_BF16 if dt is torch.bfloat16 else RDG_F32 if dt is torch.float32 else None
-    if code is None or t.dim() != 2 or t.shape[0] != T or t.shape[1] != n or (n > 1 and t.stride(1) != 1):
-        raise RdgError(RDG_EINVAL, "%s: want bfloat16 or float32 rows [%d, %d], got %s %s with strides %s" %
-                       (what, T, n, dt, list(t.shape), list(t.stride())))
-    return t.data_ptr(), code, t.stride(0) if T > 1 else n
+def _refuse(call, what, t, want):
+    raise RdgError(RDG_EINVAL, "%s: %s: want %s, got %s %s with strides %s on %s" %
+                   (call, what, want, t.dtype, list(t.shape), list(t.stride()), t.device))
 
 
-def _here(what, *tensors):
-    """Refuses tensors that are not on the current device, whose stream the call goes to."""
-    device = _device_of()
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise RdgError(RDG_EINVAL, "%s: a tensor is on %s, the current device is %d" % (what, t.device, device))
+def _matrix(call, what, t, shape, device):
+    """(address, dtype code, row stride) of bfloat16 or float32 rows of this shape, which may be apart, on this device."""
+    code = _float_codes.get(t.dtype)
+    if code is None or t.shape != shape:
+        _refuse(call, what, t, "bfloat16 or float32 rows %s" % list(shape))
+    if t.is_contiguous():
+        stride = shape[1]
+    else:
+        stride, inner = t.stride()
+        if inner != 1 and shape[1] > 1:
+            _refuse(call, what, t, "rows without gaps in them")
+        if shape[0] == 1:
+            stride = shape[1]
+    if t.get_device() != device:
+        _refuse(call, what, t, "the current device, %d" % device)
+    return t.data_ptr(), code, stride
+
+
+def _flat(call, what, t, dtype, n, device):
+    """The address of a contiguous tensor of n elements on this device."""
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        _refuse(call, what, t, "%d contiguous elements of %s" % (n, dtype))
+    if t.get_device() != device:
+        _refuse(call, what, t, "the current device, %d" % device)
+    return t.data_ptr()
 
 
 def rdg_add_norm(x, weight, eps, out=None, residual=None, residual_out=None, q=None, q_scales=None,
@@ -500,30 +518,32 @@ def rdg_add_norm(x, weight, eps, out=None, residual=None, residual_out=None, q=N
     """x, out [T, H], residual, residual_out [T, H] of one type (row strides free), weight [H] float32 or None,
     q [T, H] uint8 and q_scales [T, H/128] float32."""
     torch = _torch or _bind_torch()
-    if x.dim() != 2:
-        raise RdgError(RDG_EINVAL, "rdg_add_norm: x has to be [T, H]")
-    T, H = x.shape
-    x_ptr, dt, x_stride = _matrix(x, "rdg_add_norm: x", T, H)
+    call, shape, device = "rdg_add_norm", x.shape, _device_of()
+    if len(shape) != 2:
+        _refuse(call, "x", x, "[T, H]")
+    T, H = shape
+    x_ptr, dt, x_stride = _matrix(call, "x", x, shape, device)
     res_ptr = res_out_ptr = out_ptr = q_ptr = qs_ptr = w_ptr = None
     res_dt, res_stride, out_stride = dt, 0, 0
     if residual is not None:
-        res_ptr, res_dt, res_stride = _matrix(residual, "rdg_add_norm: residual", T, H)
+        res_ptr, res_dt, res_stride = _matrix(call, "residual", residual, shape, device)
     if residual_out is not None:
-        res_out_ptr, o_dt, o_stride = _matrix(residual_out, "rdg_add_norm: residual_out", T, H)
+        res_out_ptr, o_dt, o_stride = _matrix(call, "residual_out", residual_out, shape, device)
         if residual is None or o_dt != res_dt or o_stride != res_stride:
-            raise RdgError(RDG_EINVAL, "rdg_add_norm: residual_out differs from residual in type or stride")
+            _refuse(call, "residual_out", residual_out, "the type and strides of residual")
     if out is not None:
-        out_ptr, o_dt, out_stride = _matrix(out, "rdg_add_norm: out", T, H)
+        out_ptr, o_dt, out_stride = _matrix(call, "out", out, shape, device)
         if o_dt != dt:
-            raise RdgError(RDG_EINVAL, "rdg_add_norm: out differs from x in type")
+            _refuse(call, "out", out, "the type of x")
     if weight is not None:
-        w_ptr = _tensor(weight, "rdg_add_norm: weight", torch.float32, H)
+        w_ptr = _flat(call, "weight", weight, torch.float32, H, device)
     if q is not None:
-        q_ptr = _tensor(q, "rdg_add_norm: q", torch.uint8, T * H)
-        qs_ptr = _tensor(q_scales, "rdg_add_norm: q_scales", torch.float32, T * (H // 128))
-    _here("rdg_add_norm", x, weight, out, residual, residual_out, q, q_scales)
-    _check(_lib.rdg_add_norm(x_ptr, dt, x_stride, T, H, res_ptr, res_out_ptr, res_dt, res_stride, w_ptr, eps, out_ptr,
-                             out_stride, q_ptr, qs_ptr, q_dtype, _raw_stream(stream)), "rdg_add_norm")
+        q_ptr = _flat(call, "q", q, torch.uint8, T * H, device)
+        qs_ptr = _flat(call, "q_scales", q_scales, torch.float32, T * (H // 128), device)
+    rc = _lib.rdg_add_norm(x_ptr, dt, x_stride, T, H, res_ptr, res_out_ptr, res_dt, res_stride, w_ptr, eps, out_ptr,
+                           out_stride, q_ptr, qs_ptr, q_dtype, _stream_of(device) if stream is None else stream.cuda_stream)
+    if rc:
+        raise RdgError(rc, call)
 
 
 def rdg_linear_workspace_bytes(T, N, K, dtype):
@@ -535,32 +555,45 @@ def rdg_linear(x, x_scales, dtype, W, W_scales, out, bias=None, act=RDG_ACT_NONE
     with W_scales [ceil(N/128), K/128], out, residual [T, N] bfloat16 or float32 (row strides free), bias [N] float32;
     work: a uint8 tensor of rdg_linear_workspace_bytes."""
     torch = _torch or _bind_torch()
-    if x.dim() != 2 or out.dim() != 2:
-        raise RdgError(RDG_EINVAL, "rdg_linear: x has to be [T, K] and out [T, N]")
-    T, K = x.shape
-    N = out.shape[1]
-    kinds = {RDG_F32: (torch.float32,), RDG_BF16: (torch.bfloat16,)}.get(dtype, (torch.uint8, torch.float8_e4m3fn))
-    if x.dtype not in kinds or x.stride(1) != 1:
-        raise RdgError(RDG_EINVAL, "rdg_linear: want x rows of %s, got %s with strides %s" % (kinds, x.dtype, list(x.stride())))
-    if W.dtype not in kinds or W.numel() != N * K or not W.is_contiguous():
-        raise RdgError(RDG_EINVAL, "rdg_linear: want W of %s, %d x %d packed, got %s %s" % (kinds, N, K, W.dtype, list(W.shape)))
-    out_ptr, out_dt, out_stride = _matrix(out, "rdg_linear: out", T, N)
-    xs_ptr = ws_ptr = bias_ptr = res_ptr = None
-    res_stride = 0
+    call, device, shape, out_shape = "rdg_linear", _device_of(), x.shape, out.shape
+    if len(shape) != 2 or len(out_shape) != 2 or out_shape[0] != shape[0]:
+        _refuse(call, "x", x, "[T, K], with out [T, N]")
+    T, K = shape
+    N = out_shape[1]
+    kinds = _linear_types.get(dtype, ())
+    if x.dtype not in kinds or W.dtype not in kinds or W.numel() != N * K or not W.is_contiguous():
+        _refuse(call, "W", W, "x and W of one of %s, W %d x %d packed" % (list(kinds), N, K))
+    if x.is_contiguous():
+        x_stride = K
+    else:
+        x_stride, inner = x.stride()
+        if inner != 1:
+            _refuse(call, "x", x, "rows without gaps in them")
+        if T == 1:
+            x_stride = K
+    if x.get_device() != device or W.get_device() != device:
+        _refuse(call, "x and W", x, "the current device, %d" % device)
+    out_ptr, out_dt, out_stride = _matrix(call, "out", out, out_shape, device)
+    xs_ptr = ws_ptr = bias_ptr = res_ptr = work_ptr = None
+    res_stride = work_bytes = 0
     if len(kinds) > 1:
-        xs_ptr = _tensor(x_scales, "rdg_linear: x_scales", torch.float32, T * (K // 128))
-        ws_ptr = _tensor(W_scales, "rdg_linear: W_scales", torch.float32, (N + 127) // 128 * (K // 128))
+        xs_ptr = _flat(call, "x_scales", x_scales, torch.float32, T * (K // 128), device)
+        ws_ptr = _flat(call, "W_scales", W_scales, torch.float32, (N + 127) // 128 * (K // 128), device)
     if bias is not None:
-        bias_ptr = _tensor(bias, "rdg_linear: bias", torch.float32, N)
+        bias_ptr = _flat(call, "bias", bias, torch.float32, N, device)
     if residual is not None:
-        res_ptr, res_dt, res_stride = _matrix(residual, "rdg_linear: residual", T, N)
+        res_ptr, res_dt, res_stride = _matrix(call, "residual", residual, out_shape, device)
         if res_dt != out_dt:
-            raise RdgError(RDG_EINVAL, "rdg_linear: residual differs from out in type")
-    work_ptr, work_bytes = (None, 0) if work is None else (work.data_ptr(), work.nbytes)
-    _here("rdg_linear", x, x_scales, W, W_scales, out, bias, residual, work)
-    _check(_lib.rdg_linear(x.data_ptr(), xs_ptr, dtype, x.stride(0) if T > 1 else K, T, N, K, W.data_ptr(), ws_ptr,
-                           bias_ptr, act, res_ptr, res_stride, out_ptr, out_dt, out_stride, work_ptr, work_bytes,
-                           _raw_stream(stream)), "rdg_linear")
+            _refuse(call, "residual", residual, "the type of out")
+    if work is not None:
+        work_bytes = work.nbytes
+        if work_bytes:
+            work_ptr = _flat(call, "work", work, torch.uint8, work_bytes, device)
+    rc = _lib.rdg_linear(x.data_ptr(), xs_ptr, dtype, x_stride, T, N, K, W.data_ptr(), ws_ptr, bias_ptr, act, res_ptr,
+                         res_stride, out_ptr, out_dt, out_stride, work_ptr, work_bytes,
+                         _stream_of(device) if stream is None else stream.cuda_stream)
+    if rc:
+        raise RdgError(rc, call)
 
 
 def rdg_route_topk(logits, score, n_group, topk_group, group_best, K, renorm, scale, topk_ids, topk_w, bias=None,
@@ -568,16 +601,18 @@ def rdg_route_topk(logits, score, n_group, topk_group, group_best, K, renorm, sc
     """logits [B, N] bfloat16 or float32 (row stride free), topk_ids [B, K] int32, topk_w [B, K] float32, bias [N] float32
     or None."""
     torch = _torch or _bind_torch()
-    if logits.dim() != 2:
-        raise RdgError(RDG_EINVAL, "rdg_route_topk: logits has to be [B, N]")
-    B, N = logits.shape
-    l_ptr, dt, stride = _matrix(logits, "rdg_route_topk: logits", B, N)
-    b_ptr = None if bias is None else _tensor(bias, "rdg_route_topk: bias", torch.float32, N)
-    _here("rdg_route_topk", logits, topk_ids, topk_w, bias)
-    _check(_lib.rdg_route_topk(l_ptr, dt, stride, B, N, score, b_ptr, n_group, topk_group, group_best, K,
-                               1 if renorm else 0, scale, _tensor(topk_ids, "rdg_route_topk: topk_ids", torch.int32, B * K),
-                               _tensor(topk_w, "rdg_route_topk: topk_w", torch.float32, B * K), _raw_stream(stream)),
-           "rdg_route_topk")
+    call, device, shape = "rdg_route_topk", _device_of(), logits.shape
+    if len(shape) != 2:
+        _refuse(call, "logits", logits, "[B, N]")
+    B, N = shape
+    l_ptr, dt, stride = _matrix(call, "logits", logits, shape, device)
+    b_ptr = None if bias is None else _flat(call, "bias", bias, torch.float32, N, device)
+    rc = _lib.rdg_route_topk(l_ptr, dt, stride, B, N, score, b_ptr, n_group, topk_group, group_best, K, 1 if renorm else 0,
+                             scale, _flat(call, "topk_ids", topk_ids, torch.int32, B * K, device),
+                             _flat(call, "topk_w", topk_w, torch.float32, B * K, device),
+                             _stream_of(device) if stream is None else stream.cuda_stream)
+    if rc:
+        raise RdgError(rc, call)
 
 
 def rdg_check_status(layout_or_status, stream=None):

@@ -63,6 +63,32 @@ struct LinOp<RDG_FP8_E4M3> {
     __device__ static f32x4_t mma(f32x4_t c, op_t a, op_t b) {
         return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);
     }
+    // elements 8 c .. 8 c + 7 of the lane's 32, as they are in bf16
+    __device__ static bf16x8_t widen(op_t a, int c) {
+        typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+        bf16x8_t r;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const bf16x2_t lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)a[2 * c + h], 1.0f, false);
+            const bf16x2_t hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)a[2 * c + h], 1.0f, true);
+            r[4 * h] = lo[0], r[4 * h + 1] = lo[1], r[4 * h + 2] = hi[0], r[4 * h + 3] = hi[1];
+        }
+        return r;
+    }
+    __device__ static f32x4_t mma_wide(f32x4_t c, op_t a, op_t b) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(a, i), widen(b, i), c, 0, 0, 0);
+        return c;
+    }
+};
+
+// How a call is shared out (linear_plan in linear.hip): a kernel for some features, and one for the rest.
+enum { kRows, kTile256, kTile128, kTile128x64, kTile64x32 };  // k_linear_rows, or the tile of k_linear_tiled
+struct LinearPart {
+    int kernel, splits, features;  // splits of the reduction are joined by k_linear_join (tiles only)
+};
+struct LinearPlan {
+    LinearPart first, rest;
 };
 
 // The activations, in fp32.  gelu is y Phi(y); its tanh form y (1 + tanh(u)) / 2 is
@@ -100,10 +126,14 @@ __device__ __forceinline__ void finish4(const LinearCall& a, f32x4_t v, int64_t 
     }
 }
 
-// Features f..f+7 of token t, their bias given: as finish4.
-__device__ __forceinline__ void finish8(const LinearCall& a, float (&v)[8], const float (&bias)[8], int64_t t, int f) {
+// Features f..f+7 of token t: as finish4.
+__device__ __forceinline__ void finish8(const LinearCall& a, float (&v)[8], int64_t t, int f) {
+    if (a.bias != nullptr) {
+        float bias[8];
+        load8<false>(a.bias, f, bias);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += bias[e];
+        for (int e = 0; e < 8; ++e) v[e] += bias[e];
+    }
     if (a.act != RDG_ACT_NONE) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = activate(v[e], a.act);

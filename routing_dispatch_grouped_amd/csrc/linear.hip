@@ -5,129 +5,219 @@
 // products summed in fp32; fp8 partial sums of 128 are scaled by their
 // activation and weight block scales in fp32; one rounding at the end.
 //
-// Design: a workgroup has 16 * FPW weight rows and 16 * NR tokens; its four
-// waves take the reduction's 128-element blocks in turn (wave w blocks w, w + 4, ...), so
-// that the weights stream through in order, and add their sums in LDS in wave order.
+// Here: which kernel runs, and the kernel for few tokens, bound by reading the weights.
+// (linear_tiled.hip: for more tokens.)
+#include <type_traits>
+
 #include "linear.h"
 
 namespace rdg {
 namespace {
 
-template <int DT, int FPW, int NR>
-__global__ __launch_bounds__(256) void k_linear_rows(LinearCall a) {
+// A workgroup has 16 weight rows and 16 tokens; its waves take the reduction's 128-element blocks
+// in turn (wave w blocks w, w + NW, ...), so that the weights stream through in order, and add their sums in LDS in wave
+// order.  16 waves: one token, 7168 x 10240 in bf16 24.6 us (6.0 TB/s), with 4 or 8 waves 25.4, with two weight tiles a
+// wave 28; 16 tokens on 256 features of K = 4096: 7.9 us against 10.9.  Loading the next block during the
+// products, 24.1 us at 16 waves for twice the registers, gained nothing elsewhere.
+// A token tile's loads touch 16 rows, so their time grows with the tokens: rows_us below.
+// WIDE (fp8): products of bf16 operands.
+constexpr int NW = 16;
+
+template <int DT, bool WIDE>
+__global__ __launch_bounds__(NW * 64) void k_linear_rows(LinearCall a) {
     using O = LinOp<DT>;
     using op_t = typename O::op_t;
-    constexpr int STEPS = 128 / O::KS;              // matrix steps of a 128-element block
-    constexpr int U = STEPS > 4 ? 4 : STEPS;        // in flight
-    __shared__ f32x4_t part[4][FPW * NR][kWave];
-    const int wv = threadIdx.x / kWave, lane = lane_id();
-    const int groups = a.N / 16, panels = (groups + FPW - 1) / FPW;
-    const int panel = (int)(blockIdx.x % panels);
-    const int64_t t0 = (int64_t)(blockIdx.x / panels) * (16 * NR);
+    constexpr int STEPS = 128 / O::KS, U = STEPS > 4 ? 8 : STEPS;  // matrix steps of a block, and those in flight
+    constexpr bool FP8 = DT == RDG_FP8_E4M3;
+    __shared__ f32x4_t part[NW][kWave];
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
     const int nkb = a.K / 128;
-    // rows past the last: the last one again, not stored
-    const uint8_t* w[FPW];
+    // XCD b % 8 takes a contiguous share; the token tiles of 16 weight rows lie together in it
+    const int t_tiles = (int)(((int64_t)a.T + 15) / 16);
+    const int n = gridDim.x, xcd = blockIdx.x % 8, q8 = n / 8, r8 = n % 8;
+    const int item = xcd * q8 + (xcd < r8 ? xcd : r8) + blockIdx.x / 8;
+    const int group = item / t_tiles;
+    const int64_t t0 = (int64_t)(item % t_tiles) * 16;
+    const uint8_t* w = static_cast<const uint8_t*>(a.w) + (int64_t)group * (a.K / O::KS) * O::BLK;
+    // tokens past the last: the last one again, not stored
+    const int64_t mine = t0 + (lane & 15), t = mine < a.T ? mine : a.T - 1;
+    const uint8_t* x = static_cast<const uint8_t*>(a.x) + t * a.x_stride * O::ESZ;
+    const float* ws = FP8 ? a.w_scales + (int64_t)(group / 8) * nkb : nullptr;
+    const float* xs = FP8 ? a.x_scales + t * nkb : nullptr;
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+    auto walk = [&](auto once) {
+        for (int kb = wv; kb < nkb; kb += NW) {
 #pragma unroll
-    for (int i = 0; i < FPW; ++i) {
-        const int g = panel * FPW + i < groups ? panel * FPW + i : groups - 1;
-        w[i] = static_cast<const uint8_t*>(a.w) + (int64_t)g * (a.K / O::KS) * O::BLK;
-    }
-    const uint8_t* x[NR];
-    const float* xs[NR];
+            for (int s0 = 0; s0 < STEPS; s0 += U) {
+                op_t rw[U], rx[U];
 #pragma unroll
-    for (int j = 0; j < NR; ++j) {
-        int64_t t = t0 + j * 16 + (lane & 15);
-        t = t < a.T ? t : a.T - 1;
-        x[j] = static_cast<const uint8_t*>(a.x) + t * a.x_stride * O::ESZ;
-        xs[j] = DT == RDG_FP8_E4M3 ? a.x_scales + t * nkb : nullptr;
-    }
-    const float* ws[FPW];
-#pragma unroll
-    for (int i = 0; i < FPW; ++i) {
-        const int g = panel * FPW + i < groups ? panel * FPW + i : groups - 1;
-        ws[i] = DT == RDG_FP8_E4M3 ? a.w_scales + (int64_t)(g / 8) * nkb : nullptr;
-    }
-    f32x4_t acc[FPW][NR];
-#pragma unroll
-    for (int i = 0; i < FPW; ++i)
-#pragma unroll
-        for (int j = 0; j < NR; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-    for (int kb = wv; kb < nkb; kb += 4) {
-#pragma unroll
-        for (int s0 = 0; s0 < STEPS; s0 += U) {
-            op_t rw[U][FPW], rx[U][NR];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t step = (int64_t)kb * STEPS + s0 + u;
-#pragma unroll
-                for (int i = 0; i < FPW; ++i) rw[u][i] = O::load_w(w[i] + step * O::BLK, lane);
-#pragma unroll
-                for (int j = 0; j < NR; ++j) rx[u][j] = O::load_x(x[j], (int)step * O::KS, lane);
-            }
-            if constexpr (DT == RDG_FP8_E4M3) {
-#pragma unroll
-                for (int j = 0; j < NR; ++j) {
-                    const float sx = xs[j][kb];
-#pragma unroll
-                    for (int i = 0; i < FPW; ++i) acc[i][j] += O::mma(f32x4_t{0.f, 0.f, 0.f, 0.f}, rw[0][i], rx[0][j]) * (sx * ws[i][kb]);
+                for (int u = 0; u < U; ++u) {
+                    const int64_t step = (int64_t)kb * STEPS + s0 + u;
+                    if constexpr (decltype(once)::value) rw[u] = O::stream_w(w + step * O::BLK, lane);
+                    else rw[u] = O::load_w(w + step * O::BLK, lane);
+                    rx[u] = O::load_x(x, (int)step * O::KS, lane);
                 }
-            } else {
+                if constexpr (FP8) {
+                    const float scale = xs[kb] * ws[kb];
+                    const f32x4_t z = {0.f, 0.f, 0.f, 0.f};
+                    acc += (WIDE ? O::mma_wide(z, rw[0], rx[0]) : O::mma(z, rw[0], rx[0])) * scale;
+                } else {
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int i = 0; i < FPW; ++i)
-#pragma unroll
-                        for (int j = 0; j < NR; ++j) acc[i][j] = O::mma(acc[i][j], rw[u][i], rx[u][j]);
+                    for (int u = 0; u < U; ++u) acc = O::mma(acc, rw[u], rx[u]);
+                }
             }
         }
-    }
-#pragma unroll
-    for (int i = 0; i < FPW; ++i)
-#pragma unroll
-        for (int j = 0; j < NR; ++j) part[wv][i * NR + j][lane] = acc[i][j];
+    };
+    // weights that no other workgroup reads stream past the caches
+    if (t_tiles == 1) walk(std::true_type{});
+    else walk(std::false_type{});
+    part[wv][lane] = acc;
     __syncthreads();
     // lane l of a 16 x 16 tile: token l % 16, features 4 (l / 16) .. + 3
-    for (int c = wv; c < FPW * NR; c += 4) {
-        const int i = c / NR, j = c % NR;
-        const int64_t t = t0 + j * 16 + (lane & 15);
-        const int f = (panel * FPW + i) * 16 + (lane >> 4) * 4;
-        if (t >= a.T || f >= a.N) continue;
-        f32x4_t v = part[0][c][lane];
+    if (wv != 0 || mine >= a.T) return;
+    f32x4_t v = part[0][lane];
 #pragma unroll
-        for (int u = 1; u < 4; ++u) v += part[u][c][lane];
-        finish4(a, v, t, f);
-    }
+    for (int u = 1; u < NW; ++u) v += part[u][lane];
+    finish4(a, v, mine, group * 16 + (lane >> 4) * 4);
 }
 
-template <int DT, int FPW, int NR>
+template <int DT, bool WIDE>
 hipError_t launch_rows(const LinearCall& a, hipStream_t s) {
-    const int64_t panels = (a.N / 16 + FPW - 1) / FPW;
-    const int64_t blocks = panels * (((int64_t)a.T + 16 * NR - 1) / (16 * NR));
-    if (!grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
-    k_linear_rows<DT, FPW, NR><<<(unsigned)blocks, 256, 0, s>>>(a);
+    const int64_t blocks = (int64_t)(a.N / 16) * (((int64_t)a.T + 15) / 16);
+    if (!grid_fits(blocks, NW * 64)) return hipErrorInvalidConfiguration;
+    k_linear_rows<DT, WIDE><<<(unsigned)blocks, NW * 64, 0, s>>>(a);
     return hipGetLastError();
 }
 
-template <int DT>
-hipError_t launch_dt(const LinearCall& a, hipStream_t s) {
-    if (a.T <= 16) return launch_rows<DT, 1, 1>(a, s);
-    if (a.T <= 32) return launch_rows<DT, 1, 2>(a, s);
-    return launch_rows<DT, 2, 4>(a, s);
+// ---------------------------------------------------------------- which kernel
+// The expected time of each kernel and split in us, and the least of them.  Constants measured over 193 sizes a type
+// (8 .. 5000 tokens, 64 .. 12288 features, K of 256 .. 14336, weights from memory); the choice takes on
+// average 2% longer than the best of all at each size, 1.45 times at worst (8 tokens, 12288 features, K = 256, fp8).
+constexpr int kCus = 256;
+constexpr float kStart = 2.0f, kMore = 1.5f;            // launch, first loads, last stores; one launch more
+constexpr float kRowsRead = 6.1e6f, kTilesRead = 5.5e6f;  // bytes/us at which weights come from memory
+constexpr float kJoin = 2.4f, kJoinRate = 3.6e6f;       // the join's launch; splits' sums, written and read
+
+struct TileCost {
+    int kernel, features, tokens;
+    int per_cu;           // workgroups a CU holds (LDS)
+    float alone, loaded;  // us a stage of 128 bytes of each row and workgroup: one round of workgroups, and more
+    float tile;           // us a tile besides
+};
+// 256 x 256 is bound by the matrix core; the smaller the tile, the more bytes it loads for its products, and the less
+// of the chip a small problem leaves idle.
+constexpr TileCost kBf16Cost[4] = {{kTile256, 256, 256, 1, 1.2f, 1.4f, 6.0f},
+                                   {kTile128, 128, 128, 1, 0.383f, 0.5f, 1.8f},
+                                   {kTile128x64, 128, 64, 1, 0.282f, 0.36f, 1.2f},
+                                   {kTile64x32, 64, 32, 3, 0.138f, 0.135f, 0.8f}};
+constexpr TileCost kFp8Cost[4] = {{kTile256, 256, 256, 1, 1.3f, 1.5f, 7.0f},
+                                  {kTile128, 128, 128, 1, 0.515f, 0.63f, 2.2f},
+                                  {kTile128x64, 128, 64, 1, 0.36f, 0.40f, 1.8f},
+                                  {kTile64x32, 64, 32, 3, 0.225f, 0.176f, 0.85f}};
+constexpr TileCost kF32Cost[4] = {{kTile128, 128, 128, 1, 1.92f, 1.92f, 2.0f},
+                                  {kTile128x64, 128, 64, 1, 1.08f, 1.08f, 1.3f},
+                                  {kTile64x32, 64, 32, 3, 0.444f, 0.30f, 0.8f},
+                                  {kRows, 0, 0, 0, 0, 0, 0}};
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int size_of(int dtype) { return dtype == RDG_F32 ? 4 : dtype == RDG_BF16 ? 2 : 1; }
+
+// A wave's 2048 elements (16 waves of 128) take a time that grows with the tokens of its tile.
+float rows_us(int T, int N, int K, int dtype) {
+    const float per = dtype == RDG_F32 ? 5.0f : dtype == RDG_BF16 ? 1.25f : 0.45f;
+    const float token = dtype == RDG_F32 ? 0.6f : dtype == RDG_BF16 ? 0.097f : 0.085f;
+    const float us = K / 2048.0f * (per + token * (T < 16 ? T : 16)) * ceil_div((int64_t)(N / 16) * ceil_div(T, 16), kCus);
+    const float read_us = (float)N * K * size_of(dtype) / kRowsRead;
+    return kStart + 0.3f + (us > read_us ? us : read_us);
 }
+
+float tiles_us(const TileCost& c, int splits, int T, int N, int K, int dtype) {
+    const int stages = (int)ceil_div(K / 128, splits) * size_of(dtype);
+    const int64_t rounds = ceil_div(ceil_div(N, c.features) * ceil_div(T, c.tokens) * splits, kCus);
+    const int64_t full = rounds / c.per_cu, rest = rounds % c.per_cu;
+    auto round_us = [&](int64_t workgroups) {
+        const float loaded = c.loaded * workgroups, stage = rounds == 1 || loaded < c.alone ? c.alone : loaded;
+        return stages * stage + c.tile;
+    };
+    const float us = full * round_us(c.per_cu) + (rest ? round_us(rest) : 0.0f);
+    const float read_us = (float)N * K * size_of(dtype) / kTilesRead;
+    return kStart + (us > read_us ? us : read_us) + (splits > 1 ? kJoin + (float)splits * T * N * 8 / kJoinRate : 0.0f);
+}
+
+// One kernel for all features.
+LinearPart plan_part(int T, int N, int K, int dtype, float& least) {
+    const TileCost* cost = dtype == RDG_F32 ? kF32Cost : dtype == RDG_BF16 ? kBf16Cost : kFp8Cost;
+    LinearPart best{kRows, 1, N};
+    // (beyond 32 tokens the tiles are always faster)
+    least = T <= 32 ? rows_us(T, N, K, dtype) : 3e38f;
+    for (int i = 0; i < 4 && cost[i].kernel != kRows; ++i) {
+        const int64_t tiles = ceil_div(N, cost[i].features) * ceil_div(T, cost[i].tokens);
+        for (int splits = 1; splits <= 8 && splits <= K / 128; splits *= 2) {
+            if (splits > 1 && tiles * splits > 4 * kCus) break;  // (which also bounds the workspace: 256 MiB)
+            const float us = tiles_us(cost[i], splits, T, N, K, dtype);
+            if (us < least) least = us, best = LinearPart{cost[i].kernel, splits, N};
+        }
+    }
+    return best;
+}
+
+// Two where the last round of 256 x 256 tiles would leave much of the chip idle: whole rounds of them, and smaller tiles or
+// splits for the features behind.  bf16, 8192 x 7168 x 8192 (3.5 rounds) 695 us against 728; 2048 x 9216 x 7168
+// (1.1 rounds) 200 against 246.
+LinearPlan linear_plan(int T, int N, int K, int dtype) {
+    float least, rest_us;
+    LinearPlan p{plan_part(T, N, K, dtype, least), LinearPart{kRows, 1, 0}};
+    if (dtype == RDG_F32) return p;
+    const int64_t t_tiles = ceil_div(T, 256), rounds = ceil_div(N, 256) * t_tiles / kCus;
+    const int64_t features = rounds * kCus / t_tiles * 256;
+    if (features == 0 || features >= N) return p;
+    const TileCost& c = dtype == RDG_BF16 ? kBf16Cost[0] : kFp8Cost[0];
+    const LinearPart rest = plan_part(T, N - (int)features, K, dtype, rest_us);
+    if (tiles_us(c, 1, T, (int)features, K, dtype) + rest_us + kMore - kStart < least)
+        p = LinearPlan{LinearPart{kTile256, 1, (int)features}, rest};
+    return p;
+}
+
+hipError_t launch_part(const LinearCall& a, const LinearPart& p, hipStream_t s) {
+    // the tiles address their token rows (at most 256) and their scales with 32 bits
+    const bool near = a.x_stride * size_of(a.dtype) * 256 < (int64_t)1 << 31;
+    if (p.kernel != kRows && near) return launch_linear_tiled(a, p, s);
+    switch (a.dtype) {
+        case RDG_F32: return launch_rows<RDG_F32, false>(a, s);
+        case RDG_BF16: return launch_rows<RDG_BF16, false>(a, s);
+        default: return a.out_bf16 ? launch_rows<RDG_FP8_E4M3, false>(a, s) : launch_rows<RDG_FP8_E4M3, true>(a, s);
+    }
+}
+
+size_t part_bytes(const LinearPart& p, int T) { return p.splits > 1 ? (size_t)p.splits * T * p.features * 4 : 0; }
 
 }  // namespace
 
 hipError_t launch_linear(const LinearCall& a, hipStream_t s) {
     if (a.T == 0) return hipSuccess;
-    if (a.dtype != RDG_F32 && a.T > 256) return launch_linear_tiled(a, s);
-    switch (a.dtype) {
-        case RDG_F32: return launch_dt<RDG_F32>(a, s);
-        case RDG_BF16: return launch_dt<RDG_BF16>(a, s);
-        default: return launch_dt<RDG_FP8_E4M3>(a, s);
-    }
+    const LinearPlan p = linear_plan(a.T, a.N, a.K, a.dtype);
+    LinearCall b = a;
+    b.N = p.first.features;
+    hipError_t err = launch_part(b, p.first, s);
+    if (err != hipSuccess || p.rest.features == 0) return err;
+    // the features behind: a multiple of 256 of them are done
+    const int64_t n = b.N;
+    const int osz = a.out_bf16 ? 2 : 4;
+    b.N = p.rest.features;
+    b.w = static_cast<const uint8_t*>(a.w) + n * a.K * size_of(a.dtype);
+    b.out = static_cast<uint8_t*>(a.out) + n * osz;
+    if (a.w_scales) b.w_scales = a.w_scales + n / 128 * (a.K / 128);
+    if (a.bias) b.bias = a.bias + n;
+    if (a.residual) b.residual = static_cast<const uint8_t*>(a.residual) + n * osz;
+    return launch_part(b, p.rest, s);
 }
 
-size_t linear_workspace_bytes(int T, int N, int K, int dtype) { return 0; }
+size_t linear_workspace_bytes(int T, int N, int K, int dtype) {
+    if (T == 0) return 0;
+    // the parts' launches run one after the other, and only the second has splits
+    const LinearPlan p = linear_plan(T, N, K, dtype);
+    const size_t first = part_bytes(p.first, T), rest = part_bytes(p.rest, T);
+    return first > rest ? first : rest;
+}
 
 }  // namespace rdg

@@ -9,32 +9,60 @@ namespace {
 
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
-// s_waitcnt immediates (vmcnt in bits 3:0 and 15:14, expcnt 6:4, lgkmcnt 11:8).
-constexpr int kWaitVm0 = (7 << 4) | (15 << 8);
-constexpr int kWaitLgkm0 = 15 | (3 << 14) | (7 << 4);
-
 // What a kernel does with its operands: bf16; e4m3 with fp32 scales (each partial product of 128
-// is scaled into the sum); e4m3 with power-of-two scales (the matrix core applies them).
-enum { kBf16 = 0, kFp8 = 1, kE8m0 = 2 };
+// is scaled into the sum); e4m3 with power-of-two scales (the matrix core applies them); e4m3 with either,
+// its products from bf16 operands; fp32.
+using Yes = std::true_type;
+using No = std::false_type;
+enum { kBf16 = 0, kFp8 = 1, kE8m0 = 2, kFp8Wide = 3, kF32 = 4 };
 
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-// 16 (4) bytes a lane from base + off + IMM straight to lds + IMM + 16 (4) * lane (base and lds wave-uniform).
-// The compiler does not count these loads; meet() below waits for them.
-template <int IMM>
-__device__ __forceinline__ void dma16(const uint8_t* base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1 offset:%3" ::"v"(off), "s"(base), "s"(lds), "n"(IMM) : "memory", "m0");
+// 16 (4) bytes a lane from base + off + IMM straight to lds + IMM + 16 (4) * lane (base and lds wave-uniform); with
+// TEST where `now` < `end`.  The compiler does not count these loads: meet() below waits for them.  The branch is in the
+// assembly, as the compiler would move matrix instructions past one of its own.
+template <int IMM, bool TEST>
+__device__ __forceinline__ void dma16(int now, int end, const uint8_t* base, uint32_t off, uint32_t lds) {
+    if constexpr (!TEST)
+        asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1 offset:%3" ::"v"(off), "s"(base), "s"(lds), "n"(IMM) : "memory", "m0");
+    else
+        asm volatile("s_cmp_ge_i32 %4, %5\n\ts_cbranch_scc1 1f\n\ts_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1 offset:%3\n1:" ::"v"(off),
+                 "s"(base), "s"(lds), "n"(IMM), "s"(now), "s"(end)
+                 : "memory", "m0", "scc");
 }
-__device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory", "m0");
+__device__ __forceinline__ void dma4(int now, int end, const void* base, uint32_t off, uint32_t lds) {
+    asm volatile("s_cmp_ge_i32 %3, %4\n\ts_cbranch_scc1 1f\n\ts_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1\n1:" ::"v"(off), "s"(base),
+                 "s"(lds), "s"(now), "s"(end)
+                 : "memory", "m0", "scc");
 }
 #pragma clang diagnostic pop
 
+// Waits until at most P * min(MOST, left) of the wave's loads are outstanding (none for left <= 0), and for
+// its LDS reads.
+template <int P, int MOST, bool TEST>
+__device__ __forceinline__ void wait_loads(int left) {
+    static_assert(MOST >= 0 && MOST <= 4 && P * MOST < 64, "vmcnt is six bits");
+    if constexpr (MOST == 0 || !TEST) {
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(P * MOST) : "memory");
+    } else if constexpr (MOST <= 2) {
+        asm volatile("s_cmp_ge_i32 %0, %1\n\ts_cbranch_scc1 2f\n\ts_cmp_ge_i32 %0, 1\n\ts_cbranch_scc1 1f\n\ts_waitcnt vmcnt(0)\n"
+                     "1:\ts_waitcnt vmcnt(%2)\n2:\ts_waitcnt vmcnt(%3) lgkmcnt(0)" ::"s"(left), "n"(MOST), "n"(P), "n"(P * MOST)
+                     : "memory", "scc");
+    } else {
+        asm volatile("s_cmp_ge_i32 %0, %1\n\ts_cbranch_scc1 4f\n\ts_cmp_ge_i32 %0, 3\n\ts_cbranch_scc1 3f\n\ts_cmp_ge_i32 %0, 2\n\t"
+                     "s_cbranch_scc1 2f\n\ts_cmp_ge_i32 %0, 1\n\ts_cbranch_scc1 1f\n\ts_waitcnt vmcnt(0)\n1:\ts_waitcnt vmcnt(%2)\n"
+                     "2:\ts_waitcnt vmcnt(%3)\n3:\ts_waitcnt vmcnt(%4)\n4:\ts_waitcnt vmcnt(%5) lgkmcnt(0)" ::"s"(left), "n"(MOST), "n"(P),
+                     "n"(2 * P), "n"(3 * P), "n"(P * MOST)
+                     : "memory", "scc");
+    }
+}
+
 // LDS place of 16-byte piece c of tile row r (rows of 128 bytes).  A read's 16 rows are served
-// 16 lanes at a time, a mix of two pieces: pieces next to each other for bf16, two apart for e4m3.
-template <bool FP8>
+// 16 lanes at a time, a mix of two pieces: pieces next to each other for bf16, two apart for e4m3 (fp32: one
+// piece, read by fours of a lane each).
+template <bool NEXT>
 __device__ __forceinline__ int piece_slot(int r, int c) {
-    return c ^ ((r & 7) ^ (((r >> 3) & 1) << (FP8 ? 0 : 1)));
+    return c ^ ((r & 7) ^ (((r >> 3) & 1) << (NEXT ? 1 : 0)));
 }
 
 // f(0), f(1), .. f(N - 1) with compile-time arguments.
@@ -47,32 +75,38 @@ __device__ __forceinline__ void each(F&& f) {
     each_of<N>(f, std::make_integer_sequence<int, N>{});
 }
 
-template <int KIND, int WF, int WT, int NF, int NTK>
-__global__ __launch_bounds__(WF * WT * 64, 1) void k_linear_tiled(LinearCall a, int f_tiles, int t_tiles) {
-    constexpr bool FP8 = KIND != kBf16;
+template <int KIND, int WF, int WT, int NF, int NTK, int NB>
+__global__ __launch_bounds__(WF * WT * 64, 2) void k_linear_tiled(LinearCall a, int f_tiles, int t_tiles, int splits) {
+    constexpr bool FP8 = KIND == kFp8 || KIND == kE8m0 || KIND == kFp8Wide, F32 = KIND == kF32, BF16 = KIND == kBf16;
     constexpr int NW = WF * WT, TF = WF * NF * 16, TT = WT * NTK * 16;
-    constexpr int WB = TF * 128, XB = TT * 128, STAGE = WB + XB;  // bytes of a stage: 128 of each row
+    constexpr int WB = TF * 128, XB = TT * 128, STAGE = WB + XB;    // bytes of a stage: 128 of each row
     constexpr int PIECES = STAGE / 1024 / NW, WL = WB / 1024 / NW;  // KiB loads a wave and stage, the weights' first
-    constexpr int ESZ = FP8 ? 1 : 2, S = FP8 ? 1 : 2;             // matrix steps of a stage
+    constexpr int ESZ = FP8 ? 1 : F32 ? 4 : 2, S = FP8 ? 1 : F32 ? 8 : 2;  // matrix steps of a stage
     // fp8: scales of SC stages at a time, [token][stage], then [128 features][stage]
-    constexpr int SC = 8, FB = TF / 128, SB = (TT * SC + 64) * 4;
-    constexpr int OUT_ROW = NF * 16 + 4;                          // floats; 32 token rows a wave in the epilogue
-    constexpr int LDS_LOOP = 2 * STAGE + (FP8 ? 2 * SB : 0), LDS_OUT = NW * 32 * OUT_ROW * 4;
-    static_assert(WL % 2 == 0 && (!FP8 || (NF == 8 && SC * NW > TT * SC / 64)), "shape");
+    constexpr int SC = 8, SB = (TT * SC + 64) * 4;
+    constexpr int OUT_ROW = NF * 16 + 4;                            // floats; 32 token rows a wave in the epilogue
+    constexpr int LDS_LOOP = NB * STAGE + (FP8 ? 2 * SB : 0), LDS_OUT = NW * 32 * OUT_ROW * 4;
+    static_assert(WL % 2 == 0 && PIECES * 1024 * NW == STAGE && NTK % 2 == 0, "shape");
+    // the scales' loads of a chunk are issued 3 stages before its first use
+    static_assert(!FP8 || (128 % (NF * 16) == 0 && (SC - 3) * NW > TT * SC / 64 && NB <= 5), "shape");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS_LOOP > LDS_OUT ? LDS_LOOP : LDS_OUT];
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
     const int wf = wv / WT, wt = wv % WT;
 
     // XCD b % 8 takes a contiguous share of the tiles, ordered in bands of 4 feature tiles that are
     // walked along the tokens: the tiles that run together on an XCD share their operands in its L2.
-    const int n = f_tiles * t_tiles, xcd = blockIdx.x % 8, q8 = n / 8, r8 = n % 8;
-    const int item = xcd * q8 + (xcd < r8 ? xcd : r8) + blockIdx.x / 8;
+    const int tiles = f_tiles * t_tiles, n = tiles * splits, xcd = blockIdx.x % 8, q8 = n / 8, r8 = n % 8;
+    const int job = xcd * q8 + (xcd < r8 ? xcd : r8) + blockIdx.x / 8;
+    const int split = job / tiles, item = job % tiles;
     const int band = item / (4 * t_tiles), in_band = item % (4 * t_tiles);
     const int wide = f_tiles - 4 * band < 4 ? f_tiles - 4 * band : 4;
     const int ft = 4 * band + in_band % wide;
     const int64_t t0 = (int64_t)(in_band / wide) * TT;
     const int g0 = ft * (TF / 16), groups = a.N / 16;
-    const int row_bytes = a.K * ESZ, nst = row_bytes / 128, nkb = a.K / 128;
+    const int row_bytes = a.K * ESZ, nkb = a.K / 128;
+    // this split's blocks of 128 elements: kb0 .. kb1 - 1, in stages
+    const int kb0 = (int)((int64_t)nkb * split / splits), kb1 = (int)((int64_t)nkb * (split + 1) / splits);
+    const int nst = (kb1 - kb0) * ESZ;
     const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr_t)lds;
 
     // rows past the last: the last one again, not stored
@@ -80,35 +114,36 @@ __global__ __launch_bounds__(WF * WT * 64, 1) void k_linear_tiled(LinearCall a, 
 #pragma unroll
     for (int i = 0; i < WL / 2; ++i) {
         const int g = g0 + wv * (WL / 2) + i;
-        wsrc[i] = static_cast<const uint8_t*>(a.w) + (int64_t)(g < groups ? g : groups - 1) * 16 * row_bytes;
+        wsrc[i] = static_cast<const uint8_t*>(a.w) + (int64_t)(g < groups ? g : groups - 1) * 16 * row_bytes + (int64_t)kb0 * 2048 * ESZ;
     }
     const int rows = a.T - t0 < TT ? (int)(a.T - t0) : TT;
-    const uint8_t* xsrc = static_cast<const uint8_t*>(a.x) + t0 * a.x_stride * ESZ;
+    const uint8_t* xsrc = static_cast<const uint8_t*>(a.x) + t0 * a.x_stride * ESZ + (int64_t)kb0 * 128 * ESZ;
     const uint32_t woff = lane * 16;
     uint32_t xoff[PIECES - WL];
 #pragma unroll
     for (int i = 0; i < PIECES - WL; ++i) {
         const int r = (wv * (PIECES - WL) + i) * 8 + lane / 8;
-        xoff[i] = (uint32_t)(r < rows ? r : rows - 1) * (uint32_t)(a.x_stride * ESZ) + piece_slot<FP8>(r, lane % 8) * 16;
+        xoff[i] = (uint32_t)(r < rows ? r : rows - 1) * (uint32_t)(a.x_stride * ESZ) + piece_slot<BF16>(r, lane % 8) * 16;
     }
-    // piece p of stage st
-    auto request = [&](int st, int buf, auto pc) {
+    // piece p of stage st; with TEST if there is such a stage
+    auto request = [&](int st, int place, auto pc, auto test) {
+        constexpr bool TEST = decltype(test)::value;
         constexpr int p = decltype(pc)::value;
-        const uint32_t to = base + buf * STAGE;
+        const uint32_t to = base + place;
         if constexpr (p < WL)
-            dma16<p % 2 * 1024>(wsrc[p / 2] + (int64_t)st * 2048, woff, to + (wv * WL + p / 2 * 2) * 1024);
+            dma16<p % 2 * 1024, TEST>(st, nst, wsrc[p / 2] + (int64_t)st * 2048, woff, to + (wv * WL + p / 2 * 2) * 1024);
         else if constexpr (p < PIECES)
-            dma16<0>(xsrc + (int64_t)st * 128, xoff[p - WL], to + WB + (wv * (PIECES - WL) + p - WL) * 1024);
+            dma16<0, TEST>(st, nst, xsrc + (int64_t)st * 128, xoff[p - WL], to + WB + (wv * (PIECES - WL) + p - WL) * 1024);
     };
-    // piece `slot` (64 in all, the last ones alike) of the scales of stages SC c .. (past the end the last
+    // piece `slot` (SC * NW in all, the last ones alike) of the scales of stages SC c .. (past the end the last
     // stage's again): 8 tokens, or the tile's blocks of 128 features
     auto request_scales = [&](int c, int slot) {
         constexpr int XP = TT * SC / 64;
         const bool of_w = slot >= XP;
-        const int first = of_w ? ft * FB : slot * 8, most = of_w ? (a.N - 1) / 128 : rows - 1;
-        const int r = first + lane / SC, kb = c * SC + lane % SC;
-        dma4(of_w ? a.w_scales : a.x_scales + t0 * nkb, ((r < most ? r : most) * nkb + (kb < nkb ? kb : nkb - 1)) * 4,
-             base + 2 * STAGE + (c & 1) * SB + (of_w ? XP : slot) * 256);
+        const int first = of_w ? g0 / 8 : slot * 8, most = of_w ? (a.N - 1) / 128 : rows - 1;
+        const int r = first + lane / SC, kb = kb0 + c * SC + lane % SC;
+        dma4(c * SC, nst, of_w ? a.w_scales : a.x_scales + t0 * nkb, ((r < most ? r : most) * nkb + (kb < nkb ? kb : nkb - 1)) * 4,
+             base + NB * STAGE + (c & 1) * SB + (of_w ? XP : slot) * 256);
     };
 
     f32x4_t acc[NF][NTK];
@@ -119,158 +154,193 @@ __global__ __launch_bounds__(WF * WT * 64, 1) void k_linear_tiled(LinearCall a, 
 
     // fragments: a wave's items are (step s, weight tile i), NTK matrix instructions each.  Weight
     // fragments are read AHEAD items before their use, token fragments a step before.
-    using op_t = typename LinOp<FP8 ? RDG_FP8_E4M3 : RDG_BF16>::op_t;
-    constexpr int NI = S * NF, AHEAD = FP8 ? 1 : 3, RPI = FP8 ? 2 : 1;
-    op_t fa[AHEAD + 1], fb[S][NTK];
-    float sx[2][NTK], sw[2];
-    const uint8_t* wl = lds + wf * NF * 2048 + lane * 16;
-    const uint8_t* xl[2];
+    using op_t = typename LinOp<FP8 ? RDG_FP8_E4M3 : F32 ? RDG_F32 : RDG_BF16>::op_t;
+    constexpr int NI = S * NF, AHEAD = FP8 || NF < 4 ? 1 : 3, RPI = (2 * PIECES + NI - 1) / NI;
+    constexpr int EARLY = AHEAD * RPI < PIECES ? AHEAD * RPI : PIECES;  // pieces issued between the meeting and the stage's end
+    constexpr int SETS = S > 1 ? 2 : 1;
+    static_assert(AHEAD <= NF && (NI % (AHEAD + 1) == 0 || NI == 1), "this stage's fragments are read before the meeting");
+    static_assert(NI * RPI >= PIECES, "items");
+    op_t fa[AHEAD + 1], fb[SETS][NTK];
+    float sx[NTK], sw = 1.0f;
+    const int wl = wf * NF * 2048 + lane * (F32 ? 4 : 16);
+    int xl[F32 ? 8 : 2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int piece = FP8 ? (lane >> 4) * 2 + h : h * 4 + (lane >> 4);
-        xl[h] = lds + WB + wt * NTK * 2048 + (lane & 15) * 128 + piece_slot<FP8>(lane & 15, piece) * 16;
+    for (int h = 0; h < (F32 ? 8 : 2); ++h) {
+        const int piece = FP8 ? (lane >> 4) * 2 + h : F32 ? h : h * 4 + (lane >> 4);
+        xl[h] = WB + wt * NTK * 2048 + (lane & 15) * 128 + piece_slot<BF16>(lane & 15, piece) * 16 + (F32 ? (lane >> 4) * 4 : 0);
     }
-    auto read_a = [&](int buf, int it) {
-        const uint8_t* p = wl + buf * STAGE + (it % NF) * 2048;
+    auto read_a = [&](int place, int it) {
+        const uint8_t* p = lds + (wl + place) + (it % NF) * 2048;
         if constexpr (FP8)
             fa[it % (AHEAD + 1)] = LinOp<RDG_FP8_E4M3>::join(*reinterpret_cast<const i32x4_t*>(p), *reinterpret_cast<const i32x4_t*>(p + 1024));
         else
-            fa[it % (AHEAD + 1)] = *reinterpret_cast<const bf16x8_t*>(p + (it / NF) * 1024);
+            fa[it % (AHEAD + 1)] = *reinterpret_cast<const op_t*>(p + (it / NF) * (F32 ? 256 : 1024));
     };
-    auto read_b = [&](int buf, int s, int j) {
+    auto read_b = [&](int place, int s, int j) {
         if constexpr (FP8)
-            fb[0][j] = LinOp<RDG_FP8_E4M3>::join(*reinterpret_cast<const i32x4_t*>(xl[0] + buf * STAGE + j * 2048),
-                                                   *reinterpret_cast<const i32x4_t*>(xl[1] + buf * STAGE + j * 2048));
+            fb[0][j] = LinOp<RDG_FP8_E4M3>::join(*reinterpret_cast<const i32x4_t*>(lds + (xl[0] + place) + j * 2048),
+                                                 *reinterpret_cast<const i32x4_t*>(lds + (xl[1] + place) + j * 2048));
         else
-            fb[s][j] = *reinterpret_cast<const bf16x8_t*>(xl[s] + buf * STAGE + j * 2048);
+            fb[s % SETS][j] = *reinterpret_cast<const op_t*>(lds + (xl[s] + place) + j * 2048);
     };
-    auto read_scales = [&](int st, int set) {
-        const float* p = reinterpret_cast<const float*>(lds + 2 * STAGE + (st / SC & 1) * SB);
+    auto read_scales = [&](int st, float (&x)[NTK], float& w) {
+        const float* p = reinterpret_cast<const float*>(lds + NB * STAGE + (st / SC & 1) * SB);
 #pragma unroll
-        for (int j = 0; j < NTK; ++j) sx[set][j] = p[(wt * NTK * 16 + j * 16 + (lane & 15)) * SC + st % SC];
-        sw[set] = p[TT * SC + wf * SC + st % SC];
+        for (int j = 0; j < NTK; ++j) x[j] = p[(wt * NTK * 16 + j * 16 + (lane & 15)) * SC + st % SC];
+        w = p[TT * SC + wf * NF / 8 * SC + st % SC];
     };
-    // Every wave's loads have landed, and every wave has its fragments in registers.
-    auto meet = [&]() {
+    // In stage st: stage st + 1 has landed for every wave, and every wave has stage st's fragments in
+    // registers, so that its place is free.
+    auto meet = [&](int st, auto test) {
         __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt(kWaitVm0 & kWaitLgkm0);
+        wait_loads<PIECES, NB - 2, decltype(test)::value>(nst - 2 - st);
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    each<PIECES>([&](auto p) { request(0, 0, p); });
+    // the first NB - 1 stages, and what of the next one stage 0 takes as issued
+    each<PIECES>([&](auto p) { request(0, 0, p, Yes{}); });
     if (FP8) {
 #pragma unroll
         for (int i = 0; i < SC; ++i) request_scales(0, i * NW + wv);
     }
-    meet();
-    if (nst > 1) each<AHEAD * RPI>([&](auto p) { request(1, 1, p); });
+    each<NB - 2>([&](auto b) { each<PIECES>([&](auto p) { request(decltype(b)::value + 1, (decltype(b)::value + 1) * STAGE, p, Yes{}); }); });
+    meet(-1, Yes{});
+    each<EARLY>([&](auto p) { request(NB - 1, (NB - 1) * STAGE, p, Yes{}); });
 #pragma unroll
     for (int j = 0; j < NTK; ++j) read_b(0, 0, j);
-    if (FP8) read_scales(0, 0);
+    if (FP8) read_scales(0, sx, sw);
 #pragma unroll
     for (int it = 0; it < AHEAD; ++it) read_a(0, it);
     __builtin_amdgcn_sched_barrier(0);
 
     f32x4_t part[2][2];  // fp8 with fp32 scales: products of two token tiles, and the two before
-    // left: stages behind this one, 2 for two and more.  (No branch inside: the compiler would move the matrix
-    // instructions past it.)
-    auto stage = [&](int st, auto bufc, auto leftc) {
-        constexpr int buf = decltype(bufc)::value, left = decltype(leftc)::value;
-        float f[NTK];
+    int here = 0;        // place of stage st in LDS
+    auto stage = [&](int st, auto test) {
+        const int next = here + STAGE == NB * STAGE ? 0 : here + STAGE, before = here == 0 ? (NB - 1) * STAGE : here - STAGE;
+        float f[NTK], next_sx[NTK], next_sw = 1.0f;
         int ex[NTK], ew = 0;
-        if constexpr (KIND == kFp8) {
+        if constexpr (KIND == kFp8 || KIND == kFp8Wide) {
 #pragma unroll
-            for (int j = 0; j < NTK; ++j) f[j] = sx[buf][j] * sw[buf];
+            for (int j = 0; j < NTK; ++j) f[j] = sx[j] * sw;
         }
         if constexpr (KIND == kE8m0) {
 #pragma unroll
-            for (int j = 0; j < NTK; ++j) ex[j] = e8m0_of(sx[buf][j]);
-            ew = e8m0_of(sw[buf]);
+            for (int j = 0; j < NTK; ++j) ex[j] = e8m0_of(sx[j]);
+            ew = e8m0_of(sw);
         }
         each<NI>([&](auto itc) {
             constexpr int it = decltype(itc)::value, s = it / NF, i = it % NF;
-            if constexpr (FP8 && it == 0 && left > 0) request_scales(st / SC + 1, st % SC * NW + wv);
-            if (it + AHEAD < NI) read_a(buf, it + AHEAD);
-            if (s + 1 < S && i >= NF - NTK) read_b(buf, s + 1, i - (NF - NTK));
-            if (it == NI - AHEAD) {
-                // behind the meeting the next stage has landed and this one's place is free
-                meet();
-                if constexpr (FP8) {
-                    if constexpr (left > 0) read_scales(st + 1, buf ^ 1);
-                } else if constexpr (left > 0) {
+            if constexpr (FP8 && it == 0) request_scales(st / SC + 1, st % SC * NW + wv);
+            const op_t w = fa[it % (AHEAD + 1)];
+            if (it + AHEAD < NI) read_a(here, it + AHEAD);
+            if constexpr (s + 1 < S) {  // in the step's last items, all in one where it has fewer than NTK
+                if constexpr (NF < NTK) {
+                    if constexpr (i == NF - 1) {
 #pragma unroll
-                    for (int j = 0; j < NTK; ++j) read_b(buf ^ 1, 0, j);
+                        for (int j = 0; j < NTK; ++j) read_b(here, s + 1, j);
+                    }
+                } else if constexpr (i >= NF - NTK) {
+                    read_b(here, s + 1, i - (NF - NTK));
                 }
             }
-            // the next loads a few at a time: all at once they would hold up the wave's own instructions
-            if constexpr (it >= NI - AHEAD) {
-                if constexpr (left > 1)
-                    each<RPI>([&](auto r) { request(st + 2, buf, std::integral_constant<int, (it - (NI - AHEAD)) * RPI + decltype(r)::value>{}); });
-            } else if constexpr (left > 0 && (it + AHEAD) * RPI < PIECES) {
-                each<RPI>([&](auto r) { request(st + 1, buf ^ 1, std::integral_constant<int, (it + AHEAD) * RPI + decltype(r)::value>{}); });
+            if constexpr (it == NI - AHEAD) {
+                meet(st, test);
+                if constexpr (FP8) {
+                    read_scales(st + 1, next_sx, next_sw);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < NTK; ++j) read_b(next, 0, j);
+                }
             }
-            if (left > 0 && it + AHEAD >= NI) read_a(buf ^ 1, it + AHEAD - NI);
-            const op_t w = fa[it % (AHEAD + 1)];
-            if constexpr (KIND == kBf16) {
+            // loads a few at a time, the last stages but one's: all at once they would hold up the wave's own instructions
+            each<RPI>([&](auto r) {
+                if constexpr (it >= NI - AHEAD)
+                    request(st + NB, here, std::integral_constant<int, (it - (NI - AHEAD)) * RPI + decltype(r)::value>{}, test);
+                else
+                    request(st + NB - 1, before, std::integral_constant<int, EARLY + it * RPI + decltype(r)::value>{}, test);
+            });
+            // (behind the last stage the first fragments are read from a place that holds none, and not used)
+            if (it + AHEAD >= NI) read_a(next, it + AHEAD - NI);
+            if constexpr (BF16 || F32) {
 #pragma unroll
                 for (int j = 0; j < NTK; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, fb[s][j], acc[i][j], 0, 0, 0);
+                    acc[i][j] = LinOp<F32 ? RDG_F32 : RDG_BF16>::mma(acc[i][j], w, fb[s % SETS][j]);
             } else if constexpr (KIND == kE8m0) {
 #pragma unroll
                 for (int j = 0; j < NTK; ++j) {
                     acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, fb[0][j], acc[i][j], 0, 0, 0, ew, 0, ex[j]);
-                    if (left > 0 && it == NI - 1) {
+                    if (it == NI - 1) {
                         __builtin_amdgcn_sched_barrier(0);
-                        read_b(buf ^ 1, 0, j);  // in its predecessor's place, used for the last time
+                        read_b(next, 0, j);  // in its predecessor's place, used for the last time
                     }
                 }
             } else {
                 // two products at a time, and behind them the two before them into the sum
 #pragma unroll
                 for (int h = 0; h < NTK / 2; ++h) {
-                    const int now = it * (NTK / 2) + h, before = now - 1;
+                    const int now = it * (NTK / 2) + h, then = now - 1;
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) part[now % 2][u] = LinOp<RDG_FP8_E4M3>::mma(f32x4_t{0.f, 0.f, 0.f, 0.f}, w, fb[0][2 * h + u]);
+                    for (int u = 0; u < 2; ++u) {
+                        const f32x4_t z = {0.f, 0.f, 0.f, 0.f};
+                        part[now % 2][u] = KIND == kFp8Wide ? LinOp<RDG_FP8_E4M3>::mma_wide(z, w, fb[0][2 * h + u]) : LinOp<RDG_FP8_E4M3>::mma(z, w, fb[0][2 * h + u]);
+                    }
                     __builtin_amdgcn_sched_barrier(0);
-                    if (left > 0 && it == NI - 1) {
+                    if (it == NI - 1) {
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) read_b(buf ^ 1, 0, 2 * h + u);
+                        for (int u = 0; u < 2; ++u) read_b(next, 0, 2 * h + u);
                     }
                     if (now > 0) {
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
-                            const int jb = before % (NTK / 2) * 2 + u;
-                            acc[before / (NTK / 2)][jb] += part[before % 2][u] * f[jb];
+                            const int jb = then % (NTK / 2) * 2 + u;
+                            acc[then / (NTK / 2)][jb] += part[then % 2][u] * f[jb];
                         }
                     }
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
         });
-        if constexpr (KIND == kFp8) {
+        if constexpr (KIND == kFp8 || KIND == kFp8Wide) {
             constexpr int last = NI * (NTK / 2) - 1;
 #pragma unroll
             for (int u = 0; u < 2; ++u) acc[NF - 1][NTK - 2 + u] += part[last % 2][u] * f[NTK - 2 + u];
         }
+        if constexpr (FP8) {
+#pragma unroll
+            for (int j = 0; j < NTK; ++j) sx[j] = next_sx[j];
+            sw = next_sw;
+        }
+        here = next;
     };
-    using I0 = std::integral_constant<int, 0>;
-    using I1 = std::integral_constant<int, 1>;
-    using I2 = std::integral_constant<int, 2>;
     int st = 0;
-    for (; st + 3 < nst; st += 2) {
-        stage(st, I0{}, I2{});
-        stage(st + 1, I1{}, I2{});
-    }
-    if (!FP8 || nst % 2 == 0) {  // two stages left (bf16: K is a multiple of 128)
-        stage(st, I0{}, I1{});
-        stage(st + 1, I1{}, I0{});
-    } else if (nst > 1) {
-        stage(st, I0{}, I2{});
-        stage(st + 1, I1{}, I1{});
-        stage(st + 2, I0{}, I0{});
+    if constexpr (F32) {
+        // sums of 512 products each, then their sum: the rounding errors of one long chain of fp32 products grow with its
+        // length (K = 4096: 1.1e-6 of the result in one chain, 4e-7 in eights)
+        f32x4_t total[NF][NTK];
+        auto flush = [&](bool first) {
+#pragma unroll
+            for (int i = 0; i < NF; ++i)
+#pragma unroll
+                for (int j = 0; j < NTK; ++j) {
+                    total[i][j] = first ? acc[i][j] : total[i][j] + acc[i][j];
+                    acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                }
+        };
+        flush(true);
+        while (st < nst) {
+            const int stop = st + 16 < nst ? st + 16 : nst, free = stop < nst - NB ? stop : nst - NB;
+            for (; st < free; ++st) stage(st, No{});
+            for (; st < stop; ++st) stage(st, Yes{});
+            flush(false);
+        }
+#pragma unroll
+        for (int i = 0; i < NF; ++i)
+#pragma unroll
+            for (int j = 0; j < NTK; ++j) acc[i][j] = total[i][j];
     } else {
-        stage(st, I0{}, I0{});
+        for (; st < nst - NB; ++st) stage(st, No{});
+        for (; st < nst; ++st) stage(st, Yes{});
     }
 
     // ---------------------------------------------------------------- epilogue
@@ -279,10 +349,6 @@ __global__ __launch_bounds__(WF * WT * 64, 1) void k_linear_tiled(LinearCall a, 
     constexpr int LPR = NF * 2, RPP = 64 / LPR;  // lanes a row, rows a pass
     float* tile = reinterpret_cast<float*>(lds) + wv * 32 * OUT_ROW;
     const int f = (g0 + wf * NF) * 16 + lane % LPR * 8;
-    float bias[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) bias[e] = 0.0f;
-    if (a.bias != nullptr && f < a.N) load8<false>(a.bias, f, bias);
 #pragma unroll
     for (int half = 0; half < NTK / 2; ++half) {
 #pragma unroll
@@ -299,7 +365,10 @@ __global__ __launch_bounds__(WF * WT * 64, 1) void k_linear_tiled(LinearCall a, 
             const int64_t t = t0 + (wt * NTK + half * 2) * 16 + row;
             float v[8];
             load8<false>(tile + row * OUT_ROW, lane % LPR * 8, v);
-            if (t < a.T && f < a.N) finish8(a, v, bias, t, f);
+            if (t < a.T && f < a.N) {
+                if (splits == 1) finish8(a, v, t, f);
+                else store8<false>(a.parts, ((int64_t)split * a.T + t) * a.N + f, v);
+            }
         }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
@@ -307,20 +376,56 @@ __global__ __launch_bounds__(WF * WT * 64, 1) void k_linear_tiled(LinearCall a, 
     }
 }
 
-template <int KIND, int WF, int WT, int NF, int NTK>
-hipError_t launch(const LinearCall& a, hipStream_t s) {
+// The splits' sums in their order, and the epilogue: 8 features a thread.
+__global__ __launch_bounds__(256) void k_linear_join(LinearCall a, int splits) {
+    const int per_row = a.N / 8;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, all = (int64_t)a.T * per_row;
+    if (i >= all) return;
+    float v[8], p[8];
+    load8<false>(a.parts, i * 8, v);
+    for (int s = 1; s < splits; ++s) {
+        load8<false>(a.parts, ((int64_t)s * all + i) * 8, p);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += p[e];
+    }
+    finish8(a, v, i / per_row, (int)(i % per_row) * 8);
+}
+
+template <int KIND, int WF, int WT, int NF, int NTK, int NB>
+hipError_t launch(const LinearCall& a, int splits, hipStream_t s) {
     constexpr int TF = WF * NF * 16, TT = WT * NTK * 16;
-    const int64_t f_tiles = (a.N + TF - 1) / TF, t_tiles = ((int64_t)a.T + TT - 1) / TT;
-    if (!grid_fits(f_tiles * t_tiles, WF * WT * 64)) return hipErrorInvalidConfiguration;
-    k_linear_tiled<KIND, WF, WT, NF, NTK><<<(unsigned)(f_tiles * t_tiles), WF * WT * 64, 0, s>>>(a, (int)f_tiles, (int)t_tiles);
+    const int64_t f_tiles = (a.N + TF - 1) / TF, t_tiles = ((int64_t)a.T + TT - 1) / TT, all = f_tiles * t_tiles * splits;
+    const int64_t join = ((int64_t)a.T * (a.N / 8) + 255) / 256;
+    if (!grid_fits(all, WF * WT * 64) || !grid_fits(join, 256)) return hipErrorInvalidConfiguration;
+    k_linear_tiled<KIND, WF, WT, NF, NTK, NB><<<(unsigned)all, WF * WT * 64, 0, s>>>(a, (int)f_tiles, (int)t_tiles, splits);
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess || splits == 1) return err;
+    k_linear_join<<<(unsigned)join, 256, 0, s>>>(a, splits);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_linear_tiled(const LinearCall& a, hipStream_t s) {
-    if (a.dtype == RDG_BF16) return launch<kBf16, 2, 4, 8, 4>(a, s);
-    return a.dtype == RDG_FP8_E4M3 ? launch<kFp8, 2, 4, 8, 4>(a, s) : launch<kE8m0, 2, 4, 8, 4>(a, s);
+template <int KIND>
+static hipError_t launch_kind(const LinearCall& a, const LinearPart& p, hipStream_t s) {
+    switch (p.kernel) {
+        case kTile256:
+            // fp32 keeps two sets of sums, and products of widened operands need registers for them
+            if constexpr (KIND == kF32) return launch<KIND, 2, 4, 4, 2, 4>(a, p.splits, s);
+            else return launch<KIND, 2, 4, 8, KIND == kFp8Wide ? 2 : 4, 2>(a, p.splits, s);
+        case kTile128: return launch<KIND, 2, 4, 4, 2, 4>(a, p.splits, s);
+        case kTile128x64: return launch<KIND, 4, 2, 2, 2, 5>(a, p.splits, s);
+        default: return launch<KIND, 4, 1, 1, 2, 4>(a, p.splits, s);
+    }
+}
+
+hipError_t launch_linear_tiled(const LinearCall& a, const LinearPart& p, hipStream_t s) {
+    switch (a.dtype) {
+        case RDG_F32: return launch_kind<kF32>(a, p, s);
+        case RDG_BF16: return launch_kind<kBf16>(a, p, s);
+        case RDG_FP8_E4M3: return a.out_bf16 ? launch_kind<kFp8>(a, p, s) : launch_kind<kFp8Wide>(a, p, s);
+        default: return a.out_bf16 ? launch_kind<kE8m0>(a, p, s) : launch_kind<kFp8Wide>(a, p, s);
+    }
 }
 
 }  // namespace rdg

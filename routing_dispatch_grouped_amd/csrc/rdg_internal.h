@@ -306,7 +306,8 @@ struct LinearCall {
 };
 size_t linear_workspace_bytes(int T, int N, int K, int dtype);
 hipError_t launch_linear(const LinearCall& a, hipStream_t s);
-hipError_t launch_linear_tiled(const LinearCall& a, hipStream_t s);
+struct LinearPart;
+hipError_t launch_linear_tiled(const LinearCall& a, const LinearPart& p, hipStream_t s);
 
 struct RouteCall {
     const void* logits;
