@@ -184,144 +184,333 @@ __global__ __launch_bounds__(256) void k_route(const float* __restrict__ logits,
 // scores is larger does not depend on how a sum was ordered; c, the groups' sums
 // and the weights are fp32.
 //
-// Bound by latency and the vector unit: a row is at most 4 KiB.  A token has
-// SEG lanes (8, 16, 32 or 64, the fewest that hold its experts one each), so
-// that few experts do not leave most of a wave idle, and VPL experts a lane
-// from 65 experts on: expert e on lane e % 64.  Each of the K rounds is a maximum of
-// ordered score bits across the token's lanes in the vector unit, and a ballot
-// for the lowest expert that holds it.
+// Bound by the vector unit for many tokens: the fp64 exponentials, and the rounds in which one
+// expert after the other is taken.  Up to 32 experts a token has SEG lanes (8, 16 or 32, the fewest that
+// hold its experts one each); beyond, a wave with VPL experts a lane, expert e on lane e % 64.
+// A round is a maximum of ordered score bits across the token's lanes, in the vector unit, and a ballot for
+// the lowest expert that holds it.
 constexpr int kTopkThreads = 256;
 
-template <int SEG, int VPL>
-__global__ __launch_bounds__(kTopkThreads) void k_route_topk(RouteCall a) {
-    constexpr int PER = kTopkThreads / SEG;  // tokens a workgroup
-    static_assert(VPL == 1 || SEG == kWave, "several experts a lane only in whole waves");
-    __shared__ float choice_lds[PER][SEG * VPL];
-    __shared__ float plain_lds[PER][SEG * VPL];
-    __shared__ float rank_lds[PER][SEG * VPL];
-    const int slot = threadIdx.x / SEG, sub = threadIdx.x % SEG, first = lane_id() / SEG * SEG;
-    // past the last token: the last one again, not stored (the exchanges take every lane of the wave)
-    const int64_t at = (int64_t)blockIdx.x * PER + slot;
-    const bool live = at < a.B;
-    const int64_t t = live ? at : a.B - 1;
-    float* ch = choice_lds[slot];
-    float* pl = plain_lds[slot];
-
-    // NaN counts as -inf, +inf as the largest finite value
-    float x[VPL];
+// The logits of token t that lane `first` of STEP lanes holds, -inf past the last; NaN counts as -inf, +inf as the
+// largest finite value.  All are requested before the first is looked at.
+template <int STEP, int VPL>
+__device__ __forceinline__ void topk_logits(const RouteCall& a, int64_t t, int first, float (&x)[VPL]) {
+    uint32_t u[VPL];
+    if (a.bf16) {
+        const uint16_t* row = static_cast<const uint16_t*>(a.logits) + t * a.stride;
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-        const int e = sub + SEG * v;
-        x[v] = -__builtin_inff();
-        if (e < a.N) {
-            const int64_t i = t * a.stride + e;
-            const float l = a.bf16 ? bf16_to_f32(static_cast<const uint16_t*>(a.logits)[i]) : static_cast<const float*>(a.logits)[i];
-            x[v] = l != l ? -__builtin_inff() : fminf(l, 3.402823466e38f);
-        }
-    }
-    float p[VPL];
-    if (a.softmax) {
-        float top = x[0];
+        for (int v = 0; v < VPL; ++v) u[v] = row[first + STEP * v < a.N ? first + STEP * v : a.N - 1];
 #pragma unroll
-        for (int v = 1; v < VPL; ++v) top = fmaxf(top, x[v]);
-        top = across<SEG>(top, [](float q, float r) { return fmaxf(q, r); });
-        double e[VPL], sum = 0.0;
-#pragma unroll
-        for (int v = 0; v < VPL; ++v) {
-            // a row of nothing but -inf has no scores: all 0
-            e[v] = x[v] == -__builtin_inff() ? 0.0 : exp64(fmax((double)x[v] - (double)top, -800.0));
-            sum += e[v];
-        }
-        sum = across<SEG>(sum, [](double q, double r) { return q + r; });
-#pragma unroll
-        for (int v = 0; v < VPL; ++v) p[v] = sum > 0.0 ? (float)(e[v] / sum) : 0.0f;
+        for (int v = 0; v < VPL; ++v) u[v] <<= 16;
     } else {
+        const uint32_t* row = static_cast<const uint32_t*>(a.logits) + t * a.stride;
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) p[v] = score_sigmoid(x[v]);
+        for (int v = 0; v < VPL; ++v) u[v] = row[first + STEP * v < a.N ? first + STEP * v : a.N - 1];
     }
-
-    uint32_t key[VPL];  // 0: no candidate (any longer)
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-        const int e = sub + SEG * v;
-        float c = p[v];
-        if (a.bias != nullptr && e < a.N) {
-            c += a.bias[e];
-            if (c != c) c = -__builtin_inff();
-            pl[e] = p[v];
-        }
-        key[v] = e < a.N ? ordered_bits(c) : 0u;
-        if (a.n_group > 1 && e < a.N) ch[e] = c;
-    }
-    if (a.n_group > 1) {
-        const int gs = a.N / a.n_group;
-        float* rank = rank_lds[slot];
-        __syncthreads();
-        for (int g = sub; g < a.n_group; g += SEG) {
-            float best = -__builtin_inff(), next = best;
-            for (int i = g * gs; i < (g + 1) * gs; ++i) {
-                const float c = ch[i];
-                next = fmaxf(next, fminf(best, c));
-                best = fmaxf(best, c);
-            }
-            rank[g] = a.group_best == 2 && gs >= 2 ? best + next : best;
-        }
-        __syncthreads();
-        // kept: fewer than topk_group groups are better (larger, or as large with a lower index)
-        for (int g = sub; g < a.n_group; g += SEG) {
-            const uint32_t mine = ordered_bits(rank[g]);
-            int better = 0;
-            for (int h = 0; h < a.n_group; ++h) {
-                const uint32_t other = ordered_bits(rank[h]);
-                better += other > mine || (other == mine && h < g);
-            }
-            ch[g] = better < a.topk_group ? 1.0f : 0.0f;  // the choices are in registers
-        }
-        __syncthreads();
-#pragma unroll
-        for (int v = 0; v < VPL; ++v) {
-            const int e = sub + SEG * v;
-            if (e < a.N && ch[e / gs] == 0.0f) key[v] = 0u;
-        }
-    } else if (a.bias != nullptr) {
-        __syncthreads();
-    }
-
-    const uint64_t seg_mask = SEG == 64 ? ~0ull : ((1ull << (SEG & 63)) - 1) << first;
-    float sum = 0.0f, my_p = 0.0f;
-    int my_id = 0;
-    for (int k = 0; k < a.K; ++k) {
-        uint32_t m = key[0];
-#pragma unroll
-        for (int v = 1; v < VPL; ++v) m = key[v] > m ? key[v] : m;
-        m = across<SEG>(m, [](uint32_t q, uint32_t r) { return q > r ? q : r; });
-        int e = -1;
-#pragma unroll
-        for (int v = 0; v < VPL; ++v) {
-            const uint64_t have = __ballot(key[v] == m) & seg_mask;
-            if (e < 0 && have != 0) e = __ffsll((unsigned long long)have) - 1 - first + SEG * v;
-        }
-#pragma unroll
-        for (int v = 0; v < VPL; ++v)
-            if (sub + SEG * v == e) key[v] = 0u;
-        // without a bias the choice is the score: back from its ordered bits
-        const float pe = a.bias != nullptr ? pl[e] : __uint_as_float(m & 0x7fffffffu);
-        sum += pe;
-        if (sub == k) my_id = e, my_p = pe;
-    }
-    if (live && sub < a.K) {
-        const float w = !a.renorm ? my_p : sum > 0.0f ? my_p / sum : 0.0f;
-        a.ids[t * a.K + sub] = my_id;
-        a.w[t * a.K + sub] = w * a.scale;
+        const float l = __uint_as_float(u[v]);
+        x[v] = first + STEP * v < a.N && l == l ? fminf(l, 3.402823466e38f) : -__builtin_inff();
     }
 }
 
-template <int SEG, int VPL>
-hipError_t launch(const RouteCall& a, hipStream_t s) {
-    constexpr int PER = kTopkThreads / SEG;
-    const int64_t blocks = ((int64_t)a.B + PER - 1) / PER;
+// The scores of a token's logits, spread over LANES lanes.
+template <int LANES, int VPL>
+__device__ __forceinline__ void topk_scores(bool softmax, const float (&x)[VPL], float (&p)[VPL]) {
+    if (!softmax) {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) p[v] = score_sigmoid(x[v]);
+        return;
+    }
+    float top = x[0];
+#pragma unroll
+    for (int v = 1; v < VPL; ++v) top = fmaxf(top, x[v]);
+    top = across<LANES>(top, [](float q, float r) { return fmaxf(q, r); });
+    // a row of nothing but -inf has no scores: exp(-inf) everywhere
+    const double shift = fmaxf(top, -3.402823466e38f);
+    double e[VPL], sum = 0.0;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+        e[v] = exp64(__builtin_fmax((double)x[v] - shift, -800.0));
+        sum += e[v];
+    }
+    sum = across<LANES>(sum, [](double q, double r) { return q + r; });
+    const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) p[v] = (float)(e[v] * inv);
+}
+
+__device__ __forceinline__ uint32_t topk_key(float c) { return ordered_bits(c == c ? c : -__builtin_inff()); }
+__device__ __forceinline__ float topk_value(uint32_t key) {  // of a key that is not 0
+    return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
+// The largest of the wave's values, in a scalar register: each row of 16 shifted over itself, then row by row
+// into the last lane.
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t x) {
+    auto with = [&](uint32_t y) { x = y > x ? y : x; };
+    with(lane_of<0x111>(x));  // row_shr:1, 0 comes in
+    with(lane_of<0x112>(x));
+    with(lane_of<0x114>(x));
+    with(lane_of<0x118>(x));
+    with(lane_of<0x142>(x));  // row_bcast:15
+    with(lane_of<0x143>(x));  // row_bcast:31
+    return (uint32_t)__builtin_amdgcn_readlane((int)x, kWave - 1);
+}
+
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+__device__ __forceinline__ void topk_store(const RouteCall& a, int64_t t, int k, int id, float p, float sum) {
+    const float w = !a.renorm ? p : sum > 0.0f ? p / sum : 0.0f;
+    a.ids[t * a.K + k] = id;
+    a.w[t * a.K + k] = w * a.scale;
+}
+
+// Up to 32 experts: SEG lanes a token.
+template <int SEG>
+__global__ __launch_bounds__(kTopkThreads) void k_route_few(RouteCall a) {
+    constexpr int PER = kTopkThreads / SEG;  // tokens a workgroup
+    __shared__ float choice_lds[PER][SEG], plain_lds[PER][SEG], rank_lds[PER][SEG];
+    const int slot = threadIdx.x / SEG, sub = threadIdx.x % SEG, first = lane_id() / SEG * SEG;
+    // past the last token: the last one again, not stored (the exchanges take every lane of the wave)
+    const int64_t at = (int64_t)blockIdx.x * PER + slot;
+    const bool live = at < a.B, mine = sub < a.N;
+    const int64_t t = live ? at : a.B - 1;
+    float* pl = plain_lds[slot];
+    float x[1], p[1];
+    topk_logits<SEG>(a, t, sub, x);
+    topk_scores<SEG>(a.softmax, x, p);
+    float c = p[0];
+    if (a.bias != nullptr && mine) {
+        c += a.bias[sub];
+        pl[sub] = p[0];
+    }
+    uint32_t key = mine ? topk_key(c) : 0u;  // 0: no candidate (any longer)
+    if (a.n_group > 1) {
+        // group `sub`: its rank; kept where fewer than topk_group groups are better (larger, or as large with a lower index)
+        const int gs = a.N / a.n_group;
+        float* ch = choice_lds[slot];
+        float* rank = rank_lds[slot];
+        if (mine) ch[sub] = topk_value(key);
+        wave_lds_fence();
+        uint32_t own = 0u;
+        if (sub < a.n_group) {
+            float best = -__builtin_inff(), next = best;
+            for (int i = sub * gs; i < (sub + 1) * gs; ++i) {
+                next = fmaxf(next, fminf(best, ch[i]));
+                best = fmaxf(best, ch[i]);
+            }
+            rank[sub] = a.group_best == 2 && gs >= 2 ? best + next : best;
+            own = ordered_bits(rank[sub]);
+        }
+        wave_lds_fence();
+        int better = 0;
+        for (int h = 0; h < a.n_group; ++h) {
+            const uint32_t other = ordered_bits(rank[h]);
+            better += other > own || (other == own && h < sub);
+        }
+        const uint64_t kept = __ballot(better < a.topk_group && sub < a.n_group);
+        if (mine && !(kept >> (first + sub / gs) & 1)) key = 0u;
+    }
+    wave_lds_fence();
+    const uint64_t seg_mask = ((1ull << SEG) - 1) << first;
+    float sum = 0.0f, my_p = 0.0f;
+    int my_id = 0;
+    for (int k = 0; k < a.K; ++k) {
+        const uint32_t m = across<SEG>(key, [](uint32_t q, uint32_t r) { return q > r ? q : r; });
+        const int e = __ffsll((unsigned long long)(__ballot(key == m) & seg_mask)) - 1 - first;
+        if (sub == e) key = 0u;
+        const float pe = a.bias != nullptr ? pl[e] : topk_value(m);
+        sum += pe;
+        if (sub == k) my_id = e, my_p = pe;
+    }
+    if (live && sub < a.K) topk_store(a, t, sub, my_id, my_p, sum);
+}
+
+// More experts: a wave a token.
+template <int VPL>
+__global__ __launch_bounds__(kTopkThreads) void k_route_wave(RouteCall a) {
+    constexpr int WAVES = kTopkThreads / kWave;
+    // lanes that hold their experts in descending order offer one at a time; for more than 4 that costs more than it saves
+    constexpr bool SORTED = VPL <= 4;
+    __shared__ float choice_lds[WAVES][kWave * VPL], plain_lds[WAVES][kWave * VPL];
+    __shared__ uint2 chosen_lds[WAVES][32];
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
+    const int64_t t = (int64_t)blockIdx.x * WAVES + wv;
+    if (t >= a.B) return;  // nothing below synchronises across waves
+    float* pl = plain_lds[wv];
+    float x[VPL], p[VPL];
+    topk_logits<kWave>(a, t, lane, x);
+    topk_scores<kWave>(a.softmax, x, p);
+    uint32_t key[VPL];  // 0: no candidate (any longer)
+    if (a.bias != nullptr) {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            const int e = lane + kWave * v;
+            key[v] = topk_key(p[v] + a.bias[e < a.N ? e : a.N - 1]);
+            pl[e] = p[v];
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) key[v] = topk_key(p[v]);
+    }
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) key[v] = lane + kWave * v < a.N ? key[v] : 0u;
+    if (a.n_group > 1) {
+        float* ch = choice_lds[wv];
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) ch[lane + kWave * v] = topk_value(key[v]);
+        wave_lds_fence();
+        const int gs = a.N / a.n_group;
+        // e / gs: e + 1/2 is at least gs / 2 parts in 1024 gs from a multiple of gs, more than fp32 loses
+        const float per_gs = 1.0f / gs;
+        auto group_of = [&](int e) { return (int)((e + 0.5f) * per_gs); };
+        auto merge = [](float& best, float& next, float b2, float n2) {
+            next = fmaxf(fmaxf(next, n2), fminf(best, b2));
+            best = fmaxf(best, b2);
+        };
+        if (a.n_group <= 8) {
+            // eight lanes a group
+            const int g = lane / 8;
+            float best = -__builtin_inff(), next = best;
+            if (g < a.n_group)
+                for (int i = g * gs + lane % 8; i < (g + 1) * gs; i += 8) merge(best, next, ch[i], -__builtin_inff());
+            merge(best, next, lane_of<kSwap1>(best), lane_of<kSwap1>(next));
+            merge(best, next, lane_of<kSwap2>(best), lane_of<kSwap2>(next));
+            merge(best, next, lane_of<kMirror8>(best), lane_of<kMirror8>(next));
+            const uint32_t own = ordered_bits(a.group_best == 2 && gs >= 2 ? best + next : best);
+            int better = 0;
+            for (int h = 0; h < a.n_group; ++h) {
+                const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)own, h * 8);
+                better += other > own || (other == own && h < g);
+            }
+            const uint64_t kept = __ballot(better < a.topk_group);
+#pragma unroll
+            for (int v = 0; v < VPL; ++v)
+                if (!(kept >> (group_of(lane + kWave * v) * 8 & 63) & 1)) key[v] = 0u;
+        } else {
+            // a lane a group; the choices are in registers, so their ranks and then who is kept take their place
+            float rank[VPL];
+#pragma unroll
+            for (int v = 0; v < VPL; ++v) {
+                const int g = lane + kWave * v;
+                float best = -__builtin_inff(), next = best;
+                if (g < a.n_group)
+                    for (int i = g * gs; i < (g + 1) * gs; ++i) merge(best, next, ch[i], -__builtin_inff());
+                rank[v] = a.group_best == 2 && gs >= 2 ? best + next : best;
+            }
+            wave_lds_fence();
+#pragma unroll
+            for (int v = 0; v < VPL; ++v)
+                if (lane + kWave * v < a.n_group) ch[lane + kWave * v] = rank[v];
+            wave_lds_fence();
+            int better[VPL];
+#pragma unroll
+            for (int v = 0; v < VPL; ++v) better[v] = 0;
+            for (int h = 0; h < a.n_group; ++h) {
+                const uint32_t other = ordered_bits(ch[h]);
+#pragma unroll
+                for (int v = 0; v < VPL; ++v) {
+                    const uint32_t own = ordered_bits(rank[v]);
+                    better[v] += other > own || (other == own && h < lane + kWave * v);
+                }
+            }
+            wave_lds_fence();
+#pragma unroll
+            for (int v = 0; v < VPL; ++v)
+                if (lane + kWave * v < a.n_group) ch[lane + kWave * v] = better[v] < a.topk_group ? 1.0f : 0.0f;
+            wave_lds_fence();
+#pragma unroll
+            for (int v = 0; v < VPL; ++v) {
+                const int e = lane + kWave * v;
+                if (e < a.N && ch[group_of(e)] == 0.0f) key[v] = 0u;
+            }
+        }
+    }
+    wave_lds_fence();
+
+    uint32_t slots = 0;  // SORTED: which of the lane's experts key[0], key[1], .. belong to, a byte each
+    if constexpr (SORTED) {
+        uint32_t s[VPL];
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) s[v] = v;
+        auto order = [&](int i) {  // neighbours, as large ones staying: the lower expert first
+            const bool swap = key[i + 1] > key[i];
+            const uint32_t k = key[i], q = s[i];
+            key[i] = swap ? key[i + 1] : k, key[i + 1] = swap ? k : key[i + 1];
+            s[i] = swap ? s[i + 1] : q, s[i + 1] = swap ? q : s[i + 1];
+        };
+#pragma unroll
+        for (int n = VPL - 1; n > 0; --n)
+#pragma unroll
+            for (int i = 0; i < n; ++i) order(i);
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) slots |= s[v] << (8 * v);
+    }
+    uint2* chosen = chosen_lds[wv];  // expert and key
+    float sum = 0.0f;
+    for (int k = 0; k < a.K; ++k) {
+        uint32_t m = key[0];
+        if constexpr (!SORTED) {
+#pragma unroll
+            for (int v = 1; v < VPL; ++v) m = key[v] > m ? key[v] : m;
+        }
+        m = wave_max_u32(m);
+        // the lowest expert that holds m; the lane that holds it notes it and goes on to its next
+        if constexpr (SORTED) {
+            bool mine = key[0] == m;
+            const uint64_t have = __ballot(mine);
+            if (have & (have - 1)) {  // a tie of several lanes
+                int e = kWave * VPL;
+                for (uint64_t h = have; h != 0; h &= h - 1) {
+                    const int l = __builtin_ctzll(h), at = (__builtin_amdgcn_readlane((int)slots, l) & 255) * kWave + l;
+                    e = at < e ? at : e;
+                }
+                mine = lane == e % kWave;
+            }
+            if (mine) {
+                chosen[k] = make_uint2((slots & 255) * kWave + lane, m);
+#pragma unroll
+                for (int v = 0; v + 1 < VPL; ++v) key[v] = key[v + 1];
+                key[VPL - 1] = 0u;
+                slots >>= 8;
+            }
+        } else {
+            int e = 0;
+#pragma unroll
+            for (int v = VPL - 1; v >= 0; --v) {
+                const uint64_t have = __ballot(key[v] == m);
+                if (have != 0) e = __builtin_ctzll(have) + kWave * v;
+            }
+            if (lane == 0) chosen[k] = make_uint2(e, m);
+#pragma unroll
+            for (int v = 0; v < VPL; ++v) key[v] = lane + kWave * v == e ? 0u : key[v];
+        }
+        sum += topk_value(m);
+    }
+    wave_lds_fence();
+    if (lane < a.K) {
+        const uint2 own = chosen[lane];
+        float p_own = topk_value(own.y);  // without a bias the choice is the score
+        if (a.bias != nullptr) {
+            p_own = pl[own.x];
+            sum = 0.0f;
+            if (a.renorm)
+                for (int k = 0; k < a.K; ++k) sum += pl[chosen[k].x];
+        }
+        topk_store(a, t, lane, (int)own.x, p_own, sum);
+    }
+}
+
+template <class Kernel>
+hipError_t launch_topk(Kernel kernel, int tokens, const RouteCall& a, hipStream_t s) {
+    const int64_t blocks = ((int64_t)a.B + tokens - 1) / tokens;
     if (!grid_fits(blocks, kTopkThreads)) return hipErrorInvalidConfiguration;
-    k_route_topk<SEG, VPL><<<(unsigned)blocks, kTopkThreads, 0, s>>>(a);
+    kernel<<<(unsigned)blocks, kTopkThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -342,15 +531,16 @@ hipError_t launch_route(const float* logits, const float* bias, int B, int N, in
 
 hipError_t launch_route_topk(const RouteCall& a, hipStream_t s) {
     if (a.B == 0) return hipSuccess;
-    // a lane holds the K-th choice until the end, so the lanes are no fewer than K (K <= N)
-    if (a.N <= 8) return launch<8, 1>(a, s);
-    if (a.N <= 16) return launch<16, 1>(a, s);
-    if (a.N <= 32) return launch<32, 1>(a, s);
-    if (a.N <= 64) return launch<64, 1>(a, s);
-    if (a.N <= 128) return launch<64, 2>(a, s);
-    if (a.N <= 256) return launch<64, 4>(a, s);
-    if (a.N <= 512) return launch<64, 8>(a, s);
-    return launch<64, 16>(a, s);
+    // lane k holds the k-th choice until the end: the lanes are no fewer than K (K <= N)
+    if (a.N <= 8) return launch_topk(k_route_few<8>, kTopkThreads / 8, a, s);
+    if (a.N <= 16) return launch_topk(k_route_few<16>, kTopkThreads / 16, a, s);
+    if (a.N <= 32) return launch_topk(k_route_few<32>, kTopkThreads / 32, a, s);
+    if (a.N <= 64) return launch_topk(k_route_wave<1>, kTopkThreads / kWave, a, s);
+    if (a.N <= 128) return launch_topk(k_route_wave<2>, kTopkThreads / kWave, a, s);
+    if (a.N <= 192) return launch_topk(k_route_wave<3>, kTopkThreads / kWave, a, s);
+    if (a.N <= 256) return launch_topk(k_route_wave<4>, kTopkThreads / kWave, a, s);
+    if (a.N <= 512) return launch_topk(k_route_wave<8>, kTopkThreads / kWave, a, s);
+    return launch_topk(k_route_wave<16>, kTopkThreads / kWave, a, s);
 }
 
 }  // namespace rdg

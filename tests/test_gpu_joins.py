@@ -230,6 +230,26 @@ def test_linear_of_whole_numbers_is_exact(T, N, K, kind):
     assert np.array_equal(f64(out), c["xv"] @ c["wv"].T)
 
 
+# every tile, with and without splits, whole rounds of 256 x 256 tiles with others behind them, an odd number of stages
+LARGE = [(2300, 9232, 640), (4000, 5136, 256), (2048, 9216, 384), (700, 4112, 2048), (1100, 2064, 4096), (129, 7184, 3968),
+         (64, 7184, 7168), (1000, 272, 16384), (300, 4112, 512), (500, 12304, 1152), (4097, 4112, 128), (100, 18432, 2048),
+         (260, 784, 7168), (900, 1040, 14336)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "fp8", "e8m0"])
+@pytest.mark.parametrize("T,N,K", LARGE)
+def test_linear_of_whole_numbers_at_larger_sizes(T, N, K, kind):
+    c = linear_case(T, N, K, kind, True, gap=16)
+    x, w = (torch.from_numpy(c[v]).to(DEV) for v in ("xv", "wv"))
+    want = x @ w.T                             # float64
+    assert torch.equal(run_linear(c, F32, gap=4).double(), want)
+    if kind != "f32":                          # the kernels of 16-bit outputs, with the whole epilogue
+        bias, res = torch.arange(N, device=DEV).float() - N // 2, spaced(T, N, BF, 8)
+        res.copy_(torch.randint(-9, 10, (T, N), device=DEV, generator=c["g"]))
+        got = run_linear(c, BF, "relu", bias, res, gap=8)
+        assert torch.equal(got, ((want + bias).clamp(min=0) + res.double()).float().to(BF))
+
+
 @pytest.mark.parametrize("kind,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32"), ("fp8", "bf16"), ("fp8", "f32"),
                                       ("e8m0", "bf16"), ("e8m0", "f32")])
 @pytest.mark.parametrize("T,N,K,act,bias,res", [
