@@ -46,8 +46,8 @@ class rdg_kv_step(ctypes.Structure):
                 ("status", ctypes.c_void_p), ("work", ctypes.c_void_p)]
 
 
-if not os.path.exists(LIB_PATH):
-    raise ImportError("librdg.so is not built (run routing_dispatch_grouped_amd/_build.py or "
+if not (os.path.exists(LIB_PATH) and os.path.exists(os.path.join(_HERE, "_binding.so"))):
+    raise ImportError("librdg.so or _binding.so is not built (run routing_dispatch_grouped_amd/_build.py or "
                       "__graft_entry__.build()); there is no fallback implementation")
 
 _lib = ctypes.CDLL(LIB_PATH)
@@ -120,20 +120,16 @@ def _check(rc, what):
         raise RdgError(rc, what)
 
 
-# torch and its current-stream lookup, bound at the first call: the small calls
-# of a decode step take as long on the host as on the GPU.
-_torch = _stream_of = _device_of = None
-_float_codes, _linear_types = {}, {}  # element types by torch's, and torch's of an rdg_linear operand
+# torch, its current-stream lookup and the part of the binding that is in C++ (it needs torch loaded), bound at the first
+# call: the small calls of a decode step take as long on the host as on the GPU.
+_torch = _stream_of = _device_of = _cpp = None
 
 
 def _bind_torch():
-    global _torch, _stream_of, _device_of
+    global _torch, _stream_of, _device_of, _cpp
     import torch
-    _stream_of, _device_of = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-    _float_codes.update({torch.bfloat16: RDG_BF16, torch.float32: RDG_F32})
-    codes = (torch.uint8, torch.float8_e4m3fn)
-    _linear_types.update({RDG_F32: (torch.float32,), RDG_BF16: (torch.bfloat16,), RDG_FP8_E4M3: codes,
-                          RDG_FP8_E4M3_UE8M0: codes})
+    from . import _binding
+    _stream_of, _device_of, _cpp = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, _binding
     _torch = torch
     return torch
 
@@ -481,69 +477,23 @@ def rdg_paged_attention(q, step, cache, max_q, max_kv, scale, out, lse=None, wor
                                     _raw_stream(stream)), "rdg_paged_attention")
 
 
-def _refuse(call, what, t, want):
-    raise RdgError(RDG_EINVAL, "%s: %s: want %s, got %s %s with strides %s on %s" %
-                   (call, what, want, t.dtype, list(t.shape), list(t.stride()), t.device))
-
-
-def _matrix(call, what, t, shape, device):
-    """(address, dtype code, row stride) of bfloat16 or float32 rows of this shape, which may be apart, on this device."""
-    code = _float_codes.get(t.dtype)
-    if code is None or t.shape != shape:
-        _refuse(call, what, t, "bfloat16 or float32 rows %s" % list(shape))
-    if t.is_contiguous():
-        stride = shape[1]
-    else:
-        stride, inner = t.stride()
-        if inner != 1 and shape[1] > 1:
-            _refuse(call, what, t, "rows without gaps in them")
-        if shape[0] == 1:
-            stride = shape[1]
-    if t.get_device() != device:
-        _refuse(call, what, t, "the current device, %d" % device)
-    return t.data_ptr(), code, stride
-
-
-def _flat(call, what, t, dtype, n, device):
-    """The address of a contiguous tensor of n elements on this device."""
-    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
-        _refuse(call, what, t, "%d contiguous elements of %s" % (n, dtype))
-    if t.get_device() != device:
-        _refuse(call, what, t, "the current device, %d" % device)
-    return t.data_ptr()
+def _answer(call, r):
+    """Raises what a function of _binding answered: the C call's error code, or the text of a refusal."""
+    if isinstance(r, str):
+        raise RdgError(RDG_EINVAL, "%s: %s" % (call, r))
+    raise RdgError(r, call)
 
 
 def rdg_add_norm(x, weight, eps, out=None, residual=None, residual_out=None, q=None, q_scales=None,
                  q_dtype=RDG_FP8_E4M3, stream=None):
     """x, out [T, H], residual, residual_out [T, H] of one type (row strides free), weight [H] float32 or None,
     q [T, H] uint8 and q_scales [T, H/128] float32."""
-    torch = _torch or _bind_torch()
-    call, shape, device = "rdg_add_norm", x.shape, _device_of()
-    if len(shape) != 2:
-        _refuse(call, "x", x, "[T, H]")
-    T, H = shape
-    x_ptr, dt, x_stride = _matrix(call, "x", x, shape, device)
-    res_ptr = res_out_ptr = out_ptr = q_ptr = qs_ptr = w_ptr = None
-    res_dt, res_stride, out_stride = dt, 0, 0
-    if residual is not None:
-        res_ptr, res_dt, res_stride = _matrix(call, "residual", residual, shape, device)
-    if residual_out is not None:
-        res_out_ptr, o_dt, o_stride = _matrix(call, "residual_out", residual_out, shape, device)
-        if residual is None or o_dt != res_dt or o_stride != res_stride:
-            _refuse(call, "residual_out", residual_out, "the type and strides of residual")
-    if out is not None:
-        out_ptr, o_dt, out_stride = _matrix(call, "out", out, shape, device)
-        if o_dt != dt:
-            _refuse(call, "out", out, "the type of x")
-    if weight is not None:
-        w_ptr = _flat(call, "weight", weight, torch.float32, H, device)
-    if q is not None:
-        q_ptr = _flat(call, "q", q, torch.uint8, T * H, device)
-        qs_ptr = _flat(call, "q_scales", q_scales, torch.float32, T * (H // 128), device)
-    rc = _lib.rdg_add_norm(x_ptr, dt, x_stride, T, H, res_ptr, res_out_ptr, res_dt, res_stride, w_ptr, eps, out_ptr,
-                           out_stride, q_ptr, qs_ptr, q_dtype, _stream_of(device) if stream is None else stream.cuda_stream)
-    if rc:
-        raise RdgError(rc, call)
+    if _cpp is None:
+        _bind_torch()
+    r = _cpp.add_norm(x, weight, eps, out, residual, residual_out, q, q_scales, q_dtype, _device_of(),
+                      _stream_of if stream is None else stream.cuda_stream)
+    if r is not None:
+        _answer("rdg_add_norm", r)
 
 
 def rdg_linear_workspace_bytes(T, N, K, dtype):
@@ -554,65 +504,24 @@ def rdg_linear(x, x_scales, dtype, W, W_scales, out, bias=None, act=RDG_ACT_NONE
     """x [T, K] (row stride free; fp8 codes as uint8 or float8_e4m3fn) with x_scales [T, K/128] float32, W [N, K] packed
     with W_scales [ceil(N/128), K/128], out, residual [T, N] bfloat16 or float32 (row strides free), bias [N] float32;
     work: a uint8 tensor of rdg_linear_workspace_bytes."""
-    torch = _torch or _bind_torch()
-    call, device, shape, out_shape = "rdg_linear", _device_of(), x.shape, out.shape
-    if len(shape) != 2 or len(out_shape) != 2 or out_shape[0] != shape[0]:
-        _refuse(call, "x", x, "[T, K], with out [T, N]")
-    T, K = shape
-    N = out_shape[1]
-    kinds = _linear_types.get(dtype, ())
-    if x.dtype not in kinds or W.dtype not in kinds or W.numel() != N * K or not W.is_contiguous():
-        _refuse(call, "W", W, "x and W of one of %s, W %d x %d packed" % (list(kinds), N, K))
-    if x.is_contiguous():
-        x_stride = K
-    else:
-        x_stride, inner = x.stride()
-        if inner != 1:
-            _refuse(call, "x", x, "rows without gaps in them")
-        if T == 1:
-            x_stride = K
-    if x.get_device() != device or W.get_device() != device:
-        _refuse(call, "x and W", x, "the current device, %d" % device)
-    out_ptr, out_dt, out_stride = _matrix(call, "out", out, out_shape, device)
-    xs_ptr = ws_ptr = bias_ptr = res_ptr = work_ptr = None
-    res_stride = work_bytes = 0
-    if len(kinds) > 1:
-        xs_ptr = _flat(call, "x_scales", x_scales, torch.float32, T * (K // 128), device)
-        ws_ptr = _flat(call, "W_scales", W_scales, torch.float32, (N + 127) // 128 * (K // 128), device)
-    if bias is not None:
-        bias_ptr = _flat(call, "bias", bias, torch.float32, N, device)
-    if residual is not None:
-        res_ptr, res_dt, res_stride = _matrix(call, "residual", residual, out_shape, device)
-        if res_dt != out_dt:
-            _refuse(call, "residual", residual, "the type of out")
-    if work is not None:
-        work_bytes = work.nbytes
-        if work_bytes:
-            work_ptr = _flat(call, "work", work, torch.uint8, work_bytes, device)
-    rc = _lib.rdg_linear(x.data_ptr(), xs_ptr, dtype, x_stride, T, N, K, W.data_ptr(), ws_ptr, bias_ptr, act, res_ptr,
-                         res_stride, out_ptr, out_dt, out_stride, work_ptr, work_bytes,
-                         _stream_of(device) if stream is None else stream.cuda_stream)
-    if rc:
-        raise RdgError(rc, call)
+    if _cpp is None:
+        _bind_torch()
+    r = _cpp.linear(x, x_scales, dtype, W, W_scales, out, bias, act, residual, work, _device_of(),
+                    _stream_of if stream is None else stream.cuda_stream)
+    if r is not None:
+        _answer("rdg_linear", r)
 
 
 def rdg_route_topk(logits, score, n_group, topk_group, group_best, K, renorm, scale, topk_ids, topk_w, bias=None,
                    stream=None):
     """logits [B, N] bfloat16 or float32 (row stride free), topk_ids [B, K] int32, topk_w [B, K] float32, bias [N] float32
     or None."""
-    torch = _torch or _bind_torch()
-    call, device, shape = "rdg_route_topk", _device_of(), logits.shape
-    if len(shape) != 2:
-        _refuse(call, "logits", logits, "[B, N]")
-    B, N = shape
-    l_ptr, dt, stride = _matrix(call, "logits", logits, shape, device)
-    b_ptr = None if bias is None else _flat(call, "bias", bias, torch.float32, N, device)
-    rc = _lib.rdg_route_topk(l_ptr, dt, stride, B, N, score, b_ptr, n_group, topk_group, group_best, K, 1 if renorm else 0,
-                             scale, _flat(call, "topk_ids", topk_ids, torch.int32, B * K, device),
-                             _flat(call, "topk_w", topk_w, torch.float32, B * K, device),
-                             _stream_of(device) if stream is None else stream.cuda_stream)
-    if rc:
-        raise RdgError(rc, call)
+    if _cpp is None:
+        _bind_torch()
+    r = _cpp.route_topk(logits, score, n_group, topk_group, group_best, K, 1 if renorm else 0, scale, topk_ids, topk_w,
+                        bias, _device_of(), _stream_of if stream is None else stream.cuda_stream)
+    if r is not None:
+        _answer("rdg_route_topk", r)
 
 
 def rdg_check_status(layout_or_status, stream=None):

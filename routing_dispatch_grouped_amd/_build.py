@@ -1,14 +1,17 @@
-"""Build librdg.so (HIP, gfx950) in-tree with hipcc."""
+"""Build librdg.so (HIP, gfx950) in-tree with hipcc, and _binding.so, the part of the Python binding that is in C++."""
 import concurrent.futures
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "librdg.so")
+BINDING = os.path.join(PKG, "_binding.so")
 BUILD = os.path.join(PKG, "_build")
 
 SOURCES = ["abi.hip", "route.hip", "dispatch.hip", "quant.hip", "pack.hip", "ffn.hip", "ffn_tiled.hip", "combine.hip",
@@ -43,16 +46,47 @@ def _compile(src):
     return obj
 
 
+def _compile_binding():
+    """binding.cpp against torch's headers, found without importing torch."""
+    obj = os.path.join(BUILD, "binding.o")
+    include = os.path.join(_torch(), "include")
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", INCLUDE, "-isystem", include, "-isystem",
+           os.path.join(include, "torch", "csrc", "api", "include"), "-isystem", sysconfig.get_paths()["include"],
+           "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("compile failed for binding.cpp:\n%s\n%s" % (" ".join(cmd), r.stderr))
+    return obj
+
+
+def _torch():
+    return importlib.util.find_spec("torch").submodule_search_locations[0]
+
+
+def _link_binding(obj):
+    """Next to librdg.so, which it finds by its own folder; torch's libraries are those that the process has loaded."""
+    tmp = BINDING + ".tmp"
+    cmd = [CXX, "-shared", "-o", tmp, obj, "-L", PKG, "-l:librdg.so", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(_torch(), "lib"),
+           "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("link failed for _binding.so:\n%s" % r.stderr)
+    os.replace(tmp, BINDING)
+
+
 def build(verbose=False):
     os.makedirs(BUILD, exist_ok=True)
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, SOURCES))
+        binding = binding.result()
     tmp = OUT + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s" % r.stderr)
     os.replace(tmp, OUT)
+    _link_binding(binding)
     if verbose:
         print("built", OUT)
     return OUT

@@ -148,3 +148,27 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
         rdg.rdg_linear(x, None, rdg.RDG_BF16, torch.empty(16, 256, dtype=torch.bfloat16), None, torch.empty(4, 16))
     with pytest.raises(rdg.RdgError, match="device"):
         rdg.rdg_route_topk(x, 0, 1, 1, 1, 2, 1, 1.0, torch.empty(4, 2, dtype=torch.int32), torch.empty(4, 2))
+
+
+def test_what_is_no_tensor_is_refused(monkeypatch):
+    import torch
+    rdg = _rdg()
+    rdg._bind_torch()
+    monkeypatch.setattr(rdg, "_device_of", lambda: -1)
+    x, f32 = torch.empty(4, 256), torch.float32
+    many = torch.empty(1, 256).expand(1 << 31, 256)   # one row more than 32 bits count
+    for call in (lambda: rdg.rdg_add_norm(None, None, 1e-6, out=x),
+                 lambda: rdg.rdg_add_norm(x, None, 1e-6, out=x.numpy()),
+                 lambda: rdg.rdg_add_norm(x, None, "eps", out=x),
+                 lambda: rdg.rdg_add_norm(x, None, 1e-6, q=torch.empty(4, 256, dtype=torch.uint8)),
+                 lambda: rdg.rdg_add_norm(many, None, 1e-6, out=many),
+                 lambda: rdg.rdg_linear(x, None, 9, x, None, x),
+                 lambda: rdg.rdg_linear(x, None, rdg.RDG_F32, x.to_sparse(), None, torch.empty(4, 4)),
+                 lambda: rdg.rdg_linear(x, None, rdg.RDG_F32, x, None, torch.empty(4, 4), act=None),
+                 lambda: rdg.rdg_linear(x, None, rdg.RDG_F32, x, None, torch.empty(4, 4), act=1 << 40),
+                 lambda: rdg.rdg_route_topk(many, 0, 1, 1, 1, 2, 1, 1.0, x.int(), x),
+                 lambda: rdg.rdg_route_topk(x, 0, 1, 1, 1, -1, 1, 1.0, torch.empty(4, 2, dtype=torch.int32),
+                                            torch.empty(4, 2, dtype=f32))):
+        with pytest.raises(rdg.RdgError) as err:
+            call()
+        assert err.value.code == rdg.RDG_EINVAL
