@@ -90,13 +90,20 @@ hipError_t launch_rows(const LinearCall& a, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------- which kernel
-// The expected time of each kernel and split in us, and the least of them.  Constants measured over 193 sizes a type
-// (8 .. 5000 tokens, 64 .. 12288 features, K of 256 .. 14336, weights from memory); the choice takes on
-// average 2% longer than the best of all at each size, 1.45 times at worst (8 tokens, 12288 features, K = 256, fp8).
+// The expected time of each kernel and split in us, and the least of them.  Constants measured over 499 sizes each of
+// bf16 and of fp8 (1 .. 5000 tokens, 64 .. 32768 features, K of 256 .. 14336, weights from memory); the choice takes on
+// average 0.6% longer than the best of all at each size, 1.3 times at worst (16 tokens, 7168 features, K = 2048, bf16: 9.8 us).
 constexpr int kCus = 256;
 constexpr float kStart = 2.0f, kMore = 1.5f;            // launch, first loads, last stores; one launch more
-constexpr float kRowsRead = 6.1e6f, kTilesRead = 5.5e6f;  // bytes/us at which weights come from memory
+constexpr float kRowsRead = 7.6e6f, kTilesRead = 7.1e6f;  // bytes/us at which weights come from memory
 constexpr float kJoin = 2.4f, kJoinRate = 3.6e6f;       // the join's launch; splits' sums, written and read
+// With few tokens a stage takes the time in which a CU gets its 128-byte lines: it has some 500 of them under way at
+// a time, for a latency that grows with the weights under way on the whole chip.  So the tile is best whose workgroups
+// just fill the CUs: 64 tokens, 18432 features, K = 7168 in bf16, of 128 features on 144 CUs 60.4 us, of 80 on 231
+// 49.6; 16384 features in e8m0, of 128 35.4 us, of 64 28.3.
+constexpr int kFewTokens = 160;
+constexpr float kLine = 0.00168f, kUnderWay = 8.0e-6f;  // us a line; us a feature of the tile and workgroup of the chip
+constexpr float kFewFp8 = 0.045f;                       // the scales' lines
 
 struct TileCost {
     int kernel, features, tokens;
@@ -106,37 +113,46 @@ struct TileCost {
 };
 // 256 x 256 is bound by the matrix core; the smaller the tile, the more bytes it loads for its products, and the less
 // of the chip a small problem leaves idle.
-constexpr TileCost kBf16Cost[4] = {{kTile256, 256, 256, 1, 1.2f, 1.4f, 6.0f},
-                                   {kTile128, 128, 128, 1, 0.383f, 0.5f, 1.8f},
-                                   {kTile128x64, 128, 64, 1, 0.282f, 0.36f, 1.2f},
-                                   {kTile64x32, 64, 32, 3, 0.138f, 0.135f, 0.8f}};
-constexpr TileCost kFp8Cost[4] = {{kTile256, 256, 256, 1, 1.3f, 1.5f, 7.0f},
-                                  {kTile128, 128, 128, 1, 0.515f, 0.63f, 2.2f},
-                                  {kTile128x64, 128, 64, 1, 0.36f, 0.40f, 1.8f},
-                                  {kTile64x32, 64, 32, 3, 0.225f, 0.176f, 0.85f}};
-constexpr TileCost kF32Cost[4] = {{kTile128, 128, 128, 1, 1.92f, 1.92f, 2.0f},
-                                  {kTile128x64, 128, 64, 1, 1.08f, 1.08f, 1.3f},
-                                  {kTile64x32, 64, 32, 3, 0.444f, 0.30f, 0.8f},
-                                  {kRows, 0, 0, 0, 0, 0, 0}};
+constexpr TileCost kBf16Cost[] = {{kTile256, 256, 256, 1, 1.2f, 1.4f, 6.0f},      {kTile128, 128, 128, 1, 0.383f, 0.5f, 1.9f},
+                                  {kTile128x64, 128, 64, 1, 0.275f, 0.36f, 1.75f}, {kTile64x32, 64, 32, 3, 0.153f, 0.135f, 0.93f},
+                                  {kTile96x64, 96, 64, 1, 0.23f, 0.34f, 1.2f},    {kTile80x64, 80, 64, 1, 0.21f, 0.27f, 1.2f},
+                                  {kTile64x64, 64, 64, 1, 0.199f, 0.22f, 1.35f}};
+constexpr TileCost kFp8Cost[] = {{kTile256, 256, 256, 1, 1.3f, 1.5f, 7.0f},       {kTile128, 128, 128, 1, 0.596f, 0.63f, 2.25f},
+                                 {kTile128x64, 128, 64, 1, 0.417f, 0.40f, 1.65f}, {kTile64x32, 64, 32, 3, 0.23f, 0.178f, 0.99f},
+                                 {kTile96x64, 96, 64, 1, 0.40f, 0.45f, 1.6f},     {kTile80x64, 80, 64, 1, 0.39f, 0.40f, 1.6f},
+                                 {kTile64x64, 64, 64, 1, 0.373f, 0.34f, 1.65f}};
+constexpr TileCost kF32Cost[] = {{kTile128, 128, 128, 1, 1.92f, 1.92f, 2.0f},
+                                 {kTile128x64, 128, 64, 1, 1.08f, 1.08f, 1.3f},
+                                 {kTile64x32, 64, 32, 3, 0.444f, 0.30f, 0.8f}};
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int size_of(int dtype) { return dtype == RDG_F32 ? 4 : dtype == RDG_BF16 ? 2 : 1; }
 
-// A wave's 2048 elements (16 waves of 128) take a time that grows with the tokens of its tile.
+// A wave's 2048 elements (16 waves of 128) take a time that grows with the tokens of its tile; or the weights' reading and
+// a round's start.
 float rows_us(int T, int N, int K, int dtype) {
-    const float per = dtype == RDG_F32 ? 5.0f : dtype == RDG_BF16 ? 1.25f : 0.45f;
-    const float token = dtype == RDG_F32 ? 0.6f : dtype == RDG_BF16 ? 0.097f : 0.085f;
-    const float us = K / 2048.0f * (per + token * (T < 16 ? T : 16)) * ceil_div((int64_t)(N / 16) * ceil_div(T, 16), kCus);
-    const float read_us = (float)N * K * size_of(dtype) / kRowsRead;
+    const float per = dtype == RDG_F32 ? 5.0f : dtype == RDG_BF16 ? 1.06f : 0.45f;
+    const float token = dtype == RDG_F32 ? 0.6f : dtype == RDG_BF16 ? 0.097f : 0.074f;
+    const int64_t rounds = ceil_div((int64_t)(N / 16) * ceil_div(T, 16), kCus);
+    const float us = K / 2048.0f * (per + token * (T < 16 ? T : 16)) * rounds;
+    const float read_us = (float)N * K * size_of(dtype) / kRowsRead + 0.43f * rounds;
     return kStart + 0.3f + (us > read_us ? us : read_us);
 }
 
 float tiles_us(const TileCost& c, int splits, int T, int N, int K, int dtype) {
     const int stages = (int)ceil_div(K / 128, splits) * size_of(dtype);
-    const int64_t rounds = ceil_div(ceil_div(N, c.features) * ceil_div(T, c.tokens) * splits, kCus);
+    const int64_t f_jobs = ceil_div(N, c.features) * splits, rounds = ceil_div(f_jobs * ceil_div(T, c.tokens), kCus);
     const int64_t full = rounds / c.per_cu, rest = rounds % c.per_cu;
     auto round_us = [&](int64_t workgroups) {
-        const float loaded = c.loaded * workgroups, stage = rounds == 1 || loaded < c.alone ? c.alone : loaded;
+        const float loaded = c.loaded * workgroups;
+        float stage = rounds == 1 || loaded < c.alone ? c.alone : loaded;
+        if (T <= kFewTokens && dtype != RDG_F32) {
+            // (a token past the last costs half a line)
+            const float lines = workgroups * (c.features + (c.tokens + (T < c.tokens ? T : c.tokens)) * 0.5f);
+            const int64_t chip = kCus * workgroups;
+            const float few = lines * kLine + kUnderWay * c.features * (f_jobs < chip ? f_jobs : chip) + (dtype == RDG_BF16 ? 0.0f : kFewFp8);
+            stage = stage > few ? stage : few;
+        }
         return stages * stage + c.tile;
     };
     const float us = full * round_us(c.per_cu) + (rest ? round_us(rest) : 0.0f);
@@ -147,10 +163,11 @@ float tiles_us(const TileCost& c, int splits, int T, int N, int K, int dtype) {
 // One kernel for all features.
 LinearPart plan_part(int T, int N, int K, int dtype, float& least) {
     const TileCost* cost = dtype == RDG_F32 ? kF32Cost : dtype == RDG_BF16 ? kBf16Cost : kFp8Cost;
+    const int kinds = dtype == RDG_F32 ? 3 : 7;
     LinearPart best{kRows, 1, N};
     // (beyond 32 tokens the tiles are always faster)
     least = T <= 32 ? rows_us(T, N, K, dtype) : 3e38f;
-    for (int i = 0; i < 4 && cost[i].kernel != kRows; ++i) {
+    for (int i = 0; i < kinds; ++i) {
         const int64_t tiles = ceil_div(N, cost[i].features) * ceil_div(T, cost[i].tokens);
         for (int splits = 1; splits <= 8 && splits <= K / 128; splits *= 2) {
             if (splits > 1 && tiles * splits > 4 * kCus) break;  // (which also bounds the workspace: 256 MiB)

@@ -38,11 +38,17 @@ __device__ __forceinline__ void dma4(int now, int end, const void* base, uint32_
 #pragma clang diagnostic pop
 
 // Waits until at most P * min(MOST, left) of the wave's loads are outstanding (none for left <= 0), and for
-// its LDS reads.
-template <int P, int MOST, bool TEST>
-__device__ __forceinline__ void wait_loads(int left) {
+// its LDS reads; a wave that has P - 1 loads a stage (`fewer`, where they are not EVEN): as many of those.
+template <int P, int MOST, bool TEST, bool EVEN>
+__device__ __forceinline__ void wait_loads(int left, int fewer) {
     static_assert(MOST >= 0 && MOST <= 4 && P * MOST < 64, "vmcnt is six bits");
-    if constexpr (MOST == 0 || !TEST) {
+    if constexpr (!EVEN && TEST) {  // (the last stages only: all waves as those with fewer)
+        wait_loads<P - 1, MOST, true, true>(left, 0);
+    } else if constexpr (!EVEN) {
+        asm volatile("s_cmp_eq_u32 %0, 0\n\ts_cbranch_scc1 1f\n\ts_waitcnt vmcnt(%1)\n1:\ts_waitcnt vmcnt(%2) lgkmcnt(0)" ::"s"(fewer),
+                     "n"((P - 1) * MOST), "n"(P * MOST)
+                     : "memory", "scc");
+    } else if constexpr (MOST == 0 || !TEST) {
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(P * MOST) : "memory");
     } else if constexpr (MOST <= 2) {
         asm volatile("s_cmp_ge_i32 %0, %1\n\ts_cbranch_scc1 2f\n\ts_cmp_ge_i32 %0, 1\n\ts_cbranch_scc1 1f\n\ts_waitcnt vmcnt(0)\n"
@@ -80,13 +86,14 @@ __global__ __launch_bounds__(WF * WT * 64, 2) void k_linear_tiled(LinearCall a, 
     constexpr bool FP8 = KIND == kFp8 || KIND == kE8m0 || KIND == kFp8Wide, F32 = KIND == kF32, BF16 = KIND == kBf16;
     constexpr int NW = WF * WT, TF = WF * NF * 16, TT = WT * NTK * 16;
     constexpr int WB = TF * 128, XB = TT * 128, STAGE = WB + XB;    // bytes of a stage: 128 of each row
-    constexpr int PIECES = STAGE / 1024 / NW, WL = WB / 1024 / NW;  // KiB loads a wave and stage, the weights' first
+    // KiB loads a wave and stage, the weights' first; where x's cannot be shared out evenly the last waves have one less
+    constexpr int WL = WB / 1024 / NW, XL = (XB / 1024 + NW - 1) / NW, PIECES = WL + XL, FULL = XB / 1024 - (XL - 1) * NW;
     constexpr int ESZ = FP8 ? 1 : F32 ? 4 : 2, S = FP8 ? 1 : F32 ? 8 : 2;  // matrix steps of a stage
     // fp8: scales of SC stages at a time, [token][stage], then [128 features][stage]
     constexpr int SC = 8, SB = (TT * SC + 64) * 4;
     constexpr int OUT_ROW = NF * 16 + 4;                            // floats; 32 token rows a wave in the epilogue
     constexpr int LDS_LOOP = NB * STAGE + (FP8 ? 2 * SB : 0), LDS_OUT = NW * 32 * OUT_ROW * 4;
-    static_assert(WL % 2 == 0 && PIECES * 1024 * NW == STAGE && NTK % 2 == 0, "shape");
+    static_assert(WL % 2 == 0 && WL * 1024 * NW == WB && NTK % 2 == 0, "shape");
     // the scales' loads of a chunk are issued 3 stages before its first use
     static_assert(!FP8 || (128 % (NF * 16) == 0 && (SC - 3) * NW > TT * SC / 64 && NB <= 5), "shape");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS_LOOP > LDS_OUT ? LDS_LOOP : LDS_OUT];
@@ -119,10 +126,13 @@ __global__ __launch_bounds__(WF * WT * 64, 2) void k_linear_tiled(LinearCall a, 
     const int rows = a.T - t0 < TT ? (int)(a.T - t0) : TT;
     const uint8_t* xsrc = static_cast<const uint8_t*>(a.x) + t0 * a.x_stride * ESZ + (int64_t)kb0 * 128 * ESZ;
     const uint32_t woff = lane * 16;
-    uint32_t xoff[PIECES - WL];
+    constexpr bool EVEN = FULL == NW;
+    const int fewer = EVEN ? 0 : (FULL - 1 - wv) >> 31;  // all bits: this wave has XL - 1 pieces of x
+    auto x_piece = [&](int i) { return EVEN ? wv * XL + i : wv + i * NW; };
+    uint32_t xoff[XL];
 #pragma unroll
-    for (int i = 0; i < PIECES - WL; ++i) {
-        const int r = (wv * (PIECES - WL) + i) * 8 + lane / 8;
+    for (int i = 0; i < XL; ++i) {
+        const int r = x_piece(i) * 8 + lane / 8;
         xoff[i] = (uint32_t)(r < rows ? r : rows - 1) * (uint32_t)(a.x_stride * ESZ) + piece_slot<BF16>(r, lane % 8) * 16;
     }
     // piece p of stage st; with TEST if there is such a stage
@@ -132,17 +142,20 @@ __global__ __launch_bounds__(WF * WT * 64, 2) void k_linear_tiled(LinearCall a, 
         const uint32_t to = base + place;
         if constexpr (p < WL)
             dma16<p % 2 * 1024, TEST>(st, nst, wsrc[p / 2] + (int64_t)st * 2048, woff, to + (wv * WL + p / 2 * 2) * 1024);
-        else if constexpr (p < PIECES)
-            dma16<0, TEST>(st, nst, xsrc + (int64_t)st * 128, xoff[p - WL], to + WB + (wv * (PIECES - WL) + p - WL) * 1024);
+        else if constexpr (p < PIECES) {
+            constexpr bool SOME = !EVEN && p == PIECES - 1;  // not every wave's: a stage past the end for the others
+            dma16<0, TEST || SOME>(SOME ? __builtin_amdgcn_readfirstlane(st | (fewer & 1 << 30)) : st, nst, xsrc + (int64_t)st * 128, xoff[p - WL],
+                                   to + WB + x_piece(p - WL) * 1024);
+        }
     };
-    // piece `slot` (SC * NW in all, the last ones alike) of the scales of stages SC c .. (past the end the last
-    // stage's again): 8 tokens, or the tile's blocks of 128 features
+    // piece `slot` of the scales of stages SC c .. (past the end the last stage's again): 8 tokens, or, behind
+    // the tokens', the tile's blocks of 128 features; no piece for a slot beyond
     auto request_scales = [&](int c, int slot) {
         constexpr int XP = TT * SC / 64;
         const bool of_w = slot >= XP;
         const int first = of_w ? g0 / 8 : slot * 8, most = of_w ? (a.N - 1) / 128 : rows - 1;
         const int r = first + lane / SC, kb = kb0 + c * SC + lane % SC;
-        dma4(c * SC, nst, of_w ? a.w_scales : a.x_scales + t0 * nkb, ((r < most ? r : most) * nkb + (kb < nkb ? kb : nkb - 1)) * 4,
+        dma4(slot > XP ? nst : c * SC, nst, of_w ? a.w_scales : a.x_scales + t0 * nkb, ((r < most ? r : most) * nkb + (kb < nkb ? kb : nkb - 1)) * 4,
              base + NB * STAGE + (c & 1) * SB + (of_w ? XP : slot) * 256);
     };
 
@@ -183,17 +196,18 @@ __global__ __launch_bounds__(WF * WT * 64, 2) void k_linear_tiled(LinearCall a, 
         else
             fb[s % SETS][j] = *reinterpret_cast<const op_t*>(lds + (xl[s] + place) + j * 2048);
     };
+    const int w_block = (g0 + wf * NF) / 8 - g0 / 8;
     auto read_scales = [&](int st, float (&x)[NTK], float& w) {
         const float* p = reinterpret_cast<const float*>(lds + NB * STAGE + (st / SC & 1) * SB);
 #pragma unroll
         for (int j = 0; j < NTK; ++j) x[j] = p[(wt * NTK * 16 + j * 16 + (lane & 15)) * SC + st % SC];
-        w = p[TT * SC + wf * NF / 8 * SC + st % SC];
+        w = p[TT * SC + w_block * SC + st % SC];
     };
     // In stage st: stage st + 1 has landed for every wave, and every wave has stage st's fragments in
     // registers, so that its place is free.
     auto meet = [&](int st, auto test) {
         __builtin_amdgcn_sched_barrier(0);
-        wait_loads<PIECES, NB - 2, decltype(test)::value>(nst - 2 - st);
+        wait_loads<PIECES, NB - 2, decltype(test)::value, EVEN>(nst - 2 - st, __builtin_amdgcn_readfirstlane(fewer));
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
     };
@@ -408,6 +422,11 @@ hipError_t launch(const LinearCall& a, int splits, hipStream_t s) {
 
 template <int KIND>
 static hipError_t launch_kind(const LinearCall& a, const LinearPart& p, hipStream_t s) {
+    if constexpr (KIND != kF32) {
+        if (p.kernel == kTile96x64) return launch<KIND, 6, 1, 1, 4, 5>(a, p.splits, s);
+        if (p.kernel == kTile80x64) return launch<KIND, 5, 1, 1, 4, 5>(a, p.splits, s);
+        if (p.kernel == kTile64x64) return launch<KIND, 4, 1, 1, 4, 5>(a, p.splits, s);
+    }
     switch (p.kernel) {
         case kTile256:
             // fp32 keeps two sets of sums, and products of widened operands need registers for them

@@ -234,6 +234,9 @@ def test_linear_of_whole_numbers_is_exact(T, N, K, kind):
 LARGE = [(2300, 9232, 640), (4000, 5136, 256), (2048, 9216, 384), (700, 4112, 2048), (1100, 2064, 4096), (129, 7184, 3968),
          (64, 7184, 7168), (1000, 272, 16384), (300, 4112, 512), (500, 12304, 1152), (4097, 4112, 128), (100, 18432, 2048),
          (260, 784, 7168), (900, 1040, 14336)]
+# tiles of 64, 80 and 96 features, whose waves load unlike numbers of pieces: cut tiles, splits, tiles across two scale blocks
+LARGE += [(33, 24560, 640), (40, 24560, 1152), (49, 18416, 896), (64, 16368, 1152), (100, 9200, 1152), (64, 10256, 7168),
+          (100, 2064, 7168), (250, 4112, 3968)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32", "fp8", "e8m0"])
