@@ -561,7 +561,8 @@ int rdg_paged_attention(const void* q, int dtype, int64_t q_stride, int T, int n
 
 /* ---------------------------------------------------------------- joins of a layer
  * What a decoder layer computes between its attention and expert halves (not on the
- * pages).  Strides are in elements; rows start on 16 bytes. */
+ * pages).  Strides are in elements, below 2^28; rows start on 16 bytes (rdg_route_topk's logits
+ * where they like).  Outputs do not overlap inputs or each other except where a call says so. */
 
 /* The residual's addition with the root-mean-square norm, and its output in 8 bits, in
  * one pass:
@@ -600,11 +601,13 @@ int rdg_add_norm(const void* x, int x_dtype, int64_t x_stride, int T, int H, con
  *             the stride is the same
  *   out       [T, out_stride] rows of N elements: RDG_F32 or RDG_BF16 (fp32 operands:
  *             RDG_F32, else RDG_EUNSUPPORTED)
- *   work      rdg_linear_workspace_bytes(T, N, K, dtype) bytes (NULL when that is 0); nothing
- *             in it needs clearing.  Calls that overlap need workspaces of their own
+ *   work      rdg_linear_workspace_bytes(T, N, K, dtype) bytes, at most 256 MiB (NULL when that is
+ *             0); nothing in it needs clearing.  Calls that overlap need workspaces of their own
  * N is a multiple of 16, K of 128.  Products are summed in fp32 (fp8: of every 128,
  * then scaled by both blocks' scales in fp32), and everything up to the one rounding of out is
- * fp32.  Deterministic.  out may not be x.  T = 0 is a no-op. */
+ * fp32.  (fp8 to RDG_BF16: the matrix core's sum of 128 products is good to about 2^-16; to RDG_F32 the
+ * products are taken from bf16 operands, which hold every code, at half the rate.)  Deterministic; a
+ * token's sums do not depend on the other tokens' values, but their order may on T.  T = 0 is a no-op. */
 size_t rdg_linear_workspace_bytes(int T, int N, int K, int dtype);
 int rdg_linear(const void* x, const float* x_scales, int dtype, int64_t x_stride, int T, int N, int K, const void* W,
                const float* W_scales, const float* bias, int act, const void* residual, int64_t res_stride, void* out,

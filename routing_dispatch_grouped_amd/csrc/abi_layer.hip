@@ -22,6 +22,11 @@ inline bool rows_ok(const void* p, int64_t stride, int64_t n, int64_t rows, int 
     return p != nullptr && aligned16(p) && stride >= n && stride < (int64_t)1 << 28 && stride * esz % 16 == 0 && rows < (int64_t)1 << 31;
 }
 
+// An output may lie where an input lies only as the same rows: the same type, and the same stride beyond one row.
+inline bool apart_or_same(const void* to, const void* from, bool same_type, int64_t to_stride, int64_t from_stride, int T) {
+    return to == nullptr || to != from || (same_type && (to_stride == from_stride || T == 1));
+}
+
 inline bool is_fp8(int dtype) { return dtype == RDG_FP8_E4M3 || dtype == RDG_FP8_E4M3_UE8M0; }
 inline bool is_float(int dtype) { return dtype == RDG_F32 || dtype == RDG_BF16; }
 inline int size_of(int dtype) { return dtype == RDG_F32 ? 4 : dtype == RDG_BF16 ? 2 : 1; }
@@ -49,8 +54,13 @@ int rdg_add_norm(const void* x, int x_dtype, int64_t x_stride, int T, int H, con
     if (out != nullptr && !rows_ok(out, out_stride, H, T, size_of(x_dtype))) return RDG_EINVAL;
     if (q != nullptr && (!aligned16(q) || q_scales == nullptr || !aligned16(q_scales))) return RDG_EINVAL;
     if (weight != nullptr && !aligned16(weight)) return RDG_EINVAL;
-    // two outputs in one place
+    // two outputs in one place, or one that would run over an input's other rows
     if (residual_out != nullptr && residual_out == out) return RDG_EINVAL;
+    if (q != nullptr && (q == x || q == residual || q == residual_out || q == out)) return RDG_EINVAL;
+    const bool alike = residual != nullptr && res_dtype == x_dtype;
+    if (!apart_or_same(residual_out, x, alike, res_stride, x_stride, T) || !apart_or_same(out, x, true, out_stride, x_stride, T) ||
+        !apart_or_same(out, residual, alike, out_stride, res_stride, T))
+        return RDG_EINVAL;
     AddNormCall a{};
     a.x = x, a.residual = residual, a.residual_out = residual_out, a.weight = weight, a.out = out, a.q = q;
     a.q_scales = q_scales, a.x_stride = x_stride, a.res_stride = res_stride, a.out_stride = out_stride, a.eps = eps;
@@ -76,6 +86,7 @@ int rdg_linear(const void* x, const float* x_scales, int dtype, int64_t x_stride
         return RDG_EINVAL;
     if (bias != nullptr && !aligned16(bias)) return RDG_EINVAL;
     if (residual != nullptr && !rows_ok(residual, res_stride, N, T, size_of(out_dtype))) return RDG_EINVAL;
+    if (out == x || out == W || !apart_or_same(out, residual, true, out_stride, res_stride, T)) return RDG_EINVAL;
     const size_t need = linear_workspace_bytes(T, N, K, dtype);
     if (need > 0 && (work == nullptr || !aligned16(work) || work_bytes < need)) return RDG_EINVAL;
     LinearCall a{};

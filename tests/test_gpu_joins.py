@@ -318,6 +318,18 @@ def test_linear_output_past_32_bit_offsets():
     assert torch.equal(out.cpu(), want)
 
 
+@pytest.mark.parametrize("T,N,stride", [(40, 256, 1 << 22), (40, 256, (1 << 22) - 8), (250, 272, (1 << 22) - 8), (300, 64, (1 << 22) + 8)])
+def test_linear_of_rows_far_apart(T, N, stride):
+    """x with 8 MiB from row to row: just below and just beyond the offsets that the tiles' loads hold."""
+    m, K = rdg(), 256
+    c = linear_case(T, N, K, "bf16", True)
+    x = torch.empty(T * stride, dtype=BF, device=DEV).as_strided((T, K), (stride, 1))
+    x.copy_(c["x"])
+    out = torch.empty(T, N, device=DEV)
+    m.rdg_linear(x, None, c["kind"], c["w"], None, out, work=work_for(T, N, K, c["kind"]))
+    assert np.array_equal(f64(out), c["xv"] @ c["wv"].T)
+
+
 # ---------------------------------------------------------------- routing
 def route(logits, score, bias=None, group=1, keep=1, best=1, K=2, renorm=True, scale=1.0):
     m = rdg()
@@ -516,3 +528,27 @@ def test_two_streams_with_workspaces_of_their_own():
     for b, w in zip(blocks, want):
         for u, v in zip(b.results(), w):
             assert torch.equal(u, v)
+
+
+def test_two_graphs_that_share_a_workspace():
+    """Captured apart, replayed in turn on one stream: what one leaves in the workspace does not reach the other."""
+    blocks = [Block(60, seed=s) for s in (11, 12)]
+    size = max(b.work.numel() for b in blocks)
+    shared = torch.empty(size, dtype=torch.uint8, device=DEV)
+    want, graphs = [], []
+    for b in blocks:
+        b.work = shared
+        b.run()
+        want.append(b.results())
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            b.run()
+        graphs.append(g)
+    for i in range(6):
+        graphs[i % 2].replay()
+        shared.fill_(0xff)
+        graphs[(i + 1) % 2].replay()
+        for b, w in zip(blocks, want):
+            for u, v in zip(b.results(), w):
+                assert torch.equal(u, v)

@@ -13,7 +13,7 @@ def _rdg():
 def _norm(**change):
     rdg = _rdg()
     a = dict(x=A, x_dtype=rdg.RDG_BF16, x_stride=256, T=4, H=256, residual=A, residual_out=A, res_dtype=rdg.RDG_BF16,
-             res_stride=256, weight=A, eps=1e-6, out=2 * A, out_stride=256, q=A, q_scales=A, q_dtype=rdg.RDG_FP8_E4M3)
+             res_stride=256, weight=A, eps=1e-6, out=2 * A, out_stride=256, q=3 * A, q_scales=A, q_dtype=rdg.RDG_FP8_E4M3)
     a.update(change)
     return rdg._lib.rdg_add_norm(*a.values(), None)
 
@@ -23,7 +23,10 @@ def _norm(**change):
     dict(x_stride=260), dict(x_stride=-256), dict(res_dtype=3), dict(res_dtype=-1), dict(residual=A + 4), dict(res_stride=248),
     dict(residual=None), dict(residual_out=A + 2), dict(weight=A + 4), dict(eps=-1.0), dict(eps=float("nan")),
     dict(eps=float("inf")), dict(out=None, q=None), dict(out=A), dict(out=2 * A + 8), dict(out_stride=128), dict(q=A + 8),
-    dict(q_scales=None), dict(q_scales=A + 4), dict(q_dtype=0), dict(q_dtype=1)])
+    dict(q_scales=None), dict(q_scales=A + 4), dict(q_dtype=0), dict(q_dtype=1),
+    # an output over an input's other rows, or over another output
+    dict(res_dtype=0), dict(res_stride=264), dict(residual_out=5 * A, out=A, out_stride=264), dict(out=A, residual_out=A), dict(q=A),
+    dict(q=2 * A), dict(x=4 * A, residual_out=5 * A, out=A, res_stride=512)])
 def test_norm_refusals(change):
     assert _norm(**change) == _rdg().RDG_EINVAL
 
@@ -39,7 +42,7 @@ def test_norm_sizes():
 def _linear(**change):
     rdg = _rdg()
     a = dict(x=A, x_scales=A, dtype=rdg.RDG_FP8_E4M3, x_stride=256, T=4, N=48, K=256, W=A, W_scales=A, bias=A, act=1,
-             residual=A, res_stride=48, out=A, out_dtype=rdg.RDG_BF16, out_stride=48, work=A, work_bytes=1 << 40)
+             residual=A, res_stride=48, out=2 * A, out_dtype=rdg.RDG_BF16, out_stride=48, work=A, work_bytes=1 << 40)
     a.update(change)
     return rdg._lib.rdg_linear(*a.values(), None)
 
@@ -48,7 +51,8 @@ def _linear(**change):
     dict(T=-1), dict(N=0), dict(N=24), dict(K=0), dict(K=192), dict(dtype=4), dict(dtype=-1), dict(x=None), dict(x=A + 8),
     dict(x_stride=128), dict(x_stride=264), dict(x_scales=None), dict(x_scales=A + 4), dict(W=None), dict(W=A + 8), dict(W_scales=None),
     dict(W_scales=A + 4), dict(bias=A + 4), dict(act=-1), dict(act=5), dict(residual=A + 8), dict(res_stride=40), dict(res_stride=52),
-    dict(out=None), dict(out=A + 4), dict(out_stride=32), dict(out_dtype=2)])
+    dict(out=None), dict(out=A + 4), dict(out_stride=32), dict(out_dtype=2), dict(out=A), dict(x=4 * A, out=A, residual=None),
+    dict(residual=2 * A, res_stride=64)])
 def test_linear_refusals(change):
     assert _linear(**change) == _rdg().RDG_EINVAL
 
