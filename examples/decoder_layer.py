@@ -5,8 +5,7 @@ cache, then the mixture-of-experts half, for prefill and decode steps.
 
 Random weights.  Requests arrive, are prefilled together, decode one token a
 step beside newly arriving ones, and hand their pages back when they finish.
-PyTorch supplies memory, streams, and the plain matrix products and norms between
-the library's calls.
+PyTorch supplies memory and streams; every step of the layer is the library's.
 """
 import os
 import sys
@@ -19,11 +18,12 @@ import routing_dispatch_grouped_amd as rdg  # noqa: E402
 
 class DecoderLayer:
     def __init__(self, hidden=512, n_q=16, n_kv=4, head_dim=64, n_experts=16, inner=256, top_k=4, page_rows=16,
-                 n_pages=64, max_requests=8, max_context=256, max_tokens=256, device="cuda", seed=0):
+                 n_pages=64, max_requests=8, max_context=256, max_tokens=256, device="cuda", seed=0,
+                 score=rdg.RDG_SCORE_SIGMOID):
         g = torch.Generator(device=device).manual_seed(seed)
         self.H, self.n_q, self.n_kv, self.D = hidden, n_q, n_kv, head_dim
         self.N, self.I, self.K, self.dev = n_experts, inner, top_k, device
-        self.max_context, self.n_pages = max_context, n_pages
+        self.max_context, self.n_pages, self.score = max_context, n_pages, score
 
         def weight(*shape):
             return (torch.randn(*shape, device=device, generator=g) * shape[-1] ** -0.5).bfloat16()
@@ -34,14 +34,14 @@ class DecoderLayer:
         self.gain_k = 1 + 0.1 * torch.randn(head_dim, device=device, generator=g)
         self.router = weight(n_experts, hidden)
 
-        def packed(*shape):
-            w = weight(*shape)
+        def packed(w):
             p = torch.empty_like(w)
             rdg.rdg_pack_weights(w, rdg.RDG_BF16, p)
             return p
 
-        self.w1, self.w3 = packed(n_experts, inner, hidden), packed(n_experts, inner, hidden)
-        self.w2 = packed(n_experts, hidden, inner)
+        self.p_qkv, self.p_o, self.p_router = packed(self.w_qkv), packed(self.w_o), packed(self.router)
+        self.w1, self.w3 = packed(weight(n_experts, inner, hidden)), packed(weight(n_experts, inner, hidden))
+        self.w2 = packed(weight(n_experts, hidden, inner))
         angle = torch.arange(max_context, device=device)[:, None] * 10000.0 ** (
             -torch.arange(0, head_dim, 2, device=device) / head_dim)
         self.cos_sin = torch.cat([angle.cos(), angle.sin()], 1).float().contiguous()
@@ -63,12 +63,22 @@ class DecoderLayer:
 
     @staticmethod
     def norm(x):
-        f = x.float()
-        return (f * torch.rsqrt((f * f).mean(-1, keepdim=True) + 1e-6)).to(x.dtype)
+        out = torch.empty_like(x)
+        rdg.rdg_add_norm(x, None, 1e-6, out=out)
+        return out
+
+    @staticmethod
+    def linear(x, w, dtype=torch.bfloat16, residual=None):
+        """x @ W.T (+ residual), W packed"""
+        (T, K), N = x.shape, w.shape[0]
+        out = torch.empty(T, N, dtype=dtype, device=x.device)
+        work = torch.empty(rdg.rdg_linear_workspace_bytes(T, N, K, rdg.RDG_BF16), dtype=torch.uint8, device=x.device)
+        rdg.rdg_linear(x, None, rdg.RDG_BF16, w, None, out, residual=residual, work=work)
+        return out
 
     def attention(self, x, max_q):
         T, n_q, D = x.shape[0], self.n_q, self.D
-        qkv = self.norm(x) @ self.w_qkv.T
+        qkv = self.linear(self.norm(x), self.p_qkv)
         q = torch.empty(T, n_q, D, dtype=x.dtype, device=self.dev)
         rdg.rdg_qk_norm_rope_store(qkv, n_q, self.n_kv, D, self.gain_q, self.gain_k, 1e-6, self.cos_sin, D, False, self.step,
                                    self.cache, q)
@@ -77,14 +87,15 @@ class DecoderLayer:
                                                                    self.max_context, rdg.RDG_BF16),
                            dtype=torch.uint8, device=self.dev)
         rdg.rdg_paged_attention(q, self.step, self.cache, max_q, self.max_context, D ** -0.5, out, work=work)
-        return x + out.view(T, -1) @ self.w_o.T
+        return self.linear(out.view(T, -1), self.p_o, residual=x)
 
     def experts(self, x):
         T, H, K = x.shape[0], self.H, self.K
         n = self.norm(x)
         ids = torch.empty(T, K, dtype=torch.int32, device=self.dev)
         w = torch.empty(T, K, dtype=torch.float32, device=self.dev)
-        rdg.rdg_route((n @ self.router.T).float().contiguous(), 4, 2, K, 1.0, ids, w)
+        logits = self.linear(n, self.p_router, torch.float32)
+        rdg.rdg_route_topk(logits, self.score, 4, 2, 2, K, True, 1.0, ids, w)
         L = rdg.Layout(rdg.RDG_CONTIGUOUS, self.N, T, K, self.dev, block_m=16)
         rdg.rdg_dispatch(n, None, rdg.RDG_BF16, ids, L, None)
         h = torch.empty(L.m_cap, self.I, dtype=x.dtype, device=self.dev)
