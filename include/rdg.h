@@ -621,7 +621,7 @@ int rdg_linear(const void* x, const float* x_scales, int dtype, int64_t x_stride
  *   bias      [N] fp32, added for the choice only, or NULL
  *   n_group   groups of N / n_group consecutive experts (1: no groups), topk_group of them kept
  *   group_best  a group's rank is its largest choice (1) or the sum of its two largest (2;
- *             the one where it has one)
+ *             the one where it has one, the larger of +inf and -inf)
  *   renorm    nonzero: topk_w = p / (sum of the K chosen p) * scale, else p * scale
  *   topk_ids  [B, K] int32 out, in (choice desc, id asc) order; topk_w [B, K] fp32 out
  * p is computed in fp64 and rounded once to fp32; the rest is fp32; ties go to the lower index.

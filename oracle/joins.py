@@ -86,7 +86,8 @@ def route_topk(logits, score, bias, n_group, topk_group, group_best, K, renorm, 
         rank = []
         for g in range(n_group):
             best = sorted(c[g * gs:(g + 1) * gs], reverse=True)
-            rank.append(np.float32(best[0] + best[1]) if group_best == 2 and gs > 1 else best[0])
+            pair = group_best == 2 and gs > 1 and not (best[0] == np.inf and best[1] == -np.inf)
+            rank.append(np.float32(best[0] + best[1]) if pair else best[0])
         kept = sorted(range(n_group), key=lambda g: (-rank[g], g))[:topk_group]
         cand = [e for g in kept for e in range(g * gs, (g + 1) * gs)]
         ids[b] = sorted(cand, key=lambda e: (-c[e], e))[:K]

@@ -270,6 +270,12 @@ __device__ __forceinline__ void topk_store(const RouteCall& a, int64_t t, int k,
     a.w[t * a.K + k] = w * a.scale;
 }
 
+// A group's rank from its two largest choices; +inf and -inf together count as the larger.
+__device__ __forceinline__ float group_rank(const RouteCall& a, int gs, float best, float next) {
+    const float sum = best + next;
+    return a.group_best == 2 && gs >= 2 && sum == sum ? sum : best;
+}
+
 // Up to 32 experts: SEG lanes a token.
 template <int SEG>
 __global__ __launch_bounds__(kTopkThreads) void k_route_few(RouteCall a) {
@@ -304,7 +310,7 @@ __global__ __launch_bounds__(kTopkThreads) void k_route_few(RouteCall a) {
                 next = fmaxf(next, fminf(best, ch[i]));
                 best = fmaxf(best, ch[i]);
             }
-            rank[sub] = a.group_best == 2 && gs >= 2 ? best + next : best;
+            rank[sub] = group_rank(a, gs, best, next);
             own = ordered_bits(rank[sub]);
         }
         wave_lds_fence();
@@ -382,7 +388,7 @@ __global__ __launch_bounds__(kTopkThreads) void k_route_wave(RouteCall a) {
             merge(best, next, lane_of<kSwap1>(best), lane_of<kSwap1>(next));
             merge(best, next, lane_of<kSwap2>(best), lane_of<kSwap2>(next));
             merge(best, next, lane_of<kMirror8>(best), lane_of<kMirror8>(next));
-            const uint32_t own = ordered_bits(a.group_best == 2 && gs >= 2 ? best + next : best);
+            const uint32_t own = ordered_bits(group_rank(a, gs, best, next));
             int better = 0;
             for (int h = 0; h < a.n_group; ++h) {
                 const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)own, h * 8);
@@ -401,7 +407,7 @@ __global__ __launch_bounds__(kTopkThreads) void k_route_wave(RouteCall a) {
                 float best = -__builtin_inff(), next = best;
                 if (g < a.n_group)
                     for (int i = g * gs; i < (g + 1) * gs; ++i) merge(best, next, ch[i], -__builtin_inff());
-                rank[v] = a.group_best == 2 && gs >= 2 ? best + next : best;
+                rank[v] = group_rank(a, gs, best, next);
             }
             wave_lds_fence();
 #pragma unroll

@@ -413,6 +413,18 @@ def test_route_of_masked_and_broken_logits(N, group, keep, score):
     check_route(logits, score, bias, group, keep, 1, 4, True)
 
 
+@pytest.mark.parametrize("N,group,keep,K", [(16, 8, 3, 4), (32, 4, 2, 8), (64, 32, 5, 8), (256, 8, 2, 8), (512, 256, 9, 12), (96, 48, 48, 32)])
+def test_route_of_biases_that_force_and_forbid(N, group, keep, K):
+    """Infinite biases of both signs, also both within a group of two."""
+    inf = float("inf")
+    g = torch.Generator(device=DEV).manual_seed(N)
+    bias = 0.1 * torch.randn(N, device=DEV, generator=g)
+    bias[3], bias[2], bias[N - 2], bias[N - 1], bias[N // 2:N // 2 + 2] = inf, -inf, inf, inf, -inf
+    for score in ("softmax", "sigmoid"):
+        for best in (1, 2):
+            check_route(torch.randn(37, N, device=DEV, generator=g), score, bias, group, keep, best, K, True)
+
+
 def test_route_of_no_tokens():
     route(torch.empty(0, 16, device=DEV), "softmax")
     torch.cuda.synchronize()
