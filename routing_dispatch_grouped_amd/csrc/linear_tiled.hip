@@ -366,12 +366,31 @@ __global__ __launch_bounds__(WF * WT * 64, 2) void k_linear_tiled(LinearCall a, 
 
     // ---------------------------------------------------------------- epilogue
     // Each wave turns its sums over in LDS (its own part; no wave reads operands any more), two token
-    // tiles at a time, and stores 8 features a lane: whole rows of its features.
-    constexpr int LPR = NF * 2, RPP = 64 / LPR;  // lanes a row, rows a pass
+    // tiles at a time, and stores 8 features a lane: whole rows of its features.  The residual of these rows is asked for
+    // first, all at once, and bias and activation are done in place in LDS by a loop of their own, whose code
+    // is there once.
+    constexpr int LPR = NF * 2, RPP = 64 / LPR, PASSES = 32 / RPP;  // lanes a row, rows a pass
     float* tile = reinterpret_cast<float*>(lds) + wv * 32 * OUT_ROW;
     const int f = (g0 + wf * NF) * 16 + lane % LPR * 8;
+    const bool whole = splits == 1, added = whole && a.residual != nullptr && f < a.N;
+    auto place = [&](int p) { return tile + (p * RPP + lane / LPR) * OUT_ROW + lane % LPR * 8; };
+    float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (whole && a.bias != nullptr && f < a.N) load8<false>(a.bias, f, bias);
 #pragma unroll
     for (int half = 0; half < NTK / 2; ++half) {
+        const int64_t first = t0 + (wt * NTK + half * 2) * 16 + lane / LPR;
+        uint4 held[PASSES][2];
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) {
+            held[p][0] = held[p][1] = make_uint4(0u, 0u, 0u, 0u);
+            const int64_t t = first + p * RPP;
+            if (added && t < a.T) {
+                const uint4* r = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.residual) +
+                                                                (t * a.res_stride + f) * (a.out_bf16 ? 2 : 4));
+                held[p][0] = r[0];
+                if (!a.out_bf16) held[p][1] = r[1];
+            }
+        }
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -380,15 +399,38 @@ __global__ __launch_bounds__(WF * WT * 64, 2) void k_linear_tiled(LinearCall a, 
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        if (whole && (a.bias != nullptr || a.act != RDG_ACT_NONE)) {
 #pragma unroll 1
-        for (int p = 0; p < 32 / RPP; ++p) {
-            const int row = p * RPP + lane / LPR;
-            const int64_t t = t0 + (wt * NTK + half * 2) * 16 + row;
+            for (int p = 0; p < PASSES; ++p) {
+                float v[8];
+                load8<false>(place(p), 0, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] += bias[e];
+                activate(v, a.act);
+                store8<false>(place(p), 0, v);  // read by this lane alone
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) {
+            const int64_t t = first + p * RPP;
             float v[8];
-            load8<false>(tile + row * OUT_ROW, lane % LPR * 8, v);
+            load8<false>(place(p), 0, v);
             if (t < a.T && f < a.N) {
-                if (splits == 1) finish8(a, v, t, f);
-                else store8<false>(a.parts, ((int64_t)split * a.T + t) * a.N + f, v);
+                if (!whole) {
+                    store8<false>(a.parts, ((int64_t)split * a.T + t) * a.N + f, v);
+                } else if (a.out_bf16) {
+                    float r[8];
+                    load8<true>(&held[p][0], 0, r);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] += r[e];
+                    store8<true>(a.out, t * a.out_stride + f, v);
+                } else {
+                    float r[8];
+                    load8<false>(&held[p][0], 0, r);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] += r[e];
+                    store8<false>(a.out, t * a.out_stride + f, v);
+                }
             }
         }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
