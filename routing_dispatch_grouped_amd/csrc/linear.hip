@@ -123,7 +123,7 @@ constexpr TileCost kFp8Cost[] = {{kTile256, 256, 256, 1, 1.3f, 1.5f, 7.0f},     
                                  {kTile64x64, 64, 64, 1, 0.373f, 0.34f, 1.65f}};
 constexpr TileCost kF32Cost[] = {{kTile128, 128, 128, 1, 1.92f, 1.92f, 2.0f},
                                  {kTile128x64, 128, 64, 1, 1.08f, 1.08f, 1.3f},
-                                 {kTile64x32, 64, 32, 3, 0.444f, 0.30f, 0.8f}};
+                                 {kTile64x32, 64, 32, 3, 0.39f, 0.30f, 0.8f}};
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int size_of(int dtype) { return dtype == RDG_F32 ? 4 : dtype == RDG_BF16 ? 2 : 1; }

@@ -173,12 +173,14 @@ __global__ __launch_bounds__(WF * WT * 64, 2) void k_linear_tiled(LinearCall a, 
         for (int j = 0; j < NTK; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
     // fragments: a wave's items are (step s, weight tile i), NTK matrix instructions each.  Weight
-    // fragments are read AHEAD items before their use, token fragments a step before.
+    // fragments are read AHEAD items before their use, token fragments a step before; fp32's, whose steps are short, both
+    // AHEAD steps where a step is an item (DEEP).
     using op_t = typename LinOp<FP8 ? RDG_FP8_E4M3 : F32 ? RDG_F32 : RDG_BF16>::op_t;
-    constexpr int NI = S * NF, AHEAD = FP8 || NF < 4 ? 1 : 3, RPI = (2 * PIECES + NI - 1) / NI;
+    constexpr bool DEEP = F32 && NF == 1;
+    constexpr int NI = S * NF, AHEAD = DEEP ? 3 : FP8 || NF < 4 ? 1 : 3, RPI = (2 * PIECES + NI - 1) / NI;
     constexpr int EARLY = AHEAD * RPI < PIECES ? AHEAD * RPI : PIECES;  // pieces issued between the meeting and the stage's end
-    constexpr int SETS = S > 1 ? 2 : 1;
-    static_assert(AHEAD <= NF && (NI % (AHEAD + 1) == 0 || NI == 1), "this stage's fragments are read before the meeting");
+    constexpr int SETS = DEEP ? AHEAD + 1 : S > 1 ? 2 : 1;
+    static_assert((AHEAD <= NF || DEEP) && (NI % (AHEAD + 1) == 0 || NI == 1), "this stage's fragments are read before the meeting");
     static_assert(NI * RPI >= PIECES, "items");
     op_t fa[AHEAD + 1], fb[SETS][NTK];
     float sx[NTK], sw = 1.0f;
@@ -229,7 +231,9 @@ __global__ __launch_bounds__(WF * WT * 64, 2) void k_linear_tiled(LinearCall a, 
     meet(-1, Yes{});
     each<EARLY>([&](auto p) { request(NB - 1, (NB - 1) * STAGE, p, Yes{}); });
 #pragma unroll
-    for (int j = 0; j < NTK; ++j) read_b(0, 0, j);
+    for (int s = 0; s < (DEEP ? AHEAD : 1); ++s)
+#pragma unroll
+        for (int j = 0; j < NTK; ++j) read_b(0, s, j);
     if (FP8) read_scales(0, sx, sw);
 #pragma unroll
     for (int it = 0; it < AHEAD; ++it) read_a(0, it);
@@ -255,7 +259,12 @@ __global__ __launch_bounds__(WF * WT * 64, 2) void k_linear_tiled(LinearCall a, 
             if constexpr (FP8 && it == 0) request_scales(st / SC + 1, st % SC * NW + wv);
             const op_t w = fa[it % (AHEAD + 1)];
             if (it + AHEAD < NI) read_a(here, it + AHEAD);
-            if constexpr (s + 1 < S) {  // in the step's last items, all in one where it has fewer than NTK
+            if constexpr (DEEP) {
+                if constexpr (it + AHEAD < NI) {
+#pragma unroll
+                    for (int j = 0; j < NTK; ++j) read_b(here, it + AHEAD, j);
+                }
+            } else if constexpr (s + 1 < S) {  // in the step's last items, all in one where it has fewer than NTK
                 if constexpr (NF < NTK) {
                     if constexpr (i == NF - 1) {
 #pragma unroll
@@ -269,7 +278,7 @@ __global__ __launch_bounds__(WF * WT * 64, 2) void k_linear_tiled(LinearCall a, 
                 meet(st, test);
                 if constexpr (FP8) {
                     read_scales(st + 1, next_sx, next_sw);
-                } else {
+                } else if constexpr (!DEEP) {
 #pragma unroll
                     for (int j = 0; j < NTK; ++j) read_b(next, 0, j);
                 }
@@ -283,6 +292,10 @@ __global__ __launch_bounds__(WF * WT * 64, 2) void k_linear_tiled(LinearCall a, 
             });
             // (behind the last stage the first fragments are read from a place that holds none, and not used)
             if (it + AHEAD >= NI) read_a(next, it + AHEAD - NI);
+            if constexpr (DEEP && it + AHEAD >= NI) {
+#pragma unroll
+                for (int j = 0; j < NTK; ++j) read_b(next, it + AHEAD - NI, j);
+            }
             if constexpr (BF16 || F32) {
 #pragma unroll
                 for (int j = 0; j < NTK; ++j)
