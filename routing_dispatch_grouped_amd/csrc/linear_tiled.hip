@@ -1,4 +1,28 @@
-// Matrix product with its epilogue for many tokens: tiles of TF features x TT tokens.
+// Matrix product with its epilogue for more than a few tokens: a workgroup has a tile of TF features x TT
+// tokens and walks over its share of the reduction in stages of 128 bytes of each row.
+//
+//   acc[f, t] = sum_k W[f, k] x[t, k]    (fp8: sum over blocks of 128 of (sum of the block) * W_scale * x_scale)
+//   out = act(acc + bias) + residual, or, with the reduction split, parts that k_linear_join adds in their order
+//
+// Features are the matrix instruction's rows and tokens its columns, so that a lane's four sums are neighbours in the
+// packed weights' order.  WF x WT waves have NF x NTK tiles of 16 x 16 each.
+//
+// Operands go from memory straight to LDS, into a ring of NB stages: up to NB - 1 stages are under way during the
+// products, a few loads at a time between matrix instructions (all at once they would hold up the wave's own).  A packed
+// weight tile is in the order of the lanes, so that its reads meet no bank twice; a token's row is 128 bytes, whose 16-byte
+// pieces are swapped (piece_slot).  One meeting of the workgroup a stage: behind it the next stage is there for
+// all and the oldest place is free.  The loop's body is there twice, without and, for the last NB stages, with tests for
+// the end.
+//
+// Large tiles are bound by the matrix core (256 x 256: bf16 8192 x 7168 x 8192 677 .. 686 us, 1.4 PFLOP/s, its units 72%
+// busy at 1.8 GHz; e8m0 4001 x 18432 x 7168 415 us, 2.55 PFLOP/s; fp32 scales 467: the sums' multiplications are nearly
+// as many cycles as the products), small ones by the lines that a compute unit has under way or by L2 (4096 tokens on 256
+// features of K = 7168: 24.4 us, 3.7 million lines from L2, 23 TB/s), with few tokens by memory (linear.hip).
+// Tiles lie in bands of four by features on each XCD: 8192 x 7168 x 8192 686 us, with bands of one 792, of two 708, of
+// eight 695, of all features 743; 4096 x 18432 x 7168 800, 807, 807, 833 and 921.
+//
+// Not kept: the 32 x 32 x 16 instruction and raised wave priority around the products (slower), a ring of 6
+// stages for 128 x 64 (no gain).
 #include <type_traits>
 #include <utility>
 

@@ -189,6 +189,9 @@ __global__ __launch_bounds__(256) void k_route(const float* __restrict__ logits,
 // hold its experts one each); beyond, a wave with VPL experts a lane, expert e on lane e % 64.
 // A round is a maximum of ordered score bits across the token's lanes, in the vector unit, and a ballot for
 // the lowest expert that holds it.
+//
+// Measured: 16384 tokens of 160 experts, 3 of 8 groups, 6 chosen 15.6 us; of 256 experts, 8 chosen 13.7; sigmoid, 4 of 8
+// groups by their two best, biased 19.2 (k_route 40.4); 32768 tokens of 8 experts 3.0; 128 of 256 4.0.
 constexpr int kTopkThreads = 256;
 
 // The logits of token t that lane `first` of STEP lanes holds, -inf past the last; NaN counts as -inf, +inf as the
