@@ -90,20 +90,22 @@ hipError_t launch_rows(const LinearCall& a, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------- which kernel
-// The expected time of each kernel and split in us, and the least of them.  Constants measured over 499 sizes each of
+// The expected time of each kernel and split in us, and the least of them.  Constants measured over 461 sizes each of
 // bf16 and of fp8 (1 .. 5000 tokens, 64 .. 32768 features, K of 256 .. 14336, weights from memory); the choice takes on
-// average 0.6% longer than the best of all at each size, 1.3 times at worst (16 tokens, 7168 features, K = 2048, bf16: 9.8 us).
+// average 1% longer than the best of all at each size, 1.23 times at worst (64 tokens, 2048 features, K = 7168, bf16: 13.5 us).
 constexpr int kCus = 256;
 constexpr float kStart = 2.0f, kMore = 1.5f;            // launch, first loads, last stores; one launch more
-constexpr float kRowsRead = 7.6e6f, kTilesRead = 7.1e6f;  // bytes/us at which weights come from memory
-constexpr float kJoin = 2.4f, kJoinRate = 3.6e6f;       // the join's launch; splits' sums, written and read
+constexpr float kRowsRead = 6.7e6f, kTilesRead = 7.5e6f;  // bytes/us at which weights come from memory
+constexpr float kJoin = 3.0f, kJoinRate = 3.6e6f;       // the join's launch; splits' sums, written and read
 // With few tokens a stage takes the time in which a CU gets its 128-byte lines: it has some 500 of them under way at
 // a time, for a latency that grows with the weights under way on the whole chip.  So the tile is best whose workgroups
 // just fill the CUs: 64 tokens, 18432 features, K = 7168 in bf16, of 128 features on 144 CUs 60.4 us, of 80 on 231
-// 49.6; 16384 features in e8m0, of 128 35.4 us, of 64 28.3.
+// 49.6; 16384 features in e8m0, of 128 35.4 us, of 64 28.3.  Weights that pass the caches
+// (k_linear_tiled's ONCE) take less.
 constexpr int kFewTokens = 160;
 constexpr float kLine = 0.00168f, kUnderWay = 8.0e-6f;  // us a line; us a feature of the tile and workgroup of the chip
-constexpr float kFewFp8 = 0.045f;                       // the scales' lines
+constexpr float kLineOnce = 0.0015f, kUnderWayOnce = 7.9e-6f;
+constexpr float kFewFp8 = 0.045f, kFewFp8Once = 0.03f;  // the scales' lines
 
 struct TileCost {
     int kernel, features, tokens;
@@ -114,13 +116,13 @@ struct TileCost {
 // 256 x 256 is bound by the matrix core; the smaller the tile, the more bytes it loads for its products, and the less
 // of the chip a small problem leaves idle.
 constexpr TileCost kBf16Cost[] = {{kTile256, 256, 256, 1, 1.2f, 1.4f, 6.0f},      {kTile128, 128, 128, 1, 0.383f, 0.5f, 1.9f},
-                                  {kTile128x64, 128, 64, 1, 0.275f, 0.36f, 1.75f}, {kTile64x32, 64, 32, 3, 0.153f, 0.135f, 0.93f},
-                                  {kTile96x64, 96, 64, 1, 0.23f, 0.34f, 1.2f},    {kTile80x64, 80, 64, 1, 0.21f, 0.27f, 1.2f},
-                                  {kTile64x64, 64, 64, 1, 0.199f, 0.22f, 1.35f}};
+                                  {kTile128x64, 128, 64, 1, 0.275f, 0.36f, 1.95f}, {kTile64x32, 64, 32, 3, 0.141f, 0.135f, 0.93f},
+                                  {kTile96x64, 96, 64, 1, 0.23f, 0.34f, 1.5f},    {kTile80x64, 80, 64, 1, 0.21f, 0.27f, 1.2f},
+                                  {kTile64x64, 64, 64, 1, 0.18f, 0.22f, 1.3f}};
 constexpr TileCost kFp8Cost[] = {{kTile256, 256, 256, 1, 1.3f, 1.5f, 7.0f},       {kTile128, 128, 128, 1, 0.596f, 0.63f, 2.25f},
-                                 {kTile128x64, 128, 64, 1, 0.417f, 0.40f, 1.65f}, {kTile64x32, 64, 32, 3, 0.23f, 0.178f, 0.99f},
-                                 {kTile96x64, 96, 64, 1, 0.40f, 0.45f, 1.6f},     {kTile80x64, 80, 64, 1, 0.39f, 0.40f, 1.6f},
-                                 {kTile64x64, 64, 64, 1, 0.373f, 0.34f, 1.65f}};
+                                 {kTile128x64, 128, 64, 1, 0.417f, 0.40f, 1.6f},  {kTile64x32, 64, 32, 3, 0.236f, 0.178f, 1.0f},
+                                 {kTile96x64, 96, 64, 1, 0.42f, 0.45f, 2.2f},     {kTile80x64, 80, 64, 1, 0.38f, 0.40f, 2.15f},
+                                 {kTile64x64, 64, 64, 1, 0.362f, 0.34f, 1.8f}};
 constexpr TileCost kF32Cost[] = {{kTile128, 128, 128, 1, 1.92f, 1.92f, 2.0f},
                                  {kTile128x64, 128, 64, 1, 1.08f, 1.08f, 1.3f},
                                  {kTile64x32, 64, 32, 3, 0.39f, 0.30f, 0.8f}};
@@ -131,11 +133,11 @@ inline int size_of(int dtype) { return dtype == RDG_F32 ? 4 : dtype == RDG_BF16 
 // A wave's 2048 elements (16 waves of 128) take a time that grows with the tokens of its tile; or the weights' reading and
 // a round's start.
 float rows_us(int T, int N, int K, int dtype) {
-    const float per = dtype == RDG_F32 ? 5.0f : dtype == RDG_BF16 ? 1.06f : 0.45f;
-    const float token = dtype == RDG_F32 ? 0.6f : dtype == RDG_BF16 ? 0.097f : 0.074f;
+    const float per = dtype == RDG_F32 ? 5.0f : dtype == RDG_BF16 ? 1.5f : 0.48f;
+    const float token = dtype == RDG_F32 ? 0.6f : dtype == RDG_BF16 ? 0.125f : 0.106f;
     const int64_t rounds = ceil_div((int64_t)(N / 16) * ceil_div(T, 16), kCus);
     const float us = K / 2048.0f * (per + token * (T < 16 ? T : 16)) * rounds;
-    const float read_us = (float)N * K * size_of(dtype) / kRowsRead + 0.43f * rounds;
+    const float read_us = (float)N * K * size_of(dtype) / kRowsRead + 0.33f * rounds;
     return kStart + 0.3f + (us > read_us ? us : read_us);
 }
 
@@ -150,7 +152,10 @@ float tiles_us(const TileCost& c, int splits, int T, int N, int K, int dtype) {
             // (a token past the last costs half a line)
             const float lines = workgroups * (c.features + (c.tokens + (T < c.tokens ? T : c.tokens)) * 0.5f);
             const int64_t chip = kCus * workgroups;
-            const float few = lines * kLine + kUnderWay * c.features * (f_jobs < chip ? f_jobs : chip) + (dtype == RDG_BF16 ? 0.0f : kFewFp8);
+            const bool once = T <= c.tokens && c.tokens <= 64;
+            const float under_way = (float)c.features * (f_jobs < chip ? f_jobs : chip);
+            const float few = lines * (once ? kLineOnce : kLine) + under_way * (once ? kUnderWayOnce : kUnderWay) +
+                              (dtype == RDG_BF16 ? 0.0f : once ? kFewFp8Once : kFewFp8);
             stage = stage > few ? stage : few;
         }
         return stages * stage + c.tile;
@@ -165,8 +170,10 @@ LinearPart plan_part(int T, int N, int K, int dtype, float& least) {
     const TileCost* cost = dtype == RDG_F32 ? kF32Cost : dtype == RDG_BF16 ? kBf16Cost : kFp8Cost;
     const int kinds = dtype == RDG_F32 ? 3 : 7;
     LinearPart best{kRows, 1, N};
-    // (beyond 32 tokens the tiles are always faster)
-    least = T <= 32 ? rows_us(T, N, K, dtype) : 3e38f;
+    // (Beyond 32 tokens the tiles are always faster.)  At near equal times the rows, one launch that needs no workspace and
+    // takes less where some of the weights are still in the last cache: one token, 10240 features, K = 7168 in bf16,
+    // weights from memory 28.0 us, with two splits of 80 features 27.4; 147 MB over again 24.4, and 27.2.
+    least = T <= 32 ? 0.97f * rows_us(T, N, K, dtype) : 3e38f;
     for (int i = 0; i < kinds; ++i) {
         const int64_t tiles = ceil_div(N, cost[i].features) * ceil_div(T, cost[i].tokens);
         for (int splits = 1; splits <= 8 && splits <= K / 128; splits *= 2) {
