@@ -476,19 +476,20 @@ __global__ __launch_bounds__(WF * WT * 64, 2) void k_linear_tiled(LinearCall a, 
     }
 }
 
-// The splits' sums in their order, and the epilogue: 8 features a thread.
-__global__ __launch_bounds__(256) void k_linear_join(LinearCall a, int splits) {
+// The splits' sums in their order, and the epilogue: 8 features a thread, all its loads asked for at once.
+template <int SPLITS>
+__global__ __launch_bounds__(256) void k_linear_join(LinearCall a) {
     const int per_row = a.N / 8;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, all = (int64_t)a.T * per_row;
     if (i >= all) return;
-    float v[8], p[8];
-    load8<false>(a.parts, i * 8, v);
-    for (int s = 1; s < splits; ++s) {
-        load8<false>(a.parts, ((int64_t)s * all + i) * 8, p);
+    float p[SPLITS][8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += p[e];
-    }
-    finish8(a, v, i / per_row, (int)(i % per_row) * 8);
+    for (int s = 0; s < SPLITS; ++s) load8<false>(a.parts, ((int64_t)s * all + i) * 8, p[s]);
+#pragma unroll
+    for (int s = 1; s < SPLITS; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[0][e] += p[s][e];
+    finish8(a, p[0], i / per_row, (int)(i % per_row) * 8);
 }
 
 template <int KIND, int WF, int WT, int NF, int NTK, int NB>
@@ -505,7 +506,9 @@ hipError_t launch(const LinearCall& a, int splits, hipStream_t s) {
         k_linear_tiled<KIND, WF, WT, NF, NTK, NB, false><<<(unsigned)all, WF * WT * 64, 0, s>>>(a, (int)f_tiles, (int)t_tiles, splits);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess || splits == 1) return err;
-    k_linear_join<<<(unsigned)join, 256, 0, s>>>(a, splits);
+    if (splits == 2) k_linear_join<2><<<(unsigned)join, 256, 0, s>>>(a);
+    else if (splits == 4) k_linear_join<4><<<(unsigned)join, 256, 0, s>>>(a);
+    else k_linear_join<8><<<(unsigned)join, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 
