@@ -85,7 +85,7 @@ struct LinOp<RDG_FP8_E4M3> {
 // How a call is shared out (linear_plan in linear.hip): a kernel for some features, and one for the rest.
 enum { kRows, kTile256, kTile128, kTile128x64, kTile64x32, kTile96x64, kTile80x64, kTile64x64 };  // k_linear_rows, or the tile of k_linear_tiled
 struct LinearPart {
-    int kernel, splits, features;  // 1, 2, 4 or 8 splits of the reduction (tiles only), joined by k_linear_join
+    int kernel, splits, features;  // 1, 2, 4, 8 or 16 splits of the reduction (tiles only), joined by k_linear_join
 };
 struct LinearPlan {
     LinearPart first, rest;

@@ -176,8 +176,10 @@ LinearPart plan_part(int T, int N, int K, int dtype, float& least) {
     least = T <= 32 ? 0.97f * rows_us(T, N, K, dtype) : 3e38f;
     for (int i = 0; i < kinds; ++i) {
         const int64_t tiles = ceil_div(N, cost[i].features) * ceil_div(T, cost[i].tokens);
-        for (int splits = 1; splits <= 8 && splits <= K / 128; splits *= 2) {
-            if (splits > 1 && tiles * splits > 4 * kCus) break;  // (which also bounds the workspace: 256 MiB)
+        for (int splits = 1; splits <= 16 && splits <= K / 128; splits *= 2) {
+            // (which also bounds the workspace: 256 MiB; 16 splits beyond one round: 128 x 512 x 7168 fp8 9.8 us, 8 8.6; within
+            // one 64 x 256 x 14336 bf16 9.2 and 10.9)
+            if (splits > 1 && tiles * splits > (splits > 8 ? kCus : 4 * kCus)) break;
             const float us = tiles_us(cost[i], splits, T, N, K, dtype);
             if (us < least) least = us, best = LinearPart{cost[i].kernel, splits, N};
         }

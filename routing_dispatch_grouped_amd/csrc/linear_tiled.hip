@@ -508,7 +508,8 @@ hipError_t launch(const LinearCall& a, int splits, hipStream_t s) {
     if (err != hipSuccess || splits == 1) return err;
     if (splits == 2) k_linear_join<2><<<(unsigned)join, 256, 0, s>>>(a);
     else if (splits == 4) k_linear_join<4><<<(unsigned)join, 256, 0, s>>>(a);
-    else k_linear_join<8><<<(unsigned)join, 256, 0, s>>>(a);
+    else if (splits == 8) k_linear_join<8><<<(unsigned)join, 256, 0, s>>>(a);
+    else k_linear_join<16><<<(unsigned)join, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -237,6 +237,8 @@ LARGE = [(2300, 9232, 640), (4000, 5136, 256), (2048, 9216, 384), (700, 4112, 20
 # tiles of 64, 80 and 96 features, whose waves load unlike numbers of pieces: cut tiles, splits, tiles across two scale blocks
 LARGE += [(33, 24560, 640), (40, 24560, 1152), (49, 18416, 896), (64, 16368, 1152), (100, 9200, 1152), (64, 10256, 7168),
           (100, 2064, 7168), (250, 4112, 3968)]
+# sixteen splits
+LARGE += [(37, 528, 7168), (64, 272, 14336), (100, 48, 3968)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32", "fp8", "e8m0"])
