@@ -188,8 +188,8 @@ LinearPart plan_part(int T, int N, int K, int dtype, float& least) {
 }
 
 // Two where the last round of 256 x 256 tiles would leave much of the chip idle: whole rounds of them, and smaller tiles or
-// splits for the features behind.  bf16, 8192 x 7168 x 8192 (3.5 rounds) 695 us against 728; 2048 x 9216 x 7168
-// (1.1 rounds) 200 against 246.
+// splits for the features behind.  bf16, 8192 x 7168 x 8192 (3.5 rounds) 686 us against 707; 2048 x 9216 x 7168
+// (1.1 rounds) 196 against 276.
 LinearPlan linear_plan(int T, int N, int K, int dtype) {
     float least, rest_us;
     LinearPlan p{plan_part(T, N, K, dtype, least), LinearPart{kRows, 1, 0}};
