@@ -566,3 +566,34 @@ def test_two_graphs_that_share_a_workspace():
         for b, w in zip(blocks, want):
             for u, v in zip(b.results(), w):
                 assert torch.equal(u, v)
+
+
+def test_two_threads_on_streams_of_their_own():
+    """The binding lets go of the interpreter during a call: two threads call at once."""
+    import threading
+    blocks = [Block(100, seed=s) for s in (21, 22)]
+    want = []
+    for b in blocks:
+        b.run()
+        want.append(b.results())
+    torch.cuda.synchronize()
+    failed = []
+
+    def serve(b):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(30):
+                    b.run()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=serve, args=(b,)) for b in blocks]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for b, w in zip(blocks, want):
+        for u, v in zip(b.results(), w):
+            assert torch.equal(u, v)
