@@ -70,7 +70,7 @@ int rdg_add_norm(const void* x, int x_dtype, int64_t x_stride, int T, int H, con
 }
 
 size_t rdg_linear_workspace_bytes(int T, int N, int K, int dtype) {
-    return linear_sizes_ok(T, N, K, dtype) ? linear_workspace_bytes(T, N, K, dtype) : 0;
+    return linear_sizes_ok(T, N, K, dtype) && T > 0 ? linear_work_bytes(linear_plan(T, N, K, dtype), T) : 0;
 }
 
 int rdg_linear(const void* x, const float* x_scales, int dtype, int64_t x_stride, int T, int N, int K, const void* W,
@@ -87,14 +87,15 @@ int rdg_linear(const void* x, const float* x_scales, int dtype, int64_t x_stride
     if (bias != nullptr && !aligned16(bias)) return RDG_EINVAL;
     if (residual != nullptr && !rows_ok(residual, res_stride, N, T, size_of(out_dtype))) return RDG_EINVAL;
     if (out == x || out == W || !apart_or_same(out, residual, true, out_stride, res_stride, T)) return RDG_EINVAL;
-    const size_t need = linear_workspace_bytes(T, N, K, dtype);
+    const LinearPlan plan = linear_plan(T, N, K, dtype);
+    const size_t need = linear_work_bytes(plan, T);
     if (need > 0 && (work == nullptr || !aligned16(work) || work_bytes < need)) return RDG_EINVAL;
     LinearCall a{};
     a.x = x, a.w = W, a.x_scales = x_scales, a.w_scales = W_scales, a.bias = bias, a.residual = residual, a.out = out;
     a.parts = static_cast<float*>(work);
     a.x_stride = x_stride, a.res_stride = res_stride, a.out_stride = out_stride;
     a.T = T, a.N = N, a.K = K, a.dtype = dtype, a.act = act, a.out_bf16 = out_dtype == RDG_BF16;
-    return hip_rc(launch_linear(a, stream));
+    return hip_rc(launch_linear(a, plan, stream));
 }
 
 int rdg_route_topk(const void* logits, int dtype, int64_t logit_stride, int B, int N, int score, const float* bias,

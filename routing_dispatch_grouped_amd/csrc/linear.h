@@ -82,14 +82,8 @@ struct LinOp<RDG_FP8_E4M3> {
     }
 };
 
-// How a call is shared out (linear_plan in linear.hip): a kernel for some features, and one for the rest.
+// The kernels of a LinearPart.
 enum { kRows, kTile256, kTile128, kTile128x64, kTile64x32, kTile96x64, kTile80x64, kTile64x64 };  // k_linear_rows, or the tile of k_linear_tiled
-struct LinearPart {
-    int kernel, splits, features;  // 1, 2, 4, 8 or 16 splits of the reduction (tiles only), joined by k_linear_join
-};
-struct LinearPlan {
-    LinearPart first, rest;
-};
 
 // The activations, in fp32 by the instructions for 2^v and 1 / v (each good to an ulp; results below 2^-126 come out as 0).
 // An exponential's argument is rounded a few times, at most 3 * 128 u of its value where it is 2^-128, u = 2^-24.

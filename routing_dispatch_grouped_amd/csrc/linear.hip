@@ -187,6 +187,21 @@ LinearPart plan_part(int T, int N, int K, int dtype, float& least) {
     return best;
 }
 
+hipError_t launch_part(const LinearCall& a, const LinearPart& p, hipStream_t s) {
+    // the tiles address their token rows (at most 256) and their scales with 32 bits
+    const bool near = a.x_stride * size_of(a.dtype) * 256 < (int64_t)1 << 31;
+    if (p.kernel != kRows && near) return launch_linear_tiled(a, p, s);
+    switch (a.dtype) {
+        case RDG_F32: return launch_rows<RDG_F32, false>(a, s);
+        case RDG_BF16: return launch_rows<RDG_BF16, false>(a, s);
+        default: return a.out_bf16 ? launch_rows<RDG_FP8_E4M3, false>(a, s) : launch_rows<RDG_FP8_E4M3, true>(a, s);
+    }
+}
+
+size_t part_bytes(const LinearPart& p, int T) { return p.splits > 1 ? (size_t)p.splits * T * p.features * 4 : 0; }
+
+}  // namespace
+
 // Two where the last round of 256 x 256 tiles would leave much of the chip idle: whole rounds of them, and smaller tiles or
 // splits for the features behind.  bf16, 8192 x 7168 x 8192 (3.5 rounds) 686 us against 707; 2048 x 9216 x 7168
 // (1.1 rounds) 196 against 276.
@@ -204,24 +219,7 @@ LinearPlan linear_plan(int T, int N, int K, int dtype) {
     return p;
 }
 
-hipError_t launch_part(const LinearCall& a, const LinearPart& p, hipStream_t s) {
-    // the tiles address their token rows (at most 256) and their scales with 32 bits
-    const bool near = a.x_stride * size_of(a.dtype) * 256 < (int64_t)1 << 31;
-    if (p.kernel != kRows && near) return launch_linear_tiled(a, p, s);
-    switch (a.dtype) {
-        case RDG_F32: return launch_rows<RDG_F32, false>(a, s);
-        case RDG_BF16: return launch_rows<RDG_BF16, false>(a, s);
-        default: return a.out_bf16 ? launch_rows<RDG_FP8_E4M3, false>(a, s) : launch_rows<RDG_FP8_E4M3, true>(a, s);
-    }
-}
-
-size_t part_bytes(const LinearPart& p, int T) { return p.splits > 1 ? (size_t)p.splits * T * p.features * 4 : 0; }
-
-}  // namespace
-
-hipError_t launch_linear(const LinearCall& a, hipStream_t s) {
-    if (a.T == 0) return hipSuccess;
-    const LinearPlan p = linear_plan(a.T, a.N, a.K, a.dtype);
+hipError_t launch_linear(const LinearCall& a, const LinearPlan& p, hipStream_t s) {
     LinearCall b = a;
     b.N = p.first.features;
     hipError_t err = launch_part(b, p.first, s);
@@ -238,10 +236,8 @@ hipError_t launch_linear(const LinearCall& a, hipStream_t s) {
     return launch_part(b, p.rest, s);
 }
 
-size_t linear_workspace_bytes(int T, int N, int K, int dtype) {
-    if (T == 0) return 0;
+size_t linear_work_bytes(const LinearPlan& p, int T) {
     // the parts' launches run one after the other, and only the second has splits
-    const LinearPlan p = linear_plan(T, N, K, dtype);
     const size_t first = part_bytes(p.first, T), rest = part_bytes(p.rest, T);
     return first > rest ? first : rest;
 }

@@ -304,9 +304,16 @@ struct LinearCall {
     int T, N, K, dtype, act;
     bool out_bf16;
 };
-size_t linear_workspace_bytes(int T, int N, int K, int dtype);
-hipError_t launch_linear(const LinearCall& a, hipStream_t s);
-struct LinearPart;
+// How a call is shared out: a kernel for some features, and one for the rest.
+struct LinearPart {
+    int kernel, splits, features;  // 1, 2, 4, 8 or 16 splits of the reduction (tiles only), joined by k_linear_join
+};
+struct LinearPlan {
+    LinearPart first, rest;
+};
+LinearPlan linear_plan(int T, int N, int K, int dtype);
+size_t linear_work_bytes(const LinearPlan& p, int T);
+hipError_t launch_linear(const LinearCall& a, const LinearPlan& p, hipStream_t s);
 hipError_t launch_linear_tiled(const LinearCall& a, const LinearPart& p, hipStream_t s);
 
 struct RouteCall {
