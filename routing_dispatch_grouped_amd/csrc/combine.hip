@@ -252,13 +252,14 @@ struct Raw<RDG_F32> {
 // has published are read past this CU's L1 and any stale line of this XCD's
 // L2 (device scope), streamed (nt), and land in LDS without occupying
 // registers, so a wave can have many of them in flight.  Issued from inline
-// assembly; the caller waits for them (vmcnt) before reading the LDS.
+// assembly (with the wait state that a load into LDS needs behind the write of
+// m0); the caller waits for them (vmcnt) before reading the LDS.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16_device_scope(const void* src, const void* lds) {
     typedef __attribute__((address_space(3))) void* lds_ptr_t;
     const uint32_t l = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr_t)lds);
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off sc1 nt" ::"v"(src), "s"(l) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off sc1 nt" ::"v"(src), "s"(l) : "memory", "m0");
 }
 #pragma clang diagnostic pop
 

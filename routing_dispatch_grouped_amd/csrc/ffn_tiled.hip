@@ -241,6 +241,7 @@ __device__ __forceinline__ void lds_barrier() {
 // wait the compiler adds can only wait longer, as loads complete in order.
 // fp8 tiles use the assembly form (gate/up and down 3% faster); bf16 tiles,
 // whose chunk is one MFMA step deep, keep the builtin (1% faster there).
+// A load into LDS needs a wait state behind the write of m0 (the builtin has it from the compiler).
 // The kernels use m0 for nothing else (clang warns about clobbering it).
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
@@ -248,14 +249,14 @@ template <bool ASM>
 __device__ __forceinline__ void dma16(const void* src, const void* lds) {
     if constexpr (ASM) {
         const uint32_t l = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr_t)lds);
-        asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(l) : "memory", "m0");
+        asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(l) : "memory", "m0");
     } else {
         __builtin_amdgcn_global_load_lds((gbl_ptr_t)src, (lds_ptr_t)lds, 16, 0, 0);
     }
 }
 __device__ __forceinline__ void dma4(const void* src, const void* lds) {
     const uint32_t l = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr_t)lds);
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(l) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(l) : "memory", "m0");
 }
 #pragma clang diagnostic pop
 

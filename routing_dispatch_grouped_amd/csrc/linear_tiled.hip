@@ -44,24 +44,29 @@ enum { kBf16 = 0, kFp8 = 1, kE8m0 = 2, kFp8Wide = 3, kF32 = 4 };
 #pragma clang diagnostic ignored "-Winline-asm"
 // 16 (4) bytes a lane from base + off + IMM straight to lds + IMM + 16 (4) * lane (base and lds wave-uniform); with
 // TEST where `now` < `end`; with ONCE past the caches.  The compiler does not count these loads: meet() below waits for
-// them.  The branch is in the assembly, as the compiler would move matrix instructions past one of its own.
-#define RDG_LOAD(how) "s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1 offset:%3" how
+// them.  The branch is in the assembly, as the compiler would move matrix instructions past one of its own.  A load into
+// LDS comes an instruction behind the write of m0 at the earliest: the branch, or an s_nop.
+#define RDG_M0 "s_mov_b32 m0, %2\n\t"
+#define RDG_LOAD(how) "global_load_lds_dwordx4 %0, %1 offset:%3" how
 #define RDG_UNLESS "s_cmp_ge_i32 %4, %5\n\ts_cbranch_scc1 1f\n\t"
+#define RDG_WAIT "s_nop 0\n\t"
 template <int IMM, bool TEST, bool ONCE>
 __device__ __forceinline__ void dma16(int now, int end, const uint8_t* base, uint32_t off, uint32_t lds) {
     if constexpr (TEST && ONCE)
-        asm volatile(RDG_UNLESS RDG_LOAD(" nt\n1:") ::"v"(off), "s"(base), "s"(lds), "n"(IMM), "s"(now), "s"(end) : "memory", "m0", "scc");
+        asm volatile(RDG_M0 RDG_UNLESS RDG_LOAD(" nt\n1:") ::"v"(off), "s"(base), "s"(lds), "n"(IMM), "s"(now), "s"(end) : "memory", "m0", "scc");
     else if constexpr (TEST)
-        asm volatile(RDG_UNLESS RDG_LOAD("\n1:") ::"v"(off), "s"(base), "s"(lds), "n"(IMM), "s"(now), "s"(end) : "memory", "m0", "scc");
+        asm volatile(RDG_M0 RDG_UNLESS RDG_LOAD("\n1:") ::"v"(off), "s"(base), "s"(lds), "n"(IMM), "s"(now), "s"(end) : "memory", "m0", "scc");
     else if constexpr (ONCE)
-        asm volatile(RDG_LOAD(" nt") ::"v"(off), "s"(base), "s"(lds), "n"(IMM) : "memory", "m0");
+        asm volatile(RDG_M0 RDG_WAIT RDG_LOAD(" nt") ::"v"(off), "s"(base), "s"(lds), "n"(IMM) : "memory", "m0");
     else
-        asm volatile(RDG_LOAD("") ::"v"(off), "s"(base), "s"(lds), "n"(IMM) : "memory", "m0");
+        asm volatile(RDG_M0 RDG_WAIT RDG_LOAD("") ::"v"(off), "s"(base), "s"(lds), "n"(IMM) : "memory", "m0");
 }
+#undef RDG_M0
 #undef RDG_LOAD
 #undef RDG_UNLESS
+#undef RDG_WAIT
 __device__ __forceinline__ void dma4(int now, int end, const void* base, uint32_t off, uint32_t lds) {
-    asm volatile("s_cmp_ge_i32 %3, %4\n\ts_cbranch_scc1 1f\n\ts_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1\n1:" ::"v"(off), "s"(base),
+    asm volatile("s_mov_b32 m0, %2\n\ts_cmp_ge_i32 %3, %4\n\ts_cbranch_scc1 1f\n\tglobal_load_lds_dword %0, %1\n1:" ::"v"(off), "s"(base),
                  "s"(lds), "s"(now), "s"(end)
                  : "memory", "m0", "scc");
 }
