@@ -20,10 +20,11 @@ namespace {
 // wave 28; 16 tokens on 256 features of K = 4096: 7.9 us against 10.9.  Loading the next block during the
 // products, 24.1 us at 16 waves for twice the registers, gained nothing elsewhere.
 // A token tile's loads touch 16 rows, so their time grows with the tokens: rows_us below.
-// WIDE (fp8): products of bf16 operands.
+// e4m3 products are taken from bf16 operands (LinOp::mma_wide): one token on 18432 features of K = 7168 takes 21.7 us either
+// way, eight tokens 24.7 and 24.6.
 constexpr int NW = 16;
 
-template <int DT, bool WIDE>
+template <int DT>
 __global__ __launch_bounds__(NW * 64) void k_linear_rows(LinearCall a) {
     using O = LinOp<DT>;
     using op_t = typename O::op_t;
@@ -60,7 +61,7 @@ __global__ __launch_bounds__(NW * 64) void k_linear_rows(LinearCall a) {
                 if constexpr (FP8) {
                     const float scale = xs[kb] * ws[kb];
                     const f32x4_t z = {0.f, 0.f, 0.f, 0.f};
-                    acc += (WIDE ? O::mma_wide(z, rw[0], rx[0]) : O::mma(z, rw[0], rx[0])) * scale;
+                    acc += O::mma_wide(z, rw[0], rx[0]) * scale;
                 } else {
 #pragma unroll
                     for (int u = 0; u < U; ++u) acc = O::mma(acc, rw[u], rx[u]);
@@ -81,11 +82,11 @@ __global__ __launch_bounds__(NW * 64) void k_linear_rows(LinearCall a) {
     finish4(a, v, mine, group * 16 + (lane >> 4) * 4);
 }
 
-template <int DT, bool WIDE>
+template <int DT>
 hipError_t launch_rows(const LinearCall& a, hipStream_t s) {
     const int64_t blocks = (int64_t)(a.N / 16) * (((int64_t)a.T + 15) / 16);
     if (!grid_fits(blocks, NW * 64)) return hipErrorInvalidConfiguration;
-    k_linear_rows<DT, WIDE><<<(unsigned)blocks, NW * 64, 0, s>>>(a);
+    k_linear_rows<DT><<<(unsigned)blocks, NW * 64, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -192,9 +193,9 @@ hipError_t launch_part(const LinearCall& a, const LinearPart& p, hipStream_t s) 
     const bool near = a.x_stride * size_of(a.dtype) * 256 < (int64_t)1 << 31;
     if (p.kernel != kRows && near) return launch_linear_tiled(a, p, s);
     switch (a.dtype) {
-        case RDG_F32: return launch_rows<RDG_F32, false>(a, s);
-        case RDG_BF16: return launch_rows<RDG_BF16, false>(a, s);
-        default: return a.out_bf16 ? launch_rows<RDG_FP8_E4M3, false>(a, s) : launch_rows<RDG_FP8_E4M3, true>(a, s);
+        case RDG_F32: return launch_rows<RDG_F32>(a, s);
+        case RDG_BF16: return launch_rows<RDG_BF16>(a, s);
+        default: return launch_rows<RDG_FP8_E4M3>(a, s);
     }
 }
 

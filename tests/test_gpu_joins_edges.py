@@ -1,0 +1,83 @@
+"""The joins of a decoder layer where their arithmetic or their plans could go wrong: sums of 8-bit products of unlike
+sizes.
+
+The matrix core adds e4m3 products eight at a time (consecutive elements), each cut to a multiple of 2^-13 of the
+power of two of the largest of them, P = 2^(the operands' exponents together, -6 for subnormal ones); the
+sums of eight are added as fp32 holds them.  So up to seven products lose less than 2^-13 P each.
+
+Tolerances (u = 2^-24): 2 (K + 8) u of the sum of magnitudes for sums in fp32 whose blocks are scaled; 7 2^-13 P of
+every eight products where e4m3 operands go to the matrix core as they are; half a step of the output's type.
+"""
+import numpy as np
+import pytest
+import torch
+
+from harness import DEV, rdg
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+BF, F32, F8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+HALF = {BF: 2.0 ** -8, F32: 2.0 ** -24}
+
+
+def work_for(T, N, K, dtype):
+    n = rdg().rdg_linear_workspace_bytes(T, N, K, dtype)
+    return torch.full((n,), 0xff, dtype=torch.uint8, device=DEV) if n else None
+
+
+def code_of(kind):
+    m = rdg()
+    return dict(bf16=m.RDG_BF16, f32=m.RDG_F32, fp8=m.RDG_FP8_E4M3, e8m0=m.RDG_FP8_E4M3_UE8M0)[kind]
+
+
+def packed(w, code):
+    p = torch.empty_like(w)
+    rdg().rdg_pack_weights(w, code, p)
+    return p
+
+
+# ---------------------------------------------------------------- 8-bit sums
+def any_codes(g, *shape):
+    """e4m3 values whose exponents are as likely: products from 2^-18 to 2^17 side by side."""
+    c = torch.randint(0, 0x7f, shape, device=DEV, generator=g, dtype=torch.uint8)
+    return (c | torch.randint(0, 2, shape, device=DEV, generator=g, dtype=torch.uint8) << 7).view(F8)
+
+
+def power_of(v):
+    """2^exponent of e4m3 values, 2^-6 for subnormal ones, 0 for zeros."""
+    p = torch.exp2(torch.frexp(v.double().abs())[1].double() - 1).clamp(min=2.0 ** -6)
+    return torch.where(v.double() == 0, 0.0, p)
+
+
+@pytest.mark.parametrize("kind", ["fp8", "e8m0"])
+@pytest.mark.parametrize("T,N,K", [(1, 64, 128), (4, 48, 256), (8, 256, 4096), (40, 80, 384), (70, 144, 1024), (300, 272, 512)])
+def test_sums_of_8_bit_products_of_unlike_sizes(T, N, K, kind):
+    """The residual takes the sum away, so that the 16-bit output shows what the sum lost."""
+    m = rdg()
+    g = torch.Generator(device=DEV).manual_seed(T + N + K)
+    code = code_of(kind)
+    x, w = any_codes(g, T, K), any_codes(g, N, K)
+    scale = lambda *s: (torch.exp2(torch.randint(-2, 3, s, device=DEV, generator=g).float()) if kind == "e8m0"  # noqa: E731
+                        else 0.25 + torch.rand(*s, device=DEV, generator=g))
+    xs, ws = scale(T, K // 128), scale(-(-N // 128), K // 128)
+    wide_x, wide_w = xs.double().repeat_interleave(128, 1), ws.double().repeat_interleave(128, 1).repeat_interleave(128, 0)[:N]
+    a, b = x.double() * wide_x, w.double() * wide_w
+    want, size = (a @ b.T).cpu(), (a.abs() @ b.abs().T).cpu()
+    # the largest power of two of every eight products, scaled
+    p, q = (power_of(x) * wide_x).cpu(), (power_of(w) * wide_w).cpu()
+    cut = torch.zeros(T, N, dtype=torch.float64)
+    for k in range(0, K, 8):
+        cut += (p[:, None, k:k + 8] * q[None, :, k:k + 8]).amax(-1)
+    pw = packed(w, code)
+    for out_type in (BF, F32):
+        res = (-want).to(DEV).to(out_type)
+        out = torch.empty(T, N, dtype=out_type, device=DEV)
+        m.rdg_linear(x, xs, code, pw, ws, out, residual=res, work=work_for(T, N, K, code))
+        left = want + res.double().cpu()
+        tol = 2 * (K + 8) * U * size
+        if out_type == BF and T > 4:      # (the kernel for few tokens takes its products from bf16 operands)
+            tol = tol + 7 * 2.0 ** -13 * cut
+        tol = tol + HALF[out_type] * (left.abs() + tol) + 2 * U * want.abs()
+        err = (out.double().cpu() - left).abs()
+        assert (err <= tol).all(), (out_type, float((err / tol).max()))
