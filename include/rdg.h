@@ -596,7 +596,7 @@ int rdg_add_norm(const void* x, int x_dtype, int64_t x_stride, int T, int H, con
  *   W         [N, K] in dtype, packed by rdg_pack_weights (n_mat = 1), with W_scales
  *             [ceil(N/128), K/128] for fp8, as rdg_quantize_fp8 with block_rows 128 gives them
  *   bias      [N] fp32 or NULL
- *   act       RDG_ACT_*
+ *   act       RDG_ACT_*; an infinite sum gives +inf, or, from -inf, 0 (relu) or NaN (-inf times a factor of 0)
  *   residual  [T, res_stride] rows of N elements in out_dtype, or NULL; may be out where
  *             the stride is the same
  *   out       [T, out_stride] rows of N elements: RDG_F32 or RDG_BF16 (fp32 operands:

@@ -81,3 +81,51 @@ def test_sums_of_8_bit_products_of_unlike_sizes(T, N, K, kind):
         tol = tol + HALF[out_type] * (left.abs() + tol) + 2 * U * want.abs()
         err = (out.double().cpu() - left).abs()
         assert (err <= tol).all(), (out_type, float((err / tol).max()))
+
+
+# ---------------------------------------------------------------- activations of sums that are not finite
+@pytest.mark.parametrize("T", [2, 70])
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
+def test_activations_of_infinite_and_huge_sums(act, T):
+    """As the formulas have them: y max(0, sign y) at +inf and beyond what fp32's exponentials hold; at -inf
+    relu is 0, and y times a factor of 0 is NaN, as are NaN."""
+    m = rdg()
+    inf, nan, big = float("inf"), float("nan"), torch.finfo(F32).max
+    bias = torch.tensor([inf, -inf, nan, big, -big, 1e20, -1e20, 40.0, -40.0, 1000.0, -1000.0, 0.0, -0.0, 13.0, 1e-30, -1e-30], device=DEV)
+    code = [m.RDG_ACT_NONE, m.RDG_ACT_RELU, m.RDG_ACT_SILU, m.RDG_ACT_GELU, m.RDG_ACT_GELU_TANH]
+    code = code[["none", "relu", "silu", "gelu", "gelu_tanh"].index(act)]
+    for dtype in (BF, F32):
+        x, w = torch.zeros(T, 128, dtype=dtype, device=DEV), torch.ones(16, 128, dtype=dtype, device=DEV)
+        out = torch.empty(T, 16, device=DEV)
+        c = m.RDG_BF16 if dtype == BF else m.RDG_F32
+        m.rdg_linear(x, None, c, packed(w, c), None, out, bias=bias, act=code, work=work_for(T, 16, 128, c))
+        y = bias.double().cpu()
+        if act == "none":
+            want = y
+        elif act == "relu":
+            want = torch.where(y < 0, 0.0, y)
+        else:
+            small = {"silu": torch.sigmoid(y), "gelu": 0.5 * torch.erfc(-y / 2 ** 0.5),
+                     "gelu_tanh": torch.sigmoid((8 / torch.pi) ** 0.5 * (y + 0.044715 * y ** 3))}[act]
+            want = y * small
+        got = out.double().cpu()
+        for row in got:
+            assert torch.equal(row.isnan(), want.isnan())
+            finite = want.isfinite()
+            assert torch.equal(row[~finite & ~want.isnan()], want[~finite & ~want.isnan()])
+            # 512 u: an exponential's argument of at most 128 rounded four times; results below 2^-126 may be 0
+            assert ((row - want)[finite].abs() <= 512 * U * want[finite].abs() + 2.0 ** -126).all()
+
+
+def test_a_sum_that_overflows_comes_out_as_its_activation_of_infinity():
+    m = rdg()
+    for T in (2, 70):
+        x, w = torch.full((T, 128), 2.0 ** 100, dtype=BF, device=DEV), torch.full((16, 128), 2.0 ** 27, dtype=BF, device=DEV)
+        w[1::2] *= -1
+        p = packed(w, m.RDG_BF16)
+        for act, low in ((m.RDG_ACT_NONE, -float("inf")), (m.RDG_ACT_RELU, 0.0), (m.RDG_ACT_SILU, None), (m.RDG_ACT_GELU, None),
+                         (m.RDG_ACT_GELU_TANH, None)):
+            out = torch.empty(T, 16, device=DEV)
+            m.rdg_linear(x, None, m.RDG_BF16, p, None, out, act=act, work=work_for(T, 16, 128, m.RDG_BF16))
+            assert (out[:, ::2] == float("inf")).all()
+            assert out[:, 1::2].isnan().all() if low is None else (out[:, 1::2] == low).all()
