@@ -42,6 +42,9 @@ class DecoderLayer:
         self.p_qkv, self.p_o, self.p_router = packed(self.w_qkv), packed(self.w_o), packed(self.router)
         self.w1, self.w3 = packed(weight(n_experts, inner, hidden)), packed(weight(n_experts, inner, hidden))
         self.w2 = packed(weight(n_experts, hidden, inner))
+        # one workspace for the three products, of up to max_tokens
+        self.work = torch.empty(max(rdg.rdg_linear_workspace_bound(max_tokens, *w.shape, rdg.RDG_BF16)
+                                    for w in (self.p_qkv, self.p_o, self.p_router)), dtype=torch.uint8, device=device)
         angle = torch.arange(max_context, device=device)[:, None] * 10000.0 ** (
             -torch.arange(0, head_dim, 2, device=device) / head_dim)
         self.cos_sin = torch.cat([angle.cos(), angle.sin()], 1).float().contiguous()
@@ -67,13 +70,10 @@ class DecoderLayer:
         rdg.rdg_add_norm(x, None, 1e-6, out=out)
         return out
 
-    @staticmethod
-    def linear(x, w, dtype=torch.bfloat16, residual=None):
+    def linear(self, x, w, dtype=torch.bfloat16, residual=None):
         """x @ W.T (+ residual), W packed"""
-        (T, K), N = x.shape, w.shape[0]
-        out = torch.empty(T, N, dtype=dtype, device=x.device)
-        work = torch.empty(rdg.rdg_linear_workspace_bytes(T, N, K, rdg.RDG_BF16), dtype=torch.uint8, device=x.device)
-        rdg.rdg_linear(x, None, rdg.RDG_BF16, w, None, out, residual=residual, work=work)
+        out = torch.empty(x.shape[0], w.shape[0], dtype=dtype, device=x.device)
+        rdg.rdg_linear(x, None, rdg.RDG_BF16, w, None, out, residual=residual, work=self.work)
         return out
 
     def attention(self, x, max_q):

@@ -602,7 +602,9 @@ int rdg_add_norm(const void* x, int x_dtype, int64_t x_stride, int T, int H, con
  *   out       [T, out_stride] rows of N elements: RDG_F32 or RDG_BF16 (fp32 operands:
  *             RDG_F32, else RDG_EUNSUPPORTED)
  *   work      rdg_linear_workspace_bytes(T, N, K, dtype) bytes, at most 256 MiB (NULL when that is
- *             0); nothing in it needs clearing.  Calls that overlap need workspaces of their own
+ *             0); nothing in it needs clearing.  Calls that overlap need workspaces of their own.  The size
+ *             rises and falls with T (0 for many T); rdg_linear_workspace_bound(T, N, K, dtype) bytes, also at most
+ *             256 MiB, do for every call of up to T tokens
  * N is a multiple of 16, K of 128.  Products are summed in fp32 (fp8: of every 128,
  * then scaled by both blocks' scales in fp32), and everything up to the one rounding of out is
  * fp32.  (fp8 to RDG_BF16 with more than a few tokens: the matrix core adds the products of eight consecutive elements with
@@ -611,6 +613,7 @@ int rdg_add_norm(const void* x, int x_dtype, int64_t x_stride, int T, int H, con
  * and are added as fp32 holds them, at half the rate.)  Deterministic; a
  * token's sums do not depend on the other tokens' values, but their order may on T.  T = 0 is a no-op. */
 size_t rdg_linear_workspace_bytes(int T, int N, int K, int dtype);
+size_t rdg_linear_workspace_bound(int T, int N, int K, int dtype);
 int rdg_linear(const void* x, const float* x_scales, int dtype, int64_t x_stride, int T, int N, int K, const void* W,
                const float* W_scales, const float* bias, int act, const void* residual, int64_t res_stride, void* out,
                int out_dtype, int64_t out_stride, void* work, size_t work_bytes, rdg_stream_t stream);

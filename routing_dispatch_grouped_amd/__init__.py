@@ -89,6 +89,7 @@ _SIGS = {
     "rdg_paged_attention": ([_P, _I, _I64, _I, _I, _SP, _CP, _I, _I, _F, _I, _I, _P, _I64, _P, _P, _SZ, _P], _I),
     "rdg_add_norm": ([_P, _I, _I64, _I, _I, _P, _P, _I, _I64, _P, _F, _P, _I64, _P, _P, _I, _P], _I),
     "rdg_linear_workspace_bytes": ([_I, _I, _I, _I], _SZ),
+    "rdg_linear_workspace_bound": ([_I, _I, _I, _I], _SZ),
     "rdg_linear": ([_P, _P, _I, _I64, _I, _I, _I, _P, _P, _P, _I, _P, _I64, _P, _I, _I64, _P, _SZ, _P], _I),
     "rdg_route_topk": ([_P, _I, _I64, _I, _I, _I, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P], _I),
     "rdg_check_status": ([_P, _P, _P], _I),
@@ -500,10 +501,15 @@ def rdg_linear_workspace_bytes(T, N, K, dtype):
     return int(_lib.rdg_linear_workspace_bytes(T, N, K, dtype))
 
 
+def rdg_linear_workspace_bound(T, N, K, dtype):
+    """Bytes that do for every call of up to T tokens."""
+    return int(_lib.rdg_linear_workspace_bound(T, N, K, dtype))
+
+
 def rdg_linear(x, x_scales, dtype, W, W_scales, out, bias=None, act=RDG_ACT_NONE, residual=None, work=None, stream=None):
     """x [T, K] (row stride free; fp8 codes as uint8 or float8_e4m3fn) with x_scales [T, K/128] float32, W [N, K] packed
     with W_scales [ceil(N/128), K/128], out, residual [T, N] bfloat16 or float32 (row strides free), bias [N] float32;
-    work: a uint8 tensor of rdg_linear_workspace_bytes."""
+    work: a uint8 tensor of rdg_linear_workspace_bytes, or rdg_linear_workspace_bound of the most tokens."""
     if _cpp is None:
         _bind_torch()
     r = _cpp.linear(x, x_scales, dtype, W, W_scales, out, bias, act, residual, work, _device_of(),

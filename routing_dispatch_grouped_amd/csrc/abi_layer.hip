@@ -73,6 +73,10 @@ size_t rdg_linear_workspace_bytes(int T, int N, int K, int dtype) {
     return linear_sizes_ok(T, N, K, dtype) && T > 0 ? linear_work_bytes(linear_plan(T, N, K, dtype), T) : 0;
 }
 
+size_t rdg_linear_workspace_bound(int T, int N, int K, int dtype) {
+    return linear_sizes_ok(T, N, K, dtype) ? linear_work_bound(T, N, K, dtype) : 0;
+}
+
 int rdg_linear(const void* x, const float* x_scales, int dtype, int64_t x_stride, int T, int N, int K, const void* W,
                const float* W_scales, const float* bias, int act, const void* residual, int64_t res_stride, void* out,
                int out_dtype, int64_t out_stride, void* work, size_t work_bytes, rdg_stream_t stream) {

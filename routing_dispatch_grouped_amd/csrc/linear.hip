@@ -166,10 +166,20 @@ float tiles_us(const TileCost& c, int splits, int T, int N, int K, int dtype) {
     return kStart + (us > read_us ? us : read_us) + (splits > 1 ? kJoin + (float)splits * T * N * 8 / kJoinRate : 0.0f);
 }
 
+const TileCost* costs(int dtype, int& kinds) {
+    kinds = dtype == RDG_F32 ? 3 : 7;
+    return dtype == RDG_F32 ? kF32Cost : dtype == RDG_BF16 ? kBf16Cost : kFp8Cost;
+}
+
+// The most tiles whose reduction is split so often, which also bounds the workspace: 256 MiB.  (16 splits beyond one round:
+// 128 x 512 x 7168 fp8 9.8 us, 8 8.6; within one 64 x 256 x 14336 bf16 9.2 and 10.9.)
+constexpr int kMostSplits = 16;
+constexpr int most_tiles(int splits) { return (splits > 8 ? kCus : 4 * kCus) / splits; }
+
 // One kernel for all features.
 LinearPart plan_part(int T, int N, int K, int dtype, float& least) {
-    const TileCost* cost = dtype == RDG_F32 ? kF32Cost : dtype == RDG_BF16 ? kBf16Cost : kFp8Cost;
-    const int kinds = dtype == RDG_F32 ? 3 : 7;
+    int kinds;
+    const TileCost* cost = costs(dtype, kinds);
     LinearPart best{kRows, 1, N};
     // (Beyond 32 tokens the tiles are always faster.)  At near equal times the rows, one launch that needs no workspace and
     // takes less where some of the weights are still in the last cache: one token, 10240 features, K = 7168 in bf16,
@@ -177,10 +187,8 @@ LinearPart plan_part(int T, int N, int K, int dtype, float& least) {
     least = T <= 32 ? 0.97f * rows_us(T, N, K, dtype) : 3e38f;
     for (int i = 0; i < kinds; ++i) {
         const int64_t tiles = ceil_div(N, cost[i].features) * ceil_div(T, cost[i].tokens);
-        for (int splits = 1; splits <= 16 && splits <= K / 128; splits *= 2) {
-            // (which also bounds the workspace: 256 MiB; 16 splits beyond one round: 128 x 512 x 7168 fp8 9.8 us, 8 8.6; within
-            // one 64 x 256 x 14336 bf16 9.2 and 10.9)
-            if (splits > 1 && tiles * splits > (splits > 8 ? kCus : 4 * kCus)) break;
+        for (int splits = 1; splits <= kMostSplits && splits <= K / 128; splits *= 2) {
+            if (splits > 1 && tiles > most_tiles(splits)) break;
             const float us = tiles_us(cost[i], splits, T, N, K, dtype);
             if (us < least) least = us, best = LinearPart{cost[i].kernel, splits, N};
         }
@@ -241,6 +249,20 @@ size_t linear_work_bytes(const LinearPlan& p, int T) {
     // the parts' launches run one after the other, and only the second has splits
     const size_t first = part_bytes(p.first, T), rest = part_bytes(p.rest, T);
     return first > rest ? first : rest;
+}
+
+// Of every kind of tile and number of splits the outputs of the most tiles that may have so many, but no more than there are.
+size_t linear_work_bound(int T, int N, int K, int dtype) {
+    int kinds;
+    const TileCost* cost = costs(dtype, kinds);
+    int64_t most = 0;
+    for (int i = 0; i < kinds; ++i)
+        for (int splits = 2; splits <= kMostSplits && splits <= K / 128; splits *= 2) {
+            const int64_t held = (int64_t)most_tiles(splits) * cost[i].features * cost[i].tokens, outputs = (int64_t)T * N;
+            const int64_t bytes = 4 * splits * (held < outputs ? held : outputs);
+            most = most > bytes ? most : bytes;
+        }
+    return (size_t)most;
 }
 
 }  // namespace rdg

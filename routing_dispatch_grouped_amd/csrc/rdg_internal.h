@@ -313,6 +313,7 @@ struct LinearPlan {
 };
 LinearPlan linear_plan(int T, int N, int K, int dtype);
 size_t linear_work_bytes(const LinearPlan& p, int T);
+size_t linear_work_bound(int T, int N, int K, int dtype);  // no less than the plans' of up to T tokens
 hipError_t launch_linear(const LinearCall& a, const LinearPlan& p, hipStream_t s);
 hipError_t launch_linear_tiled(const LinearCall& a, const LinearPart& p, hipStream_t s);
 

@@ -129,3 +129,26 @@ def test_a_sum_that_overflows_comes_out_as_its_activation_of_infinity():
             m.rdg_linear(x, None, m.RDG_BF16, p, None, out, act=act, work=work_for(T, 16, 128, m.RDG_BF16))
             assert (out[:, ::2] == float("inf")).all()
             assert out[:, 1::2].isnan().all() if low is None else (out[:, 1::2] == low).all()
+
+
+# ---------------------------------------------------------------- one workspace for all batches
+@pytest.mark.parametrize("kind", ["bf16", "f32", "fp8", "e8m0"])
+def test_one_workspace_for_all_batches(kind):
+    """Sized once for the most tokens: every batch up to them runs, and whole numbers come out exactly."""
+    m = rdg()
+    code, most, N, K = code_of(kind), 1300, 2064, 3968
+    g = torch.Generator(device=DEV).manual_seed(3)
+    nat = {"bf16": BF, "f32": F32}.get(kind, F8)
+    x, w = (torch.randint(-3, 4, (n, K), device=DEV, generator=g).float() for n in (most, N))
+    want = x.double() @ w.double().T
+    xs = torch.ones(most, K // 128, device=DEV) if nat is F8 else None
+    ws = torch.ones(-(-N // 128), K // 128, device=DEV) if nat is F8 else None
+    p, x = packed(w.to(nat), code), x.to(nat)
+    work = torch.empty(m.rdg_linear_workspace_bound(most, N, K, code), dtype=torch.uint8, device=DEV)
+    sizes = [1, 2, 9, 16, 17, 33, 64, 100, 160, 257, 300, 512, 777, 1024, 1300]
+    assert len({m.rdg_linear_workspace_bytes(T, N, K, code) for T in sizes}) > 2
+    for T in sizes:
+        work.fill_(0xff)
+        out = torch.full((T, N), float("nan"), device=DEV)
+        m.rdg_linear(x[:T], None if xs is None else xs[:T], code, p, ws, out, work=work)
+        assert torch.equal(out.double(), want[:T]), T
