@@ -35,6 +35,8 @@ class DecoderLayer:
         self.router = weight(n_experts, hidden)
 
         def packed(w):
+            if w.dim() == 2:  # products take rows by sixteens and columns by blocks of 128: zeros fill them up
+                w = torch.nn.functional.pad(w, (0, -w.shape[1] % 128, 0, -w.shape[0] % 16))
             p = torch.empty_like(w)
             rdg.rdg_pack_weights(w, rdg.RDG_BF16, p)
             return p
@@ -72,6 +74,8 @@ class DecoderLayer:
 
     def linear(self, x, w, dtype=torch.bfloat16, residual=None):
         """x @ W.T (+ residual), W packed"""
+        if x.shape[1] < w.shape[1]:
+            x = torch.nn.functional.pad(x, (0, w.shape[1] - x.shape[1]))
         out = torch.empty(x.shape[0], w.shape[0], dtype=dtype, device=x.device)
         rdg.rdg_linear(x, None, rdg.RDG_BF16, w, None, out, residual=residual, work=self.work)
         return out
@@ -89,13 +93,16 @@ class DecoderLayer:
         rdg.rdg_paged_attention(q, self.step, self.cache, max_q, self.max_context, D ** -0.5, out, work=work)
         return self.linear(out.view(T, -1), self.p_o, residual=x)
 
+    def logits(self, n):
+        """The router's, of the experts that there are: rows may be apart."""
+        return self.linear(n, self.p_router, torch.float32)[:, :self.N]
+
     def experts(self, x):
         T, H, K = x.shape[0], self.H, self.K
         n = self.norm(x)
         ids = torch.empty(T, K, dtype=torch.int32, device=self.dev)
         w = torch.empty(T, K, dtype=torch.float32, device=self.dev)
-        logits = self.linear(n, self.p_router, torch.float32)
-        rdg.rdg_route_topk(logits, self.score, 4, 2, 2, K, True, 1.0, ids, w)
+        rdg.rdg_route_topk(self.logits(n), self.score, 4, 2, 2, K, True, 1.0, ids, w)
         L = rdg.Layout(rdg.RDG_CONTIGUOUS, self.N, T, K, self.dev, block_m=16)
         rdg.rdg_dispatch(n, None, rdg.RDG_BF16, ids, L, None)
         h = torch.empty(L.m_cap, self.I, dtype=x.dtype, device=self.dev)

@@ -605,7 +605,8 @@ int rdg_add_norm(const void* x, int x_dtype, int64_t x_stride, int T, int H, con
  *             0); nothing in it needs clearing.  Calls that overlap need workspaces of their own.  The size
  *             rises and falls with T (0 for many T); rdg_linear_workspace_bound(T, N, K, dtype) bytes, also at most
  *             256 MiB, do for every call of up to T tokens
- * N is a multiple of 16, K of 128.  Products are summed in fp32 (fp8: of every 128,
+ * N is a multiple of 16, K of 128, as rdg_pack_weights takes them (a router of 8 experts: rows of zeros fill W up, and
+ * rdg_route_topk reads the first columns of out).  Products are summed in fp32 (fp8: of every 128,
  * then scaled by both blocks' scales in fp32), and everything up to the one rounding of out is
  * fp32.  (fp8 to RDG_BF16 with more than a few tokens: the matrix core adds the products of eight consecutive elements with
  * each cut to a multiple of 2^-13 of the power of two of the largest, which on even terms is 1.5e-5 of a sum and at most
