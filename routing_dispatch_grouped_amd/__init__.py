@@ -46,9 +46,9 @@ class rdg_kv_step(ctypes.Structure):
                 ("status", ctypes.c_void_p), ("work", ctypes.c_void_p)]
 
 
-if not (os.path.exists(LIB_PATH) and os.path.exists(os.path.join(_HERE, "_binding.so"))):
-    raise ImportError("librdg.so or _binding.so is not built (run routing_dispatch_grouped_amd/_build.py or "
-                      "__graft_entry__.build()); there is no fallback implementation")
+_NOT_BUILT = "%s is not built (run routing_dispatch_grouped_amd/_build.py or __graft_entry__.build()); there is no fallback implementation"
+if not os.path.exists(LIB_PATH):
+    raise ImportError(_NOT_BUILT % "librdg.so")
 
 _lib = ctypes.CDLL(LIB_PATH)
 _P, _I, _I64, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
@@ -121,18 +121,28 @@ def _check(rc, what):
         raise RdgError(rc, what)
 
 
-# torch, its current-stream lookup and the part of the binding that is in C++ (it needs torch loaded), bound at the first
-# call: the small calls of a decode step take as long on the host as on the GPU.
+# torch, its current-stream lookup and the part of the binding that is in C++ (it needs torch loaded; the calls that
+# are marshalled here do without it), bound at the first call: the small calls of a decode step take as long on
+# the host as on the GPU.
 _torch = _stream_of = _device_of = _cpp = None
 
 
 def _bind_torch():
-    global _torch, _stream_of, _device_of, _cpp
+    global _torch, _stream_of, _device_of
     import torch
-    from . import _binding
-    _stream_of, _device_of, _cpp = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, _binding
+    _stream_of, _device_of = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
     _torch = torch
     return torch
+
+
+def _bind_cpp():
+    global _cpp
+    if _torch is None:
+        _bind_torch()
+    if not os.path.exists(os.path.join(_HERE, "_binding.so")):
+        raise ImportError(_NOT_BUILT % "_binding.so")
+    from . import _binding
+    _cpp = _binding
 
 
 def _raw_stream(stream):
@@ -490,7 +500,7 @@ def rdg_add_norm(x, weight, eps, out=None, residual=None, residual_out=None, q=N
     """x, out [T, H], residual, residual_out [T, H] of one type (row strides free), weight [H] float32 or None,
     q [T, H] uint8 and q_scales [T, H/128] float32."""
     if _cpp is None:
-        _bind_torch()
+        _bind_cpp()
     r = _cpp.add_norm(x, weight, eps, out, residual, residual_out, q, q_scales, q_dtype, _device_of(),
                       _stream_of if stream is None else stream.cuda_stream)
     if r is not None:
@@ -511,7 +521,7 @@ def rdg_linear(x, x_scales, dtype, W, W_scales, out, bias=None, act=RDG_ACT_NONE
     with W_scales [ceil(N/128), K/128], out, residual [T, N] bfloat16 or float32 (row strides free), bias [N] float32;
     work: a uint8 tensor of rdg_linear_workspace_bytes, or rdg_linear_workspace_bound of the most tokens."""
     if _cpp is None:
-        _bind_torch()
+        _bind_cpp()
     r = _cpp.linear(x, x_scales, dtype, W, W_scales, out, bias, act, residual, work, _device_of(),
                     _stream_of if stream is None else stream.cuda_stream)
     if r is not None:
@@ -523,7 +533,7 @@ def rdg_route_topk(logits, score, n_group, topk_group, group_best, K, renorm, sc
     """logits [B, N] bfloat16 or float32 (row stride free), topk_ids [B, K] int32, topk_w [B, K] float32, bias [N] float32
     or None."""
     if _cpp is None:
-        _bind_torch()
+        _bind_cpp()
     r = _cpp.route_topk(logits, score, n_group, topk_group, group_best, K, 1 if renorm else 0, scale, topk_ids, topk_w,
                         bias, _device_of(), _stream_of if stream is None else stream.cuda_stream)
     if r is not None:

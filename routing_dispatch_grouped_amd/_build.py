@@ -60,7 +60,9 @@ def _compile_binding():
 
 
 def _torch():
-    return importlib.util.find_spec("torch").submodule_search_locations[0]
+    """torch's folder, None where there is no torch (the library needs none)."""
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec else None
 
 
 def _link_binding(obj):
@@ -77,18 +79,20 @@ def _link_binding(obj):
 def build(verbose=False):
     os.makedirs(BUILD, exist_ok=True)
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = ex.submit(_compile_binding) if _torch() else None
         objs = list(ex.map(_compile, SOURCES))
-        binding = binding.result()
     tmp = OUT + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s" % r.stderr)
     os.replace(tmp, OUT)
-    _link_binding(binding)
     if verbose:
         print("built", OUT)
+    if binding is not None:
+        _link_binding(binding.result())
+    elif verbose:
+        print("no torch here, so no", BINDING)
     return OUT
 
 
