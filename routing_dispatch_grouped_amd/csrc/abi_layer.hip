@@ -73,6 +73,13 @@ size_t rdg_linear_workspace_bytes(int T, int N, int K, int dtype) {
     return linear_sizes_ok(T, N, K, dtype) && T > 0 ? linear_work_bytes(linear_plan(T, N, K, dtype), T) : 0;
 }
 
+// For the tests, not in rdg.h: kernel, splits and features of a call's two parts.
+void rdg_linear_plan_of(int T, int N, int K, int dtype, int* parts) {
+    const LinearPlan p = linear_plan(T, N, K, dtype);
+    const LinearPart* of[2] = {&p.first, &p.rest};
+    for (int i = 0; i < 2; ++i) parts[3 * i] = of[i]->kernel, parts[3 * i + 1] = of[i]->splits, parts[3 * i + 2] = of[i]->features;
+}
+
 size_t rdg_linear_workspace_bound(int T, int N, int K, int dtype) {
     return linear_sizes_ok(T, N, K, dtype) ? linear_work_bound(T, N, K, dtype) : 0;
 }

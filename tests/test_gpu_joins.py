@@ -230,7 +230,7 @@ def test_linear_of_whole_numbers_is_exact(T, N, K, kind):
     assert np.array_equal(f64(out), c["xv"] @ c["wv"].T)
 
 
-# every tile, with and without splits, whole rounds of 256 x 256 tiles with others behind them, an odd number of stages
+# larger tiles, splits, whole rounds of 256 x 256 tiles with others behind them, an odd number of stages (every plan: test_gpu_joins_edges)
 LARGE = [(2300, 9232, 640), (4000, 5136, 256), (2048, 9216, 384), (700, 4112, 2048), (1100, 2064, 4096), (129, 7184, 3968),
          (64, 7184, 7168), (1000, 272, 16384), (300, 4112, 512), (500, 12304, 1152), (4097, 4112, 128), (100, 18432, 2048),
          (260, 784, 7168), (900, 1040, 14336)]

@@ -152,3 +152,60 @@ def test_one_workspace_for_all_batches(kind):
         out = torch.full((T, N), float("nan"), device=DEV)
         m.rdg_linear(x[:T], None if xs is None else xs[:T], code, p, ws, out, work=work)
         assert torch.equal(out.double(), want[:T]), T
+
+
+# ---------------------------------------------------------------- every plan
+# Sizes that, with those of test_gpu_joins, take every tile with every number of splits that a plan gives it, for all
+# features or for those behind whole rounds of 256 x 256, with weights past the caches and not (which is tested on the host).
+PLANS = dict(
+    bf16=[(18, 4128, 128), (1040, 16, 2048), (31, 432, 3072), (521, 16, 5248), (1025, 16, 2688), (2058, 16, 2560), (18, 2064, 2304),
+          (33, 1056, 2688), (35, 24656, 128), (33, 1120, 3200), (6190, 208, 128), (36, 2080, 2304), (38, 2080, 2688),
+          (535, 80, 5248), (1038, 80, 2816), (16, 5136, 3328), (4104, 16, 4608), (33, 1296, 7424), (34, 4128, 2560),
+          (38, 2608, 4736), (1041, 96, 4736), (528, 96, 9344), (33, 5216, 3328), (66, 800, 15872), (3527, 64, 3840),
+          (2089, 96, 4352), (35, 8336, 3840), (1035, 112, 9856), (33, 3248, 11904), (38, 6192, 6016), (2095, 112, 6272),
+          (4492, 80, 4096), (1034, 112, 13952), (2105, 112, 6912), (7426, 2192, 128), (4347, 96, 5120), (5167, 3344, 128),
+          (4137, 112, 6016), (33, 12448, 10240), (7178, 3088, 256), (129, 21904, 2048), (6520, 2400, 384), (5457, 208, 6144),
+          (134, 5472, 10240), (129, 11152, 6016), (1561, 528, 11264), (1060, 13072, 2048), (702, 21808, 1920), (2250, 7184, 2816),
+          (1027, 13072, 3584), (1660, 9296, 3840), (1408, 10912, 4352), (4624, 3408, 4352), (585, 21840, 5760), (2310, 6496, 5120),
+          (5697, 2832, 4864), (7303, 2656, 4224), (4728, 3424, 6144), (2549, 6528, 6656), (1575, 9312, 7680), (598, 21776, 8832),
+          (4240, 3952, 6912), (3480, 5008, 7168), (567, 21856, 11008), (524, 23488, 12032), (1047, 13376, 11264),
+          (550, 22096, 14976), (8192, 7168, 8192), (1302, 3616, 6912)],
+    fp8=[(16, 16, 4480), (17, 4112, 128), (17, 2064, 2560), (18, 1040, 5504), (33, 2080, 3712), (34, 1088, 6912), (25, 4144, 3840),
+         (526, 80, 9600), (1030, 80, 5376), (33, 3264, 4480), (35, 1568, 8960), (35, 912, 16256), (40, 1168, 12544),
+         (33, 4400, 4992), (98, 528, 14464), (6231, 16, 7680), (69, 5536, 2048), (38, 4208, 4992), (6381, 16, 7936),
+         (2058, 80, 5120), (57, 2144, 7296), (61, 16800, 1024), (36, 8240, 3584), (1053, 80, 14464), (39, 5520, 5760),
+         (42, 2592, 11392), (4105, 80, 4352), (71, 1472, 13696), (66, 12224, 1792), (71, 1376, 15488), (45, 20640, 1664),
+         (106, 976, 14976), (73, 3072, 6912), (71, 5536, 4352), (156, 1312, 8704), (4181, 96, 4864), (34, 12336, 5504),
+         (4179, 144, 13696), (5600, 144, 11648), (5913, 3872, 512), (5676, 272, 10624), (6851, 528, 4608), (3104, 5232, 1920),
+         (1565, 9248, 2560), (2761, 5904, 2944), (559, 22192, 4736), (771, 16544, 6144), (7172, 2128, 5376), (4146, 3936, 5248),
+         (4237, 3920, 5504), (6804, 2880, 4864), (1640, 9376, 6272), (1409, 10896, 7680), (5984, 2736, 9728), (4313, 4240, 11264),
+         (2354, 6480, 14080), (624, 21872, 16384), (4358, 3744, 14976), (1501, 21840, 14464), (4001, 18432, 7168)],
+    f32=[(10, 16, 1024), (17, 4128, 128), (17, 2080, 512), (13, 4144, 768), (33, 24640, 128), (6164, 208, 128), (37, 1040, 5248),
+         (525, 80, 5248), (33, 3120, 2688), (1549, 80, 3712), (3083, 80, 1920), (3096, 80, 3712), (1551, 80, 7552),
+         (6750, 80, 2560), (35, 12448, 3328), (6151, 80, 3328), (6315, 208, 2560)],
+)
+
+
+@pytest.mark.parametrize("kind,T,N,K", [(kind, *size) for kind in ("bf16", "fp8", "e8m0", "f32")
+                                        for size in PLANS[kind if kind != "e8m0" else "fp8"]])
+def test_every_plan_of_whole_numbers_is_exact(kind, T, N, K):
+    """Sums of at most K products of at most 9, in steps of 1/4 times at most 4: below 2^24 of the steps, so exact in fp32."""
+    m = rdg()
+    g = torch.Generator(device=DEV).manual_seed(T + 3 * N + 7 * K)
+    code, fp8 = code_of(kind), kind in ("fp8", "e8m0")
+    nat = {"bf16": BF, "f32": F32}.get(kind, F8)
+    x, w = (torch.randint(-3, 4, (n, K), device=DEV, generator=g).to(F32) for n in (T, N))
+    scale = lambda n: torch.exp2(torch.randint(-1, 2, (n, K // 128), device=DEV, generator=g).float()) if fp8 else None  # noqa: E731
+    xs, ws = scale(T), scale(-(-N // 128))
+    a, b = x.double(), w.double()
+    if fp8:
+        a, b = a * xs.repeat_interleave(128, 1), b * ws.repeat_interleave(128, 1).repeat_interleave(128, 0)[:N]
+    want = a @ b.T
+    held = torch.empty(T, K + 16, dtype=nat, device=DEV)
+    x, w = held[:, :K].copy_(x), packed(w.to(nat), code)
+    bias = torch.randint(-50, 51, (N,), device=DEV, generator=g).float()
+    for out_type in (F32,) if kind == "f32" else (F32, BF):
+        out = torch.full((T, N + 8), 7.0, dtype=out_type, device=DEV)
+        res = torch.randint(-9, 10, (T, N + 16), device=DEV, generator=g).to(out_type)[:, :N]
+        m.rdg_linear(x, xs, code, w, ws, out[:, :N], bias=bias, act=m.RDG_ACT_RELU, residual=res, work=work_for(T, N, K, code))
+        assert torch.equal(out[:, :N], ((want + bias).clamp(min=0) + res).float().to(out_type)) and (out[:, N:] == 7).all()

@@ -1,5 +1,7 @@
-"""The plans of rdg_linear on the host: what workspaces they ask for."""
+"""The plans of rdg_linear on the host: what workspaces they ask for, and that the GPU tests take each."""
+import ctypes
 import itertools
+import random
 
 import pytest
 
@@ -53,3 +55,29 @@ def test_small_products_over_long_reductions_have_splits(dtype):
         for work, size in ((a, need - 1), (None, need), (a + 8, need), (a, 0)):
             assert rdg._lib.rdg_linear(a, a, dtype, K, T, N, K, a, a, None, 0, None, 0, 2 * a, rdg.RDG_F32, N, work, size, None) == \
                 rdg.RDG_EINVAL
+
+
+KERNELS = ["rows", "256 x 256", "128 x 128", "128 x 64", "64 x 32", "96 x 64", "80 x 64", "64 x 64"]   # features x tokens
+TILE_TOKENS = [16, 256, 128, 64, 32, 64, 64, 64]
+
+
+def _forms(T, N, K, dtype):
+    """The forms of the kernels that a call takes: which part, kernel, splits, and whether its weights pass the caches (one tile of tokens
+    of at most 64)."""
+    parts = (ctypes.c_int * 6)()
+    _rdg()._lib.rdg_linear_plan_of(T, N, K, dtype, parts)
+    return {(i, KERNELS[k], splits, k >= 3 and T <= TILE_TOKENS[k])
+            for i, (k, splits, features) in enumerate((parts[:3], parts[3:])) if features}
+
+
+@pytest.mark.parametrize("kind,dtype", [("f32", 0), ("bf16", 1), ("fp8", 2), ("fp8", 3)])
+def test_the_gpu_tests_take_every_form_that_a_plan_gives(kind, dtype):
+    from test_gpu_joins import LARGE, SHAPES
+    from test_gpu_joins_edges import PLANS
+    tested = set().union(*(_forms(*size, dtype) for size in SHAPES + LARGE + PLANS[kind]))
+    assert {"rows", "128 x 128", "128 x 64", "64 x 32"} <= {f[1] for f in tested}
+    rng = random.Random(3)
+    for _ in range(40000):
+        T, N, K = int(2 ** rng.uniform(0, 13)), 16 * int(2 ** rng.uniform(0, 11)), 128 * int(2 ** rng.uniform(0, 7.1))
+        if T * N * K < 1.5e12:
+            assert _forms(T, N, K, dtype) <= tested, (T, N, K)
