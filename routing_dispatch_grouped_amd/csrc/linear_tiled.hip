@@ -522,16 +522,15 @@ hipError_t launch(const LinearCall& a, int splits, hipStream_t s) {
 
 template <int KIND>
 static hipError_t launch_kind(const LinearCall& a, const LinearPart& p, hipStream_t s) {
+    // (fp32 has no plans of these: 256 x 256 would keep two sets of sums)
     if constexpr (KIND != kF32) {
+        // (products of widened operands need registers for them, so half the tokens)
+        if (p.kernel == kTile256) return launch<KIND, 2, 4, 8, KIND == kFp8Wide ? 2 : 4, 2>(a, p.splits, s);
         if (p.kernel == kTile96x64) return launch<KIND, 6, 1, 1, 4, 5>(a, p.splits, s);
         if (p.kernel == kTile80x64) return launch<KIND, 5, 1, 1, 4, 5>(a, p.splits, s);
         if (p.kernel == kTile64x64) return launch<KIND, 4, 1, 1, 4, 5>(a, p.splits, s);
     }
     switch (p.kernel) {
-        case kTile256:
-            // fp32 keeps two sets of sums, and products of widened operands need registers for them
-            if constexpr (KIND == kF32) return launch<KIND, 2, 4, 4, 2, 4>(a, p.splits, s);
-            else return launch<KIND, 2, 4, 8, KIND == kFp8Wide ? 2 : 4, 2>(a, p.splits, s);
         case kTile128: return launch<KIND, 2, 4, 4, 2, 4>(a, p.splits, s);
         case kTile128x64: return launch<KIND, 4, 2, 2, 2, 5>(a, p.splits, s);
         default: return launch<KIND, 4, 1, 1, 2, 4>(a, p.splits, s);
