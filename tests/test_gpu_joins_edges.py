@@ -209,3 +209,93 @@ def test_every_plan_of_whole_numbers_is_exact(kind, T, N, K):
         res = torch.randint(-9, 10, (T, N + 16), device=DEV, generator=g).to(out_type)[:, :N]
         m.rdg_linear(x, xs, code, w, ws, out[:, :N], bias=bias, act=m.RDG_ACT_RELU, residual=res, work=work_for(T, N, K, code))
         assert torch.equal(out[:, :N], ((want + bias).clamp(min=0) + res).float().to(out_type)) and (out[:, N:] == 7).all()
+
+
+# ---------------------------------------------------------------- what stays apart
+@pytest.mark.parametrize("out_type", [BF, F32])
+@pytest.mark.parametrize("kind", ["fp8", "e8m0"])
+@pytest.mark.parametrize("T,N,K", [(4, 48, 256), (40, 272, 1024), (64, 256, 7168), (300, 4112, 512)])
+def test_broken_codes_and_scales_reach_their_own_row_and_column_only(T, N, K, kind, out_type):
+    m = rdg()
+    g = torch.Generator(device=DEV).manual_seed(T)
+    code = code_of(kind)
+    x, w = (torch.randn(n, K, device=DEV, generator=g).to(F8) for n in (T, N))
+    xs, ws = torch.ones(T, K // 128, device=DEV), torch.ones(-(-N // 128), K // 128, device=DEV)
+    run = lambda: m.rdg_linear(x, xs, code, packed(w, code), ws, out, work=work_for(T, N, K, code))  # noqa: E731
+    out = torch.empty(T, N, dtype=out_type, device=DEV)
+    run()
+    want = out.clone()
+    x[1, K - 1] = w[N - 2, 5] = x[T - 1, 0] = float("nan")
+    xs[2, K // 128 - 1] = float("inf") if kind == "fp8" else 2.0 ** 127
+    run()
+    rows, cols = [1, T - 1], [N - 2]
+    assert out[rows].isnan().all() and out[:, cols].isnan().all()
+    keep = torch.ones(T, N, dtype=torch.bool, device=DEV)
+    keep[rows + [2]] = False
+    keep[:, cols] = False
+    assert torch.equal(out[keep], want[keep])
+    assert (out[2, :N - 2].abs() > 1e30).all()       # an infinite or huge sum
+
+
+def test_norm_onto_the_residual_and_onto_short_rows():
+    """Outputs in an input's place where rows share a workgroup, and behind the last row another one's lanes read the last again."""
+    m = rdg()
+    for T, H in ((1, 128), (3, 128), (37, 128), (33, 256), (7, 512), (9, 1024), (5, 4096)):
+        g = torch.Generator(device=DEV).manual_seed(T + H)
+        x, r = (torch.randn(T, H, device=DEV, generator=g).to(BF) for _ in range(2))
+        want, sums = torch.empty_like(x), torch.empty_like(x)
+        m.rdg_add_norm(x, None, 1e-6, out=want, residual=r, residual_out=sums)
+        r1, x1, x2, r2 = r.clone(), x.clone(), x.clone(), r.clone()
+        m.rdg_add_norm(x, None, 1e-6, out=r1, residual=r1)
+        m.rdg_add_norm(x1, None, 1e-6, out=x1, residual=r)
+        m.rdg_add_norm(x2, None, 1e-6, out=r2, residual=r2, residual_out=x2)
+        for got, exp in ((r1, want), (x1, want), (r2, want), (x2, sums)):
+            assert torch.equal(got, exp), (T, H)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "fp8", "e8m0"])
+def test_split_products_captured_and_on_a_stream_of_their_own(kind):
+    """Replayed with new operands and other work between, and given a stream that is not the current one."""
+    m = rdg()
+    T, N, K, code = 64, 256, 7168, code_of(kind)
+    nat = {"bf16": BF, "f32": F32}.get(kind, F8)
+    g = torch.Generator(device=DEV).manual_seed(9)
+    x, w = (torch.randn(n, K, device=DEV, generator=g).to(nat) for n in (T, N))
+    fp8 = nat is F8
+    xs, ws = (torch.ones(n, K // 128, device=DEV) if fp8 else None for n in (T, N // 128))
+    p, out, work = packed(w, code), torch.empty(T, N, device=DEV), work_for(T, N, K, code)
+    assert work is not None
+    call = lambda to, space, **how: m.rdg_linear(x, xs, code, p, ws, to, act=m.RDG_ACT_SILU, work=space, **how)  # noqa: E731
+    call(out, work)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out, work)
+    eager, other = torch.empty_like(out), torch.empty_like(work)
+    for i in range(4):
+        x.copy_(torch.randn(T, K, device=DEV, generator=g).to(nat))
+        work.fill_(0xff)
+        graph.replay()
+        call(eager, other)
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager) and eager.isfinite().all()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    apart = torch.full_like(out, float("nan"))
+    torch.cuda.synchronize()
+    call(apart, other, stream=side)
+    side.synchronize()
+    assert torch.equal(apart, eager)
+
+
+def test_products_below_the_normal_range():
+    """Subnormal operands and sums are kept."""
+    m = rdg()
+    for dtype, code in ((BF, m.RDG_BF16), (F32, m.RDG_F32)):
+        for T in (2, 70):
+            for a, b in ((-130, 20), (20, -130), (-100, -40), (-133, 0), (-63, -64)):
+                x, w = torch.zeros(T, 128, dtype=dtype, device=DEV), torch.zeros(16, 128, dtype=dtype, device=DEV)
+                x[:, 3], w[:, 3] = 2.0 ** a, 2.0 ** b
+                out = torch.empty(T, 16, device=DEV)
+                m.rdg_linear(x, None, code, packed(w, code), None, out)
+                assert (out == 2.0 ** (a + b)).all()
