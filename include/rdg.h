@@ -592,7 +592,8 @@ int rdg_add_norm(const void* x, int x_dtype, int64_t x_stride, int T, int H, con
 /* Matrix product with its epilogue:
  *   out[t] = act(x[t] W^T + bias) + residual[t]
  *   x         [T, x_stride] rows of K elements: RDG_F32, RDG_BF16, RDG_FP8_E4M3 or
- *             RDG_FP8_E4M3_UE8M0 (dtype), with x_scales [T, K/128] fp32 for the last two
+ *             RDG_FP8_E4M3_UE8M0 (dtype), with x_scales [T, K/128] fp32 for the last two.  Rows 8 MiB or more
+ *             apart take the kernel for few tokens, at any T
  *   W         [N, K] in dtype, packed by rdg_pack_weights (n_mat = 1), with W_scales
  *             [ceil(N/128), K/128] for fp8, as rdg_quantize_fp8 with block_rows 128 gives them
  *   bias      [N] fp32 or NULL

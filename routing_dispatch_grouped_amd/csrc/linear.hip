@@ -16,9 +16,10 @@ namespace {
 
 // A workgroup has 16 weight rows and 16 tokens; its waves take the reduction's 128-element blocks
 // in turn (wave w blocks w, w + NW, ...), so that the weights stream through in order, and add their sums in LDS in wave
-// order.  16 waves: one token, 7168 x 10240 in bf16 24.6 us (6.0 TB/s), with 4 or 8 waves 25.4, with two weight tiles a
-// wave 28; 16 tokens on 256 features of K = 4096: 7.9 us against 10.9.  Loading the next block during the
-// products, 24.1 us at 16 waves for twice the registers, gained nothing elsewhere.
+// order.  One token, 10240 features of K = 7168 in bf16: 25.0 to 26.6 us with the weights from memory (5.5 to 5.9 TB/s), 23.1 to
+// 25.6 with the same 147 MB over again, some of which the last cache holds.  Over again: 24.6 with 16 waves, 25.4 with 4 or 8, 28
+// with two weight tiles a wave; 16 tokens on 256 features of K = 4096: 7.9 us against 10.9.  Loading the next block
+// during the products, 24.1 us at 16 waves for twice the registers, gained nothing elsewhere.
 // A token tile's loads touch 16 rows, so their time grows with the tokens: rows_us below.
 // e4m3 products are taken from bf16 operands (LinOp::mma_wide): one token on 18432 features of K = 7168 takes 21.7 us either
 // way, eight tokens 24.7 and 24.6.
@@ -92,8 +93,11 @@ hipError_t launch_rows(const LinearCall& a, hipStream_t s) {
 
 // ---------------------------------------------------------------- which kernel
 // The expected time of each kernel and split in us, and the least of them.  Constants measured over 461 sizes each of
-// bf16 and of fp8 (1 .. 5000 tokens, 64 .. 32768 features, K of 256 .. 14336, weights from memory); the choice takes on
-// average 1% longer than the best of all at each size, 1.23 times at worst (64 tokens, 2048 features, K = 7168, bf16: 13.5 us).
+// bf16 and of fp8 (1 .. 5000 tokens, 64 .. 32768 features, K of 256 .. 14336, weights from memory), before the join asked for all
+// splits at once and 16 splits came; the choice took on average 1% longer than the best of all at each size, 1.23 times at
+// worst (64 tokens, 2048 features, K = 7168, bf16: 13.5 us).  With both, at 25 sizes of up to 32 tokens and all three types: 8%
+// at worst (16 tokens, 7168 features, K = 2048, bf16: 9.7 us, k_linear_rows 9.0), 2% or less at the others.
+// e4m3 to fp32 is planned with the costs of e4m3 to bf16, whose products take half the time.
 constexpr int kCus = 256;
 constexpr float kStart = 2.0f, kMore = 1.5f;            // launch, first loads, last stores; one launch more
 constexpr float kRowsRead = 6.7e6f, kTilesRead = 7.5e6f;  // bytes/us at which weights come from memory
@@ -181,9 +185,12 @@ LinearPart plan_part(int T, int N, int K, int dtype, float& least) {
     int kinds;
     const TileCost* cost = costs(dtype, kinds);
     LinearPart best{kRows, 1, N};
-    // (Beyond 32 tokens the tiles are always faster.)  At near equal times the rows, one launch that needs no workspace and
-    // takes less where some of the weights are still in the last cache: one token, 10240 features, K = 7168 in bf16,
-    // weights from memory 28.0 us, with two splits of 80 features 27.4; 147 MB over again 24.4, and 27.2.
+    // (Beyond 32 tokens the tiles are always faster.)  At near equal times the rows, one launch that needs no workspace.
+    // us from memory, and over again, for the rows and for the best of the tiles:
+    //   bf16  1 x 10240 x 7168  25.3, 24.8  27.4, 26.1     4 x 10240 x 7168  27.5, 26.1  27.4, 26.1
+    //         1 x  7168 x 8192  21.4, 20.0  22.0, 20.8     2 x  1536 x 7168   8.3,  7.4   8.6,  8.3
+    //   e8m0  8 x 18432 x 7168  24.2, 23.5  25.6, 24.9     1 x  7168 x 18432 22.9, 20.8  24.9, 23.5
+    //   fp32  1 x  7168 x 2048  16.0, 14.1  16.5, 15.4
     least = T <= 32 ? 0.97f * rows_us(T, N, K, dtype) : 3e38f;
     for (int i = 0; i < kinds; ++i) {
         const int64_t tiles = ceil_div(N, cost[i].features) * ceil_div(T, cost[i].tokens);

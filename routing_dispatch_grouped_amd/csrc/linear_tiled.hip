@@ -14,9 +14,9 @@
 // all and the oldest place is free.  The loop's body is there twice, without and, for the last NB stages, with tests for
 // the end.
 //
-// Large tiles are bound by the matrix core (256 x 256: bf16 8192 x 7168 x 8192 677 .. 686 us, 1.4 PFLOP/s, its units 72%
-// busy at 1.8 GHz; e8m0 4001 x 18432 x 7168 415 us, 2.55 PFLOP/s; fp32 scales 467: the sums' multiplications are nearly
-// as many cycles as the products), small ones by the lines that a compute unit has under way or by L2 (4096 tokens on 256
+// Large tiles are bound by the matrix core (256 x 256: bf16 8192 x 7168 x 8192 677 .. 711 us from card to card, 1.4 PFLOP/s, its
+// units 72% busy at 1.8 GHz; e8m0 4001 x 18432 x 7168 415 .. 437 us, 2.5 PFLOP/s; fp32 scales 467 .. 493: the sums'
+// multiplications are nearly as many cycles as the products), small ones by the lines that a compute unit has under way or by L2 (4096 tokens on 256
 // features of K = 7168: 24.4 us, 3.7 million lines from L2, 23 TB/s), with few tokens by memory (linear.hip).
 // Tiles lie in bands of four by features on each XCD: 8192 x 7168 x 8192 686 us, with bands of one 792, of two 708, of
 // eight 695, of all features 743; 4096 x 18432 x 7168 800, 807, 807, 833 and 921.
@@ -503,8 +503,11 @@ hipError_t launch(const LinearCall& a, int splits, hipStream_t s) {
     const int64_t f_tiles = (a.N + TF - 1) / TF, t_tiles = ((int64_t)a.T + TT - 1) / TT, all = f_tiles * t_tiles * splits;
     const int64_t join = ((int64_t)a.T * (a.N / 8) + 255) / 256;
     if (!grid_fits(all, WF * WT * 64) || !grid_fits(join, 256)) return hipErrorInvalidConfiguration;
-    // weights that no other workgroup reads pass the caches: 64 tokens, 18432 features, K = 7168 in e8m0 32.3 -> 29.8 us, in
-    // bf16 63.6 -> 61.3 (with a second tile of tokens it would cost: 256 tokens of 7168 x 7168 51.5 -> 55.7)
+    // weights that no other workgroup reads pass the caches.  us from memory, and with the same weights over again, past the
+    // caches and through them: 64 tokens, 18432 features, K = 7168 in e8m0 28.8, 27.1 and 29.7, 26.8, in bf16 50.8, 49.5 and
+    // 53.7, 44.5; 24576 features 59.5, 58.5 and 65.7, 65.0.  A layer's weights come from memory, as the other layers' have passed
+    // since; weights that the last cache keeps (256 MiB) pay up to a fifth (7168 features 26.2 and 20.9).  With a second
+    // tile of tokens it would cost: 256 tokens of 7168 x 7168 51.5 -> 55.7.
     if (NF <= 2 && t_tiles == 1)
         k_linear_tiled<KIND, WF, WT, NF, NTK, NB, (NF <= 2)><<<(unsigned)all, WF * WT * 64, 0, s>>>(a, (int)f_tiles, 1, splits);
     else
