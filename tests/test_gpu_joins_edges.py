@@ -158,7 +158,7 @@ def test_one_workspace_for_all_batches(kind):
 # Sizes that, with those of test_gpu_joins, take every tile with every number of splits that a plan gives it, for all
 # features or for those behind whole rounds of 256 x 256, with weights past the caches and not (which is tested on the host).
 PLANS = dict(
-    bf16=[(18, 4128, 128), (1040, 16, 2048), (31, 432, 3072), (521, 16, 5248), (1025, 16, 2688), (2058, 16, 2560), (18, 2064, 2304),
+    bf16=[(18, 4128, 128), (1040, 16, 2048), (11, 1040, 4096), (521, 16, 5248), (1025, 16, 2688), (2058, 16, 2560), (18, 2064, 2304),
           (33, 1056, 2688), (35, 24656, 128), (33, 1120, 3200), (6190, 208, 128), (36, 2080, 2304), (38, 2080, 2688),
           (535, 80, 5248), (1038, 80, 2816), (16, 5136, 3328), (4104, 16, 4608), (33, 1296, 7424), (34, 4128, 2560),
           (38, 2608, 4736), (1041, 96, 4736), (528, 96, 9344), (33, 5216, 3328), (66, 800, 15872), (3527, 64, 3840),
@@ -175,7 +175,7 @@ PLANS = dict(
          (33, 4400, 4992), (98, 528, 14464), (6231, 16, 7680), (69, 5536, 2048), (38, 4208, 4992), (6381, 16, 7936),
          (2058, 80, 5120), (57, 2144, 7296), (61, 16800, 1024), (36, 8240, 3584), (1053, 80, 14464), (39, 5520, 5760),
          (42, 2592, 11392), (4105, 80, 4352), (71, 1472, 13696), (66, 12224, 1792), (71, 1376, 15488), (45, 20640, 1664),
-         (106, 976, 14976), (73, 3072, 6912), (71, 5536, 4352), (156, 1312, 8704), (4181, 96, 4864), (34, 12336, 5504),
+         (106, 976, 14976), (65, 2960, 6784), (71, 5536, 4352), (156, 1312, 8704), (4181, 96, 4864), (34, 12336, 5504),
          (4179, 144, 13696), (5600, 144, 11648), (5913, 3872, 512), (5676, 272, 10624), (6851, 528, 4608), (3104, 5232, 1920),
          (1565, 9248, 2560), (2761, 5904, 2944), (559, 22192, 4736), (771, 16544, 6144), (7172, 2128, 5376), (4146, 3936, 5248),
          (4237, 3920, 5504), (6804, 2880, 4864), (1640, 9376, 6272), (1409, 10896, 7680), (5984, 2736, 9728), (4313, 4240, 11264),
