@@ -95,8 +95,9 @@ hipError_t launch_rows(const LinearCall& a, hipStream_t s) {
 // The expected time of each kernel and split in us, and the least of them.  Constants measured over 461 sizes each of
 // bf16 and of fp8 (1 .. 5000 tokens, 64 .. 32768 features, K of 256 .. 14336, weights from memory), before the join asked for all
 // splits at once and 16 splits came; the choice took on average 1% longer than the best of all at each size, 1.23 times at
-// worst (64 tokens, 2048 features, K = 7168, bf16: 13.5 us).  With both, at 25 sizes of up to 32 tokens and all three types: 8%
-// at worst (16 tokens, 7168 features, K = 2048, bf16: 9.7 us, k_linear_rows 9.0), 2% or less at the others.
+// worst (64 tokens, 2048 features, K = 7168, bf16: 13.5 us).  With both, at 25 sizes of up to 32 tokens and 48 of up to 1250,
+// all three types: 8% longer at worst (16 tokens, 7168 features, K = 2048, bf16: 9.7 us, k_linear_rows 9.0; 182 tokens, 192
+// features, K = 11648: 10.0, 64 x 32 with 8 splits 9.3), 2% or less at all but four.
 // e4m3 to fp32 is planned with the costs of e4m3 to bf16, whose products take half the time.
 constexpr int kCus = 256;
 constexpr float kStart = 2.0f, kMore = 1.5f;            // launch, first loads, last stores; one launch more
